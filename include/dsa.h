@@ -58,12 +58,15 @@ typedef enum { DSA_BF16 = 0, DSA_F32 = 1 } dsa_dtype;
 #define DSA_DEVERR_TIMEOUT 0x01   /* a bounded mbarrier wait ran out */
 #define DSA_DEVERR_BAD_INDEX 0x02 /* an index outside [-1, S) was skipped */
 #define DSA_DEVERR_MISALIGNED 0x03 /* shared memory not aligned as the kernel needs */
+#define DSA_DEVERR_BAD_PAGE 0x04   /* a page or a length outside the cache was skipped */
 #define DSA_STAGE_INDEXER 0x100
 #define DSA_STAGE_TOPK 0x200
 #define DSA_STAGE_FWD 0x300
 #define DSA_STAGE_BWD 0x400
 #define DSA_STAGE_LOSS 0x500
 #define DSA_STAGE_LOSS_BWD 0x600
+#define DSA_STAGE_CACHE 0x700
+#define DSA_STAGE_LATENT 0x800
 
 /* Human-readable name of a status. Never NULL. */
 const char* dsa_status_string(int status);
@@ -464,6 +467,114 @@ int dsa_indexer_loss(const void* Q, const void* K, const int32_t* idx, const flo
 int dsa_indexer_loss_bwd(const void* q_idx, const void* k_idx, const float* w,
                          const int32_t* idx, const float* dI, int B, int S, int Hi, int Di,
                          int k, float* dq_idx, float* dk_idx, float* dw, void* stream);
+
+/*
+ * ---------------------------------------------------------------- serving
+ *
+ * The layer of a model that answers token by token: rotary positions, a paged cache of
+ * latent rows, and the attention of the newest tokens over it (the absorbed form of
+ * multi-head latent attention, whose keys and values are one shared vector per token, so
+ * that the selection of the indexer gathers one row per key: "DeepSeek3.2: Onboard sparse
+ * attention", Background).
+ */
+
+/*
+ * dsa_rope - rotary positions on dims [off, off + rot) of each head; the other dims are
+ * copied. With i = 0 .. rot/2 - 1, t = pos[n] * inv_freq[i] and (a, b) the dims
+ * (off + 2i, off + 2i + 1) in DSA_ROPE_INTERLEAVED or (off + i, off + rot/2 + i) in
+ * DSA_ROPE_HALF:
+ *
+ *     y_a = mscale (x_a cos t - x_b sin t),   y_b = mscale (x_a sin t + x_b cos t)
+ *
+ * inverse != 0 takes -t. The map is linear in x and its transpose is the map at -t, so the
+ * gradient of x is dsa_rope(dy) with inverse toggled and the same mscale.
+ *
+ *   x, y      [T, H, D], bf16 (dtype = DSA_BF16) or fp32 (DSA_F32); y = x rotates in place,
+ *             any other overlap is refused (DSA_ERR_INVALID_ARG)
+ *   pos       int32 [T], any value (the angle is reduced exactly: far positions lose nothing)
+ *   inv_freq  fp32 [rot / 2], finite, radians per position
+ *
+ * Supported: D <= 1024 and off multiples of 8, rot a multiple of 16 with off + rot <= D. The
+ * arithmetic is fp32, rounded once.
+ */
+#define DSA_ROPE_INTERLEAVED 0
+#define DSA_ROPE_HALF 1
+int dsa_rope(const void* x, void* y, int dtype, const int32_t* pos, const float* inv_freq, int T,
+             int H, int D, int off, int rot, int layout, float mscale, int inverse, void* stream);
+
+/*
+ * The paged latent cache: rows of Dc latent and Dr positional dims, page_size rows to a page,
+ * uint8 [num_pages, page_size, dsa_cache_row_bytes(fmt, Dc, Dr)]; slot s is row s % page_size
+ * of page s / page_size.
+ *
+ *   DSA_CACHE_BF16  the Dc + Dr dims in bf16
+ *   DSA_CACHE_E4M3  Dc e4m3 bytes; one fp32 scale per 128 of them (the scales padded with
+ *                   zeros to a multiple of 16 bytes); the Dr dims in bf16. A scale is the
+ *                   smallest power of two 2^k, k >= -120, with max|x| <= 448 * 2^k over its
+ *                   128 dims (1 if they are all zero), and a byte is x / 2^k rounded to nearest
+ *                   even: within half an e4m3 step (2^-4 of the value, 2^-10 * 2^k for the
+ *                   smallest ones). A power of two keeps the read back exact in bf16 (a
+ *                   magnitude above 1.9375 * 2^127 rounds up and reads back as an infinity).
+ *                   A group with an infinity or a NaN reads back as NaN.
+ *
+ * Supported: Dc a multiple of 128, 128 <= Dc <= 1024; Dr a multiple of 8, 0 <= Dr <= 256.
+ * dsa_cache_row_bytes returns 0 for anything else.
+ */
+#define DSA_CACHE_BF16 0
+#define DSA_CACHE_E4M3 1
+size_t dsa_cache_row_bytes(int fmt, int Dc, int Dr);
+
+/*
+ * dsa_cache_write - rows kv (bf16 [T, Dc + Dr]) into the slots slots[T] (int32) of the cache.
+ * Slot -1 skips its row (padding); a slot outside [-1, num_slots) is skipped and recorded as
+ * DSA_STAGE_CACHE | DSA_DEVERR_BAD_INDEX. The slots >= 0 must be distinct. Every other byte of
+ * the cache is left as it was.
+ */
+int dsa_cache_write(const void* kv, const int32_t* slots, int T, int Dc, int Dr, int fmt,
+                    void* cache, int64_t num_slots, void* stream);
+
+/*
+ * dsa_cache_read - the values of the rows at slots[N] (int32, repeats allowed) as bf16
+ * kv [N, Dc + Dr]. Slot -1 gives a row of zeros; so does one outside [-1, num_slots), which
+ * is recorded as DSA_STAGE_CACHE | DSA_DEVERR_BAD_INDEX.
+ */
+int dsa_cache_read(const void* cache, int64_t num_slots, int fmt, const int32_t* slots, int N,
+                   int Dc, int Dr, void* kv, void* stream);
+
+/*
+ * dsa_latent_attn - attention of the Sq newest tokens of each sequence over its cached rows.
+ * With len = lens[b] the cached tokens of sequence b, its Sq new ones among them (they are
+ * written first), token i stands at position len - Sq + i and sees the positions up to its
+ * own:
+ *
+ *     l_j = scale * Q[b,i,h] . row_j[0 : Dc+Dr]      0 <= j <= len - Sq + i
+ *     O[b,i,h] = sum_j softmax(l)_j row_j[0 : Dc],   lse[b,i,h] = log sum_j exp(l_j)
+ *
+ * over every such j (idx = NULL), or over the listed ones: idx[b,i,:] as dsa_topk gives them
+ * (-1 entries and entries above the token's position are ignored, entries must be distinct; an
+ * entry below -1 or >= len is skipped and recorded as DSA_STAGE_LATENT |
+ * DSA_DEVERR_BAD_INDEX). Position j of sequence b is row j % page_size of page
+ * page_table[b, j / page_size]. A token with no key (len < Sq - i, or an empty list) gets O = 0
+ * and lse = -inf; a sequence with len <= 0 is skipped that way (padding). A length below 0 or
+ * above max_pages * page_size is taken as the nearest of the two, and a page outside
+ * [0, num_pages) is skipped as if its keys were not there; both are recorded as
+ * DSA_STAGE_LATENT | DSA_DEVERR_BAD_PAGE. Rows of the cache that no token sees are not read.
+ *
+ *   Q     bf16 [B, Sq, H, Dc + Dr]        cache      as above, num_pages * page_size slots
+ *   lens  int32 [B]                       page_table int32 [B, max_pages]
+ *   idx   int32 [B, Sq, k] or NULL (k = 0)
+ *   O     bf16 [B, Sq, H, Dc] out         lse        fp32 [B, Sq, H] out
+ *   ws    workspace of dsa_latent_attn_workspace_size() bytes (overwritten): the parts of
+ *         rows whose keys are split over the GPU. Nothing is kept in it between calls.
+ *
+ * Supported: (Dc, Dr) = (512, 64), 1 <= H <= 128, scale > 0 and finite, page_size >= 1,
+ * num_pages * page_size < 2^31, max_pages * page_size < 2^31.
+ */
+size_t dsa_latent_attn_workspace_size(int B, int Sq, int H, int Dc, int Dr, int k);
+int dsa_latent_attn(const void* Q, const void* cache, int fmt, int64_t num_pages, int page_size,
+                    const int32_t* page_table, int max_pages, const int32_t* lens,
+                    const int32_t* idx, int k, int B, int Sq, int H, int Dc, int Dr, float scale,
+                    void* O, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

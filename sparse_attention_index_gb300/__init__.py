@@ -14,10 +14,14 @@ Entry points (same names as the C ABI):
 * ``dsa_sparse_attn_fwd`` - attention over the selected keys -> (O, lse)
 * ``dsa_sparse_attn_fwd_dense`` - the same from the dense-tile kernel only
 * ``dsa_sparse_attn_bwd`` - its gradients -> (dQ, dK, dV)
+* ``dsa_rope`` - rotary positions on part of each head, and their inverse (the gradient)
+* ``dsa_cache_write`` / ``dsa_cache_read`` - rows of the paged latent cache (bf16 or e4m3)
+* ``dsa_latent_attn`` - attention of the newest tokens over that cache -> (O, lse)
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -29,7 +33,9 @@ DSA_BF16, DSA_F32 = 0, 1
 # device error codes (dsa_get_last_device_error): kind | stage
 DSA_DEVERR_TIMEOUT, DSA_DEVERR_BAD_INDEX, DSA_DEVERR_MISALIGNED = 0x01, 0x02, 0x03
 DSA_STAGE_INDEXER, DSA_STAGE_TOPK, DSA_STAGE_FWD, DSA_STAGE_BWD = 0x100, 0x200, 0x300, 0x400
+DSA_DEVERR_BAD_PAGE = 0x04
 DSA_STAGE_LOSS, DSA_STAGE_LOSS_BWD = 0x500, 0x600
+DSA_STAGE_CACHE, DSA_STAGE_LATENT = 0x700, 0x800
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED = 0, 1, 2
 STATUS = {0: "DSA_OK", 1: "DSA_ERR_INVALID_ARG", 2: "DSA_ERR_UNSUPPORTED", 3: "DSA_ERR_WORKSPACE",
           4: "DSA_ERR_CUDA", 5: "DSA_ERR_TIMEOUT", 6: "DSA_ERR_DEVICE"}
@@ -44,7 +50,8 @@ EXPORTS = ("dsa_status_string", "dsa_version", "dsa_get_last_device_error", "dsa
            "dsa_sparse_attn_bwd_noalloc", "dsa_indexer_loss", "dsa_indexer_loss_bwd",
            "dsa_index_topk_workspace_size", "dsa_index_topk", "dsa_index_topk_fp8",
            "dsa_index_topk_stream_workspace_size", "dsa_index_topk_stream",
-           "dsa_index_topk_stream_fp8")
+           "dsa_index_topk_stream_fp8", "dsa_rope", "dsa_cache_row_bytes", "dsa_cache_write",
+           "dsa_cache_read", "dsa_latent_attn_workspace_size", "dsa_latent_attn")
 
 
 class DsaError(RuntimeError):
@@ -98,7 +105,17 @@ def _load() -> ctypes.CDLL:
     lib.dsa_index_topk_stream_workspace_size.restype = sz
     lib.dsa_index_topk_stream.argtypes = lib.dsa_index_topk.argtypes
     lib.dsa_index_topk_stream_fp8.argtypes = lib.dsa_index_topk_fp8.argtypes
-    for name in ("dsa_get_last_device_error", "dsa_index_scores", "dsa_index_scores_fp8", "dsa_topk",
+    lib.dsa_rope.argtypes = [vp, vp, ci, vp, vp, ci, ci, ci, ci, ci, ci, cf, ci, vp]
+    lib.dsa_cache_row_bytes.argtypes = [ci, ci, ci]
+    lib.dsa_cache_row_bytes.restype = sz
+    lib.dsa_cache_write.argtypes = [vp, vp, ci, ci, ci, ci, vp, i64, vp]
+    lib.dsa_cache_read.argtypes = [vp, i64, ci, vp, ci, ci, ci, vp, vp]
+    lib.dsa_latent_attn_workspace_size.argtypes = [ci, ci, ci, ci, ci, ci]
+    lib.dsa_latent_attn_workspace_size.restype = sz
+    lib.dsa_latent_attn.argtypes = [vp, vp, ci, i64, ci, vp, ci, vp, vp, ci, ci, ci, ci, ci, ci, cf,
+                                    vp, vp, vp, sz, vp]
+    for name in ("dsa_rope", "dsa_cache_write", "dsa_cache_read", "dsa_latent_attn",
+                 "dsa_get_last_device_error", "dsa_index_scores", "dsa_index_scores_fp8", "dsa_topk",
                  "dsa_indexer_loss", "dsa_indexer_loss_bwd", "dsa_index_topk",
                  "dsa_index_topk_fp8", "dsa_index_topk_stream", "dsa_index_topk_stream_fp8",
                  "dsa_sparse_attn_fwd", "dsa_sparse_attn_fwd_dense", "dsa_sparse_attn_bwd",
@@ -688,3 +705,211 @@ def dsa_layer(q_idx, k_idx, w, Q, K, V, topk: int, scale: float, seg=None, dO=No
         out["dQ"], out["dK"], out["dV"] = dsa_sparse_attn_bwd(Q, K, V, idx, O, lse, dO, scale,
                                                                stream=stream)
     return out
+
+
+# ---------------------------------------------------------------- serving
+
+DSA_ROPE_INTERLEAVED, DSA_ROPE_HALF = 0, 1
+DSA_CACHE_BF16, DSA_CACHE_E4M3 = 0, 1
+_ROPE_LAYOUTS = {"interleaved": DSA_ROPE_INTERLEAVED, "half": DSA_ROPE_HALF}
+_CACHE_FORMATS = {"bf16": DSA_CACHE_BF16, "e4m3": DSA_CACHE_E4M3}
+
+
+def _code(value, table: dict, name: str) -> int:
+    if value not in table:
+        raise ValueError(f"{name} is one of {sorted(table)}, got {value!r}")
+    return table[value]
+
+
+def _arg(t, name: str, dtype, shape, device) -> int:
+    """A tensor argument: its type, shape and device checked, its address returned."""
+    p = _dev(t, name, dtype)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other arguments on {device}")
+    return p
+
+
+def _on(stream, device) -> int:
+    """The stream of a call on `device`: its current one where none is given."""
+    return _stream(torch.cuda.current_stream(device) if stream is None else stream)
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None,
+                     factor: float = 1.0, original_length: int = 4096, beta_fast: float = 32.0,
+                     beta_slow: float = 1.0, attention_factor: float | None = None, device=None):
+    """(inv_freq fp32 [rot/2], mscale) for dsa_rope: base ** (-2 i / rot), scaled for contexts
+    `factor` times as long as the original:
+
+    * ``None``     - unscaled;
+    * ``"linear"`` - every frequency divided by factor (positions interpolated);
+    * ``"ntk"``    - the base raised to base * factor ** (rot / (rot - 2)): the highest frequency
+      stays, the lowest is divided by factor;
+    * ``"yarn"``   - frequencies that turn at least beta_fast times within original_length
+      positions stay, those that turn at most beta_slow times are divided by factor, and the dims
+      between the two are blended linearly; mscale is attention_factor, or
+      0.1 ln(factor) + 1 where None.
+    """
+    if rot < 2 or rot % 2:
+        raise ValueError("rot is a positive even number")
+    if scaling not in (None, "linear", "ntk", "yarn"):
+        raise ValueError("scaling is None, 'linear', 'ntk' or 'yarn'")
+    if not base > 1.0 or not factor >= 1.0 or original_length < 1:
+        raise ValueError("base > 1, factor >= 1 and original_length >= 1 are needed")
+    i = torch.arange(rot // 2, dtype=torch.float64)
+    if scaling == "ntk":
+        if rot < 4:
+            raise ValueError("ntk scaling needs rot >= 4")
+        base = base * factor ** (rot / (rot - 2))
+    inv = base ** (-2.0 * i / rot)
+    mscale = 1.0
+    if scaling == "linear":
+        inv = inv / factor
+    elif scaling == "yarn":
+        if not beta_fast > beta_slow > 0.0:
+            raise ValueError("beta_fast > beta_slow > 0 is needed")
+
+        def dim_of(turns):   # the (fractional) frequency index with this many turns
+            return rot * math.log(original_length / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
+
+        lo = max(math.floor(dim_of(beta_fast)), 0)
+        hi = min(math.ceil(dim_of(beta_slow)), rot // 2 - 1)
+        blend = ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        inv = inv * (1.0 - blend) + inv / factor * blend
+        mscale = (0.1 * math.log(factor) + 1.0) if attention_factor is None else attention_factor
+    return inv.float().to("cuda" if device is None else device), mscale
+
+
+def dsa_rope(x, pos, inv_freq, off: int = 0, layout: str = "interleaved", mscale: float = 1.0,
+             inverse: bool = False, out=None, stream=None):
+    """Rotary positions on dims [off, off + rot) of each head (rot = 2 * inv_freq.numel()).
+
+    x [..., H, D] bf16 or fp32, pos int32 with x's leading shape, inv_freq fp32 [rot/2] (as
+    rope_frequencies gives it). out=x rotates in place. The gradient of x is the same call on
+    the gradient of the result with inverse toggled.
+    """
+    if not isinstance(x, torch.Tensor) or x.dim() < 2:
+        raise ValueError("x must be a tensor [..., H, D]")
+    if x.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"x must be bf16 or fp32, got {x.dtype}")
+    code = _code(layout, _ROPE_LAYOUTS, "layout")
+    xp = _dev(x, "x")
+    H, D = x.shape[-2:]
+    rot = 2 * inv_freq.numel()
+    if out is None:
+        out = torch.empty_like(x)
+    args = (xp, _arg(out, "out", x.dtype, x.shape, x.device),
+            DSA_F32 if x.dtype == torch.float32 else DSA_BF16,
+            _arg(pos, "pos", torch.int32, x.shape[:-2], x.device),
+            _arg(inv_freq, "inv_freq", torch.float32, (rot // 2,), x.device), pos.numel(), H, D,
+            off, rot, code, float(mscale), int(bool(inverse)))
+    with torch.cuda.device(x.device):
+        _check(lib.dsa_rope(*args, _on(stream, x.device)), "dsa_rope")
+    return out
+
+
+def cache_row_bytes(Dc: int, Dr: int, fmt: str = "e4m3") -> int:
+    """Bytes of one cache row (0: dims that the cache does not support)."""
+    return int(lib.dsa_cache_row_bytes(_code(fmt, _CACHE_FORMATS, "fmt"), Dc, Dr))
+
+
+def _cache_arg(cache, Dc, Dr, fmt, device) -> tuple[int, int]:
+    """(address, slots) of a cache uint8 [..., row_bytes]."""
+    p = _dev(cache, "cache", torch.uint8)
+    row = cache_row_bytes(Dc, Dr, fmt)
+    if row and cache.shape[-1] != row:
+        raise ValueError(f"cache rows must have {row} bytes, got {cache.shape[-1]}")
+    if cache.device != device:
+        raise ValueError(f"cache is on {cache.device}, the other arguments on {device}")
+    return p, cache.numel() // max(cache.shape[-1], 1)
+
+
+def dsa_cache_write(kv, slots, cache, Dc: int, fmt: str = "e4m3", stream=None):
+    """Write rows kv bf16 [T, Dc + Dr] to the slots int32 [T] of the paged cache, in place.
+
+    cache uint8 [num_pages, page_size, row_bytes] (row_bytes = cache_row_bytes(Dc, Dr, fmt));
+    slot s is row s % page_size of page s // page_size, and -1 skips a row. Returns cache.
+    """
+    kp = _dev(kv, "kv", torch.bfloat16)
+    if kv.dim() != 2 or kv.shape[1] < Dc:
+        raise ValueError("kv must be [T, Dc + Dr]")
+    T, Dr = kv.shape[0], kv.shape[1] - Dc
+    cp, num = _cache_arg(cache, Dc, Dr, fmt, kv.device)
+    sp = _arg(slots, "slots", torch.int32, (T,), kv.device)
+    with torch.cuda.device(kv.device):
+        _check(lib.dsa_cache_write(kp, sp, T, Dc, Dr, _CACHE_FORMATS[fmt], cp, num,
+                                   _on(stream, kv.device)), "dsa_cache_write")
+    return cache
+
+
+def dsa_cache_read(cache, slots, Dc: int, Dr: int, fmt: str = "e4m3", kv=None, stream=None):
+    """The rows of the cache at slots int32 [N] as bf16 [N, Dc + Dr] (zeros at slot -1)."""
+    sp = _dev(slots, "slots", torch.int32)
+    if slots.dim() != 1:
+        raise ValueError("slots must be [N]")
+    N, dev = slots.shape[0], slots.device
+    cp, num = _cache_arg(cache, Dc, Dr, fmt, dev)
+    if kv is None:
+        kv = torch.empty((N, Dc + Dr), dtype=torch.bfloat16, device=dev)
+    kp = _arg(kv, "kv", torch.bfloat16, (N, Dc + Dr), dev)
+    with torch.cuda.device(dev):
+        _check(lib.dsa_cache_read(cp, num, _CACHE_FORMATS[fmt], sp, N, Dc, Dr, kp,
+                                  _on(stream, dev)), "dsa_cache_read")
+    return kv
+
+
+def latent_attn_workspace_bytes(B, Sq, H, Dc, Dr, k=0) -> int:
+    return int(lib.dsa_latent_attn_workspace_size(B, Sq, H, Dc, Dr, k))
+
+
+def dsa_latent_attn(Q, cache, page_table, lens, scale: float, fmt: str = "e4m3", idx=None,
+                    Dc: int = 512, O=None, lse=None, ws=None, stream=None):
+    """Attention of the Sq newest tokens of each sequence over the paged latent cache.
+
+    Q [B,Sq,H,Dc+Dr] bf16, cache uint8 [num_pages, page_size, row_bytes], page_table int32
+    [B, max_pages], lens int32 [B] (cached tokens, the Sq new ones among them), idx int32
+    [B,Sq,k] (the selected positions, as dsa_topk gives them) or None for every cached key
+    -> (O bf16 [B,Sq,H,Dc], lse fp32 [B,Sq,H]).
+
+    ws: a device byte buffer of at least latent_attn_workspace_bytes(...) (allocated here if
+    None).
+    """
+    qp = _dev(Q, "Q", torch.bfloat16)
+    if Q.dim() != 4 or Q.shape[3] < Dc:
+        raise ValueError("Q must be [B, Sq, H, Dc + Dr]")
+    B, Sq, H, D = Q.shape
+    Dr, dev = D - Dc, Q.device
+    cp, _ = _cache_arg(cache, Dc, Dr, fmt, dev)
+    if cache.dim() != 3:
+        raise ValueError("cache must be [num_pages, page_size, row_bytes]")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    k = 0
+    ip = None
+    if idx is not None:
+        k = idx.shape[-1]
+        if k < 1:   # NULL would mean every cached key
+            raise ValueError("idx must list at least one slot per token (-1 for none)")
+        ip = _arg(idx, "idx", torch.int32, (B, Sq, k), dev)
+    tp = _arg(page_table, "page_table", torch.int32, (B, page_table.shape[1]), dev)
+    lp = _arg(lens, "lens", torch.int32, (B,), dev)
+    if O is None:
+        O = torch.empty((B, Sq, H, Dc), dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty((B, Sq, H), dtype=torch.float32, device=dev)
+    op = _arg(O, "O", torch.bfloat16, (B, Sq, H, Dc), dev)
+    ep = _arg(lse, "lse", torch.float32, (B, Sq, H), dev)
+    need = latent_attn_workspace_bytes(B, Sq, H, Dc, Dr, k)
+    if ws is None and need > 0:
+        ws = torch.empty((need,), dtype=torch.uint8, device=dev)
+    if ws is not None and ws.device != dev:
+        raise ValueError(f"ws is on {ws.device}, the other arguments on {dev}")
+    with torch.cuda.device(dev):
+        rc = lib.dsa_latent_attn(qp, cp, _CACHE_FORMATS[fmt], cache.shape[0], cache.shape[1], tp,
+                                 page_table.shape[1], lp, ip, k, B, Sq, H, Dc, Dr, float(scale),
+                                 op, ep, None if ws is None else _dev(ws, "ws"),
+                                 0 if ws is None else ws.numel() * ws.element_size(),
+                                 _on(stream, dev))
+    _check(rc, "dsa_latent_attn")
+    return O, lse

@@ -493,4 +493,106 @@ int dsa_indexer_loss_bwd(const void* q_idx, const void* k_idx, const float* w,
                                            dk_idx, dw, as_stream(stream));
 }
 
+int dsa_rope(const void* x, void* y, int dtype, const int32_t* pos, const float* inv_freq, int T,
+             int H, int D, int off, int rot, int layout, float mscale, int inverse, void* stream) {
+  if (!x || !y || !pos || !inv_freq) return DSA_ERR_INVALID_ARG;
+  if (T < 1 || H < 1 || D < 1 || off < 0 || rot < 1 || off > D || rot > D - off)
+    return DSA_ERR_INVALID_ARG;
+  if (dtype != DSA_F32 && dtype != DSA_BF16) return DSA_ERR_INVALID_ARG;
+  if (layout != DSA_ROPE_INTERLEAVED && layout != DSA_ROPE_HALF) return DSA_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(y) || !aligned16(pos) || !aligned16(inv_freq))
+    return DSA_ERR_INVALID_ARG;
+  if (D > 1024 || D % 8 != 0 || off % 8 != 0 || rot % 16 != 0) return DSA_ERR_UNSUPPORTED;
+  const unsigned long long n = static_cast<unsigned long long>(T) * H;   // < 2^62
+  if (n >= (1ull << 38)) return DSA_ERR_UNSUPPORTED;                     // the grid's range
+  const uintptr_t bytes = static_cast<uintptr_t>(n * D * (dtype == DSA_F32 ? 4 : 2));
+  const uintptr_t xa = reinterpret_cast<uintptr_t>(x), ya = reinterpret_cast<uintptr_t>(y);
+  if (x != y && (xa < ya ? ya - xa : xa - ya) < bytes) return DSA_ERR_INVALID_ARG;
+  return dsa::launch_rope(x, y, dtype == DSA_F32, pos, inv_freq, T, H, D, off, rot,
+                          layout == DSA_ROPE_HALF, mscale, inverse != 0, as_stream(stream));
+}
+
+size_t dsa_cache_row_bytes(int fmt, int Dc, int Dr) { return dsa::cache_row_bytes(fmt, Dc, Dr); }
+
+}  // extern "C"
+
+namespace {
+
+int cache_args_status(const void* kv, const int32_t* slots, int n, int Dc, int Dr, int fmt,
+                      const void* cache, int64_t num_slots) {
+  if (!kv || !slots || !cache) return DSA_ERR_INVALID_ARG;
+  if (n < 1 || Dc < 1 || Dr < 0 || num_slots < 1) return DSA_ERR_INVALID_ARG;
+  if (fmt != DSA_CACHE_BF16 && fmt != DSA_CACHE_E4M3) return DSA_ERR_INVALID_ARG;
+  if (!aligned16(kv) || !aligned16(slots) || !aligned16(cache)) return DSA_ERR_INVALID_ARG;
+  if (dsa::cache_row_bytes(fmt, Dc, Dr) == 0 || num_slots >= (1LL << 31))
+    return DSA_ERR_UNSUPPORTED;
+  return DSA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int dsa_cache_write(const void* kv, const int32_t* slots, int T, int Dc, int Dr, int fmt,
+                    void* cache, int64_t num_slots, void* stream) {
+  const int rc = cache_args_status(kv, slots, T, Dc, Dr, fmt, cache, num_slots);
+  if (rc != DSA_OK) return rc;
+  return dsa::launch_cache_write(kv, slots, T, Dc, Dr, fmt, cache, num_slots, as_stream(stream));
+}
+
+int dsa_cache_read(const void* cache, int64_t num_slots, int fmt, const int32_t* slots, int N,
+                   int Dc, int Dr, void* kv, void* stream) {
+  const int rc = cache_args_status(kv, slots, N, Dc, Dr, fmt, cache, num_slots);
+  if (rc != DSA_OK) return rc;
+  return dsa::launch_cache_read(cache, num_slots, fmt, slots, N, Dc, Dr, kv, as_stream(stream));
+}
+
+size_t dsa_latent_attn_workspace_size(int B, int Sq, int H, int Dc, int Dr, int k) {
+  if (B < 1 || Sq < 1 || H < 1 || H > 128 || Dc != 512 || Dr != 64 || k < 0) return 0;
+  return dsa::latent_attn_workspace(B, Sq, H, k);
+}
+
+int dsa_latent_attn(const void* Q, const void* cache, int fmt, int64_t num_pages, int page_size,
+                    const int32_t* page_table, int max_pages, const int32_t* lens,
+                    const int32_t* idx, int k, int B, int Sq, int H, int Dc, int Dr, float scale,
+                    void* O, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  if (!Q || !cache || !page_table || !lens || !O || !lse) return DSA_ERR_INVALID_ARG;
+  if (B < 1 || Sq < 1 || H < 1 || Dc < 1 || Dr < 0 || num_pages < 1 || page_size < 1 ||
+      max_pages < 1)
+    return DSA_ERR_INVALID_ARG;
+  if (k < 0 || (k > 0) != (idx != nullptr)) return DSA_ERR_INVALID_ARG;
+  if (fmt != DSA_CACHE_BF16 && fmt != DSA_CACHE_E4M3) return DSA_ERR_INVALID_ARG;
+  const void* ptrs[] = {Q, cache, page_table, lens, idx, O, lse};
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return DSA_ERR_INVALID_ARG;
+  if (Dc != 512 || Dr != 64 || H > 128) return DSA_ERR_UNSUPPORTED;
+  if (!(scale > 0.f) || scale > 3.0e38f) return DSA_ERR_UNSUPPORTED;
+  // positions, slots and query rows are counted in 32 bits
+  if (num_pages >= (1LL << 31) || num_pages * page_size >= (1LL << 31) ||
+      static_cast<long long>(max_pages) * page_size >= (1LL << 31) ||
+      static_cast<long long>(B) * Sq >= (1LL << 31) / H)
+    return DSA_ERR_UNSUPPORTED;
+  const size_t need = dsa::latent_attn_workspace(B, Sq, H, k);
+  if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws))) return DSA_ERR_WORKSPACE;
+  dsa::LatentArgs a = {};
+  a.Q = static_cast<const uint16_t*>(Q);
+  a.cache = static_cast<const uint8_t*>(cache);
+  a.page_table = page_table;
+  a.lens = lens;
+  a.idx = idx;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  a.k = k;
+  a.B = B;
+  a.Sq = Sq;
+  a.H = H;
+  a.scale = scale;
+  a.O = static_cast<uint16_t*>(O);
+  a.lse = lse;
+  a.ws = ws;
+  a.err = dsa::device_error_word();
+  return dsa::launch_latent_attn(a, fmt, as_stream(stream));
+}
+
 }  // extern "C"

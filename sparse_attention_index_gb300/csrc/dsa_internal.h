@@ -151,4 +151,30 @@ int launch_indexer_loss_bwd_simt(const void* q_idx, const void* k_idx, const flo
                                  int k, float* dq, float* dk, float* dw, cudaStream_t stream);
 bool indexer_dims_supported(int Hi, int Di);
 
+// serving: rotary positions (rope.cu), the paged latent cache (cache.cu), attention over it
+// (latent_attn.cu)
+int launch_rope(const void* x, void* y, int is_f32, const int32_t* pos, const float* inv_freq,
+                int T, int H, int D, int off, int rot, int half, float mscale, int inverse,
+                cudaStream_t stream);
+size_t cache_row_bytes(int fmt, int Dc, int Dr);   // 0: not supported
+int launch_cache_write(const void* kv, const int32_t* slots, int T, int Dc, int Dr, int fmt,
+                       void* cache, int64_t num_slots, cudaStream_t stream);
+int launch_cache_read(const void* cache, int64_t num_slots, int fmt, const int32_t* slots, int N,
+                      int Dc, int Dr, void* kv, cudaStream_t stream);
+
+struct LatentArgs {
+  const uint16_t* Q;
+  const uint8_t* cache;
+  const int32_t *page_table, *lens, *idx;
+  long long num_pages;
+  int page_size, max_pages, k, B, Sq, H;
+  float scale;
+  uint16_t* O;
+  float* lse;
+  void* ws;
+  int* err;
+};
+size_t latent_attn_workspace(int B, int Sq, int H, int k);
+int launch_latent_attn(const LatentArgs& a, int fmt, cudaStream_t stream);
+
 }  // namespace dsa

@@ -1,0 +1,199 @@
+// Rotary positions on part of each head (dsa_rope): (x_a, x_b) turned by pos * inv_freq.
+//
+// Angle. One turn is 2^64: F = inv_freq / (2 pi) turns per position as a 64-bit fraction, and
+// pos * F mod 2^64 is the turned fraction, with the whole turns dropped by the wrap. The
+// product is exact, so a far position loses nothing but F's own rounding (2^-53 of F, in
+// fp64 once per block and frequency): 2^-25 turns at the farthest position, 2^-36 at 2^20.
+// (An fp32 product pos * inv_freq is off by 2^-24 of the angle: 0.008 rad at 131072. In fp64
+// per angle it would cost as much as the memory traffic when there is one head to share it.)
+// The top 32 bits of the fraction, as a float in [-1/2, 1/2), go to sincospif.
+//
+// Bound: one read and one write of x. A thread moves 16-byte vectors and loads all of its
+// own before the block works out its angles; each (token, frequency) angle is computed once
+// per block and shared by the heads through shared memory. In the half layout the thread
+// with the vector of the first half also handles its partner rot/2 dims on, so that rotating
+// in place reads both before it writes either.
+
+#include "dsa_common.cuh"
+#include "dsa_internal.h"
+
+namespace dsa {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& v, float (&f)[16 / sizeof(T)]);
+template <>
+__device__ __forceinline__ void unpack<float>(const uint4& v, float (&f)[4]) {
+  f[0] = __uint_as_float(v.x);
+  f[1] = __uint_as_float(v.y);
+  f[2] = __uint_as_float(v.z);
+  f[3] = __uint_as_float(v.w);
+}
+template <>
+__device__ __forceinline__ void unpack<uint16_t>(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack(const float (&f)[4]) {
+  return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                    __float_as_uint(f[3]));
+}
+__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
+  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                    pack_bf16(f[6], f[7]));
+}
+
+struct RopeParams {
+  const uint4* x;
+  uint4* y;
+  const int32_t* pos;
+  const float* inv_freq;
+  long long total;   // vectors
+  int vpt;           // vectors per token (H * D / E)
+  int vpd;           // vectors per head
+  int off, rot;      // in elements
+  float mscale;
+  int inverse;
+};
+
+// V vectors per thread, strided by the block
+template <typename T, bool HALF, int V>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+  constexpr int E = 16 / sizeof(T);
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  const int nf = p.rot >> 1;
+  unsigned long long* F = reinterpret_cast<unsigned long long*>(smem_raw);
+  float2* cs = reinterpret_cast<float2*>(smem_raw + nf * sizeof(unsigned long long));
+  const int tid = threadIdx.x;
+  const bool inplace = p.x == p.y;
+  const long long v0 = static_cast<long long>(blockIdx.x) * (kThreads * V);
+  const long long v1 = min(v0 + kThreads * V, p.total);
+  const long long t0 = v0 / p.vpt;
+  const int ntok = static_cast<int>((v1 - 1) / p.vpt - t0) + 1;
+  const int first = static_cast<int>(v0 - t0 * p.vpt);   // of the block, within token t0
+
+  // what this thread's vectors are: copied, turned, or (HALF) the second of a pair, which
+  // the thread of the first handles
+  uint4 a[V], b[V];
+  int tok[V], fi[V];   // fi: -2 none, -1 copied, else the vector's first frequency
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const long long v = v0 + tid + i * kThreads;
+    fi[i] = -2;
+    tok[i] = 0;
+    if (v < v1) {
+      const int in = first + tid + i * kThreads;
+      tok[i] = in / p.vpt;
+      const int d = ((in - tok[i] * p.vpt) % p.vpd) * E - p.off;
+      if (d < 0 || d >= p.rot)
+        fi[i] = inplace ? -2 : -1;
+      else if (!HALF)
+        fi[i] = d >> 1;
+      else if (d < nf)
+        fi[i] = d;
+      if (fi[i] != -2) a[i] = p.x[v];
+      if (HALF && fi[i] >= 0) b[i] = p.x[v + nf / E];
+    }
+  }
+
+  for (int f = tid; f < nf; f += kThreads) {
+    double turns = static_cast<double>(p.inv_freq[f]) * 0.15915494309189533577;
+    turns -= floor(turns);
+    F[f] = static_cast<unsigned long long>(turns * 18446744073709551616.0);
+  }
+  __syncthreads();
+  for (int i = tid; i < ntok * nf; i += kThreads) {
+    const int t = i / nf;
+    const long long at = p.pos[t0 + t];
+    const unsigned long long u = static_cast<unsigned long long>(at) * F[i - t * nf];
+    const float half_turns = static_cast<float>(static_cast<int>(u >> 32)) * 4.6566128730773926e-10f;
+    float s, c;
+    sincospif(half_turns, &s, &c);
+    cs[i] = make_float2(c * p.mscale, (p.inverse ? -s : s) * p.mscale);
+  }
+  __syncthreads();
+
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const long long v = v0 + tid + i * kThreads;
+    if (fi[i] >= 0) {
+      const float2* w = cs + tok[i] * nf + fi[i];
+      float fa[E], fb[E];
+      unpack<T>(a[i], fa);
+      if (HALF) {
+        unpack<T>(b[i], fb);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const float2 r = w[e];
+          const float x = fa[e], y = fb[e];
+          fa[e] = x * r.x - y * r.y;
+          fb[e] = x * r.y + y * r.x;
+        }
+        p.y[v + nf / E] = pack(fb);
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const float2 r = w[e >> 1];
+          const float x = fa[e], y = fa[e + 1];
+          fa[e] = x * r.x - y * r.y;
+          fa[e + 1] = x * r.y + y * r.x;
+        }
+      }
+      p.y[v] = pack(fa);
+    } else if (fi[i] == -1) {
+      p.y[v] = a[i];
+    }
+  }
+}
+
+template <typename T, bool HALF, int V>
+int launch(const RopeParams& p, cudaStream_t stream) {
+  const int nf = p.rot / 2;
+  // tokens that a block's vectors touch
+  const long long ntok = (kThreads * V + p.vpt - 2) / p.vpt + 1;
+  const size_t smem = nf * sizeof(unsigned long long) + ntok * nf * sizeof(float2);
+  auto kern = rope_kernel<T, HALF, V>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  const long long blocks = (p.total + kThreads * V - 1) / (kThreads * V);
+  if (blocks > 0x7fffffffLL) return DSA_ERR_UNSUPPORTED;
+  kern<<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+template <typename T, bool HALF>
+int launch_v(const RopeParams& p, cudaStream_t stream) {
+  return launch<T, HALF, 4>(p, stream);
+}
+
+}  // namespace
+
+int launch_rope(const void* x, void* y, int is_f32, const int32_t* pos, const float* inv_freq,
+                int T, int H, int D, int off, int rot, int half, float mscale, int inverse,
+                cudaStream_t stream) {
+  const int E = is_f32 ? 4 : 8;
+  if (static_cast<long long>(H) * (D / E) > 0x3fffffffLL) return DSA_ERR_UNSUPPORTED;
+  RopeParams p;
+  p.x = static_cast<const uint4*>(x);
+  p.y = static_cast<uint4*>(y);
+  p.pos = pos;
+  p.inv_freq = inv_freq;
+  p.vpd = D / E;
+  p.vpt = H * p.vpd;
+  p.total = static_cast<long long>(T) * p.vpt;
+  p.off = off;
+  p.rot = rot;
+  p.mscale = mscale;
+  p.inverse = inverse;
+  if (is_f32) return half ? launch_v<float, true>(p, stream) : launch_v<float, false>(p, stream);
+  return half ? launch_v<uint16_t, true>(p, stream) : launch_v<uint16_t, false>(p, stream);
+}
+
+}  // namespace dsa

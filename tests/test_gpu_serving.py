@@ -1,0 +1,594 @@
+"""Rotary positions, the paged latent cache and the attention over it, against plain definitions in
+64 bits.
+
+Tolerances. A rounding to bf16 is off by at most 2^-8 of the value, one to fp32 by 2^-24.
+
+* rope: |y - ref| <= r |ref| + 1e-6 m (|a| + |b|), r the rounding of the output type. The second
+  term covers the angle (1.9e-7 rad for its 64-bit fraction at the farthest position, 1.9e-7 for its
+  conversion to fp32), the 2 ulp of sine and cosine (2.4e-7) and four fp32 roundings (2.4e-7).
+* cache: the same bytes as the definition.
+* attention: el bounds the error of a logit: 576 exact products added in fp32, each addition off by
+  at most 2^-23 (truncation) of the sum of magnitudes. Weights are exp(l - m) with relative error
+  2 el + 2^-18 (both l and m move; the fast exponential and its fp32 argument), rounded to bf16
+  (2^-8) for the product with the rows, whose fp32 sums lose at most keys * 2^-23. So
+  |O - ref| <= 2^-8 |ref| + (4 el + 2^-8 + 2^-17 + keys 2^-22) sum_j p_j |v_j|
+  (numerator and denominator), and |lse - ref| <= 2 el + 2^-17 + keys 2^-23 + 2^-22 |ref|. The
+  roundings of the weights are independent of the values, so the norm of the error stays within
+  2^-7 of the norm of O.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DC, DR, D = 512, 64, 576
+
+
+@pytest.fixture(scope="module")
+def dsa():
+    import sparse_attention_index_gb300 as m
+    m.dsa_get_last_device_error()
+    return m
+
+
+def no_error(dsa):
+    assert dsa.dsa_get_last_device_error() == 0
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+# -------------------------------------------------------------------------------------- rope
+
+
+def rope_ref(x, pos, inv_freq, off, rot, layout, mscale, inverse):
+    """(ref, |a| + |b| of each rotated element's pair, 0 elsewhere) in 64 bits."""
+    x = x.double()
+    i = torch.arange(rot // 2, device=x.device)
+    a, b = (off + 2 * i, off + 2 * i + 1) if layout == "interleaved" else (off + i, off + rot // 2 + i)
+    ang = pos.double()[..., None] * inv_freq.double()
+    # turns reduced before the sine, which would itself lose nothing at these sizes
+    c, s = torch.cos(ang)[..., None, :], torch.sin(ang)[..., None, :]
+    if inverse:
+        s = -s
+    y, mag = x.clone(), torch.zeros_like(x)
+    y[..., a] = mscale * (x[..., a] * c - x[..., b] * s)
+    y[..., b] = mscale * (x[..., a] * s + x[..., b] * c)
+    mag[..., a] = mag[..., b] = abs(mscale) * (x[..., a].abs() + x[..., b].abs())
+    return y, mag
+
+
+def rope_close(got, ref, mag):
+    r = 2.0 ** -8 if got.dtype == torch.bfloat16 else 2.0 ** -24
+    err = (got.double() - ref).abs()
+    assert bool((err <= r * ref.abs() + 1e-6 * mag).all()), float((err - r * ref.abs() - 1e-6 * mag).max())
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,H,D_,off,rot", [
+    (1, 1, 16, 0, 16), (1, 128, 192, 128, 64), (37, 3, 24, 8, 16), (513, 1, 64, 0, 32),
+    (5, 7, 128, 0, 128), (700, 2, 576, 512, 64), (3, 1, 1024, 0, 1024), (129, 16, 40, 24, 16),
+    (2, 5, 1000, 8, 992)])
+def test_rope(dsa, layout, dtype, T, H, D_, off, rot):
+    g = gen(T * 1000 + H)
+    x = torch.randn(T, H, D_, generator=g, device="cuda").to(dtype)
+    pos = torch.randint(0, 1 << 20, (T,), generator=g, device="cuda", dtype=torch.int32)
+    inv, _ = dsa.rope_frequencies(rot)
+    for inverse, m in ((False, 1.0), (True, 1.3688879454113936)):
+        ref, mag = rope_ref(x, pos, inv, off, rot, layout, m, inverse)
+        y = dsa.dsa_rope(x, pos, inv, off=off, layout=layout, mscale=m, inverse=inverse)
+        rope_close(y, ref, mag)
+        # dims outside the rotated part are the same bits; in place gives the same bits too
+        keep = torch.ones(D_, dtype=torch.bool, device="cuda")
+        keep[off:off + rot] = False
+        assert torch.equal(y[..., keep], x[..., keep])
+        z = x.clone()
+        assert dsa.dsa_rope(z, pos, inv, off=off, layout=layout, mscale=m, inverse=inverse,
+                            out=z) is z
+        assert torch.equal(z, y)
+    no_error(dsa)
+
+
+def test_rope_far_and_negative_positions(dsa):
+    pos = i32([0, 1, -1, 2 ** 31 - 1, -2 ** 31, 2 ** 30 + 12345, 999999937, 131071])
+    x = torch.randn(8, 2, 64, generator=gen(1), device="cuda")
+    for rot, scaling in ((64, None), (64, "yarn"), (32, "linear")):
+        inv, m = dsa.rope_frequencies(rot, scaling=scaling, factor=32.0)
+        ref, mag = rope_ref(x, pos, inv, 0, rot, "half", m, False)
+        rope_close(dsa.dsa_rope(x, pos, inv, layout="half", mscale=m), ref, mag)
+
+
+def test_rope_is_relative_and_its_inverse_is_the_gradient(dsa):
+    g = gen(2)
+    inv, _ = dsa.rope_frequencies(64)
+    T, H = 50, 4
+    x = torch.randn(T, H, 192, generator=g, device="cuda")
+    dy = torch.randn(T, H, 192, generator=g, device="cuda")
+    pos = torch.randint(0, 100000, (T,), generator=g, device="cuda", dtype=torch.int32)
+    kw = dict(off=128, layout="interleaved", mscale=1.25)
+    y = dsa.dsa_rope(x, pos, inv, **kw)
+    dx = dsa.dsa_rope(dy, pos, inv, inverse=True, **kw)
+    # <dy, J x> = <J^T dy, x>; each side sums 192 H T products with relative errors <= 2e-6
+    lhs, rhs = (dy.double() * y.double()).sum(), (dx.double() * x.double()).sum()
+    scale = (dy.double().abs() * y.double().abs()).sum() + (dx.double().abs() * x.double().abs()).sum()
+    assert abs(lhs - rhs) <= 2e-6 * scale
+    # against differences: the map is linear, so a step of any size gives the derivative up to
+    # the rounding of its two values
+    h = torch.randn(T, H, 192, generator=g, device="cuda")
+    diff = (dsa.dsa_rope(x + h, pos, inv, **kw).double() - y.double())
+    ref, mag = rope_ref((x + h).double() - x.double(), pos, inv, 128, 64, "interleaved", 1.25, False)
+    room = 2.0 ** -23 * (y.double().abs() + diff.abs()) + 1e-6 * 4 * (mag + 4)
+    assert bool(((diff - ref).abs() <= room).all())
+    # scores depend on the distance alone: <R(p) a, R(q) b> = <R(p + s) a, R(q + s) b>
+    for s in (1, 4096, 10 ** 9):
+        a, b = x[:, :1].contiguous(), dy[:, :1].contiguous()
+        p, q = pos % 1000, (pos + 7) % 1000
+        dot = lambda u, v: (u.double() * v.double()).sum(-1)  # noqa: E731
+        one = dot(dsa.dsa_rope(a, p, inv, off=128), dsa.dsa_rope(b, q, inv, off=128))
+        two = dot(dsa.dsa_rope(a, p + s, inv, off=128), dsa.dsa_rope(b, q + s, inv, off=128))
+        room = 8e-6 * (a.double().norm(dim=-1) * b.double().norm(dim=-1))
+        assert bool(((one - two).abs() <= room).all())
+
+
+def test_rope_leading_shapes_streams_and_refusals(dsa):
+    g = gen(3)
+    inv, _ = dsa.rope_frequencies(32)
+    x = torch.randn(2, 9, 3, 64, generator=g, device="cuda")
+    pos = torch.randint(0, 4096, (2, 9), generator=g, device="cuda", dtype=torch.int32)
+    y = dsa.dsa_rope(x, pos, inv, off=32)
+    assert torch.equal(y.view(18, 3, 64), dsa.dsa_rope(x.view(18, 3, 64), pos.view(18), inv, off=32))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    z = dsa.dsa_rope(x, pos, inv, off=32, stream=side)
+    side.synchronize()
+    assert torch.equal(z, y)
+    for bad in (dict(pos=pos.view(18)), dict(pos=pos.long()), dict(inv_freq=inv.double()),
+                dict(x=x.transpose(0, 1)), dict(out=torch.empty_like(x)[:1]), dict(layout="other"),
+                dict(off=40), dict(off=4)):
+        kw = dict(x=x, pos=pos, inv_freq=inv, off=32)
+        kw.update(bad)
+        with pytest.raises((TypeError, ValueError, dsa.DsaError)):
+            dsa.dsa_rope(**kw)
+
+
+# ------------------------------------------------------------------------------------- cache
+
+
+def e4m3_values():
+    b = np.arange(256)
+    e, m = (b >> 3) & 15, b & 7
+    v = np.where(e == 0, m / 8 * 2.0 ** -6, (1 + m / 8) * 2.0 ** (e - 7.0))
+    v[(b & 0x7f) == 0x7f] = np.nan
+    return np.where(b & 0x80, -v, v)
+
+
+def encode_ref(kv, Dc, fmt):
+    """The bytes of cache rows for kv bf16 [T, Dc + Dr] (CPU tensors), from the definition."""
+    T = kv.shape[0]
+    raw = kv.view(torch.int16).numpy().view(np.uint8).reshape(T, -1)
+    if fmt == "bf16":
+        return raw.copy()
+    x = kv[:, :Dc].double().numpy().reshape(T, Dc // 128, 128)
+    amax = np.abs(x).max(-1)
+    bad = ~np.isfinite(x).all(-1)
+    with np.errstate(all="ignore"):
+        k = np.ceil(np.log2(amax / 448.0))
+    k = np.where(amax == 0, 0, np.maximum(k, -120))
+    k = np.where(bad, 0, k)
+    vals = e4m3_values()
+    pos = vals[:127]                                     # 0 .. 448, ascending
+    y = np.where(np.isfinite(x), x, 0) / 2.0 ** k[..., None]
+    mid = (pos[1:] + pos[:-1]) / 2
+    lo = np.searchsorted(mid, np.abs(y), side="left")    # ties to the lower code ...
+    tie = (lo < 126) & (np.abs(y) == mid[np.minimum(lo, 125)])
+    code = np.where(tie & (lo % 2 == 1), lo + 1, lo)     # ... unless the upper one is even
+    code = (code | np.where(np.signbit(y), 0x80, 0)).astype(np.uint8)
+    scale = np.where(bad, np.nan, 2.0 ** k).astype(np.float32)
+    pad = np.zeros((T, (Dc // 128 + 3) // 4 * 4), np.float32)
+    pad[:, :Dc // 128] = scale
+    return np.concatenate([code.reshape(T, Dc), pad.view(np.uint8), raw[:, 2 * Dc:]], 1), bad
+
+
+def cache_inputs(T, Dc, Dr, seed):
+    g = torch.Generator().manual_seed(seed)
+    kv = torch.randn(T, Dc + Dr, generator=g)
+    kv *= torch.exp2(torch.randint(-30, 30, (T, 1), generator=g).float())
+    return kv.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("Dc,Dr", [(512, 64), (128, 0), (128, 64), (640, 8), (1024, 256), (256, 136)])
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("T", [1, 7, 130])
+def test_cache_write_and_read(dsa, Dc, Dr, fmt, T):
+    kv = cache_inputs(T, Dc, Dr, T + Dc)
+    if T == 7:   # a group of zeros, one of the largest values, one of the smallest
+        kv[1, :128] = 0
+        kv[2, :128] = torch.finfo(torch.bfloat16).max
+        kv[3, :128] = 2.0 ** -133
+        kv[4, :128] = -448.0
+    pages, page = 9, 19
+    row = dsa.cache_row_bytes(Dc, Dr, fmt)
+    start = torch.randint(0, 256, (pages, page, row), dtype=torch.uint8)
+    cache = start.cuda()
+    slots = torch.randperm(pages * page)[:T].to(torch.int32)
+    if T > 1:
+        slots[T // 2] = -1
+    assert dsa.dsa_cache_write(kv.cuda(), slots.cuda(), cache, Dc, fmt=fmt) is cache
+    want = start.view(-1, row).clone().numpy()
+    ref = encode_ref(kv, Dc, fmt)
+    ref = ref if fmt == "bf16" else ref[0]
+    live = slots.numpy() >= 0
+    want[slots.numpy()[live]] = ref[live]
+    assert np.array_equal(cache.view(-1, row).cpu().numpy(), want)   # every other byte unchanged
+    back = dsa.dsa_cache_read(cache, slots.cuda(), Dc, Dr, fmt=fmt).double().cpu().numpy()
+    x = kv.double().numpy()
+    assert np.array_equal(back[~live], np.zeros_like(back[~live]))
+    if fmt == "bf16":
+        assert np.array_equal(back[live], x[live])
+    else:
+        assert np.array_equal(back[:, Dc:][live], x[:, Dc:][live])
+        sc = np.repeat(ref[:, Dc:Dc + 4 * (Dc // 128)].copy().view(np.float32).astype(np.float64), 128, 1)
+        exact = e4m3_values()[ref[:, :Dc]] * sc
+        # exact in bf16, but for what rounds up past its largest value (2^128)
+        with np.errstate(invalid="ignore"):   # NaN codes in the rows that were skipped
+            held = np.where(np.abs(exact) < 2.0 ** 128, exact, np.sign(exact) * np.inf)
+        assert np.array_equal(back[:, :Dc][live], held[live])
+        err = np.abs(exact - x[:, :Dc])
+        assert (err <= np.maximum(2.0 ** -4 * np.abs(x[:, :Dc]), 2.0 ** -10 * sc)).all()
+    # repeats are allowed when reading
+    twice = torch.cat([slots, slots]).cuda()
+    again = dsa.dsa_cache_read(cache, twice, Dc, Dr, fmt=fmt).double().cpu().numpy()
+    assert np.array_equal(again[:T], back) and np.array_equal(again[T:], back)
+    no_error(dsa)
+
+
+def test_cache_values_that_are_not_finite(dsa):
+    kv = cache_inputs(4, 512, 64, 5)
+    kv[0, 3] = math.inf
+    kv[1, 200] = math.nan
+    kv[2, 511] = -math.inf
+    kv[3, 512 + 9] = math.nan          # a positional dim: kept as it is
+    cache = torch.zeros(1, 4, 656, dtype=torch.uint8, device="cuda")
+    slots = i32([0, 1, 2, 3])
+    dsa.dsa_cache_write(kv.cuda(), slots, cache, 512)
+    back = dsa.dsa_cache_read(cache, slots, 512, 64).float().cpu()
+    nan = torch.isnan(back)
+    want = torch.zeros_like(nan)
+    want[0, :128] = want[1, 128:256] = want[2, 384:512] = True
+    want[3, 512 + 9] = True
+    assert torch.equal(nan, want)
+
+
+def test_cache_bad_slots(dsa):
+    """A slot outside the cache is recorded and skipped, the others are served."""
+    kv = cache_inputs(5, 512, 64, 6).cuda()
+    for fmt in ("bf16", "e4m3"):
+        row = dsa.cache_row_bytes(512, 64, fmt)
+        cache = torch.full((2, 3, row), 7, dtype=torch.uint8, device="cuda")
+        dsa.dsa_cache_write(kv, i32([5, 6, -2, 0, 2 ** 31 - 1]), cache, 512, fmt=fmt)
+        assert dsa.dsa_get_last_device_error() == dsa.DSA_STAGE_CACHE | dsa.DSA_DEVERR_BAD_INDEX
+        untouched = cache.view(6, row)[1:5]
+        assert bool((untouched == 7).all())
+        got = dsa.dsa_cache_read(cache, i32([0, 5, -1]), 512, 64, fmt=fmt)
+        no_error(dsa)
+        bad = dsa.dsa_cache_read(cache, i32([0, 6, 5, -7]), 512, 64, fmt=fmt)
+        assert dsa.dsa_get_last_device_error() == dsa.DSA_STAGE_CACHE | dsa.DSA_DEVERR_BAD_INDEX
+        assert torch.equal(bad[0], got[0]) and torch.equal(bad[2], got[1])
+        assert not bad[1].any() and not bad[3].any() and not got[2].any()
+
+
+# --------------------------------------------------------------------------------- attention
+
+
+def make_cache(dsa, lens, page, fmt, seed, scale=1.0, spare=2):
+    """A paged cache holding random rows for each sequence, its pages shuffled; the rows behind
+    each sequence and the spare pages hold NaN. -> (cache, table, rows fp64 by sequence)."""
+    g = gen(seed)
+    need = [-(-max(n, 0) // page) for n in lens]
+    total = sum(need) + spare
+    order = torch.randperm(total, generator=g, device="cuda").tolist()
+    row = dsa.cache_row_bytes(DC, DR, fmt)
+    cache = torch.full((total, page, row), 0xff, dtype=torch.uint8, device="cuda")   # NaN everywhere
+    table = torch.full((len(lens), max(max(need), 1) + 1), 2 ** 30, dtype=torch.int32)  # never read
+    rows, first = [], 0
+    for b, n in enumerate(lens):
+        mine = order[first:first + need[b]]
+        first += need[b]
+        table[b, :need[b]] = torch.tensor(mine, dtype=torch.int32)
+        n = max(n, 0)
+        kv = (torch.randn(n, D, generator=g, device="cuda") * scale).to(torch.bfloat16)
+        if n:
+            at = torch.arange(n)
+            slots = (torch.tensor(mine)[at // page] * page + at % page).to(torch.int32).cuda()
+            dsa.dsa_cache_write(kv, slots, cache, DC, fmt=fmt)
+            kv = dsa.dsa_cache_read(cache, slots, DC, DR, fmt=fmt)
+        rows.append(kv.double())
+    return cache, table.cuda(), rows
+
+
+def attn_check(O, lse, Q, rows, lens, scale, idx=None):
+    """Holds (O, lse) to the definition in 64 bits within the tolerances above."""
+    B, Sq, H, _ = Q.shape
+    err2 = ref2 = 0.0
+    for b in range(B):
+        n = max(int(lens[b]), 0)
+        for i in range(Sq):
+            lim = n - Sq + i + 1
+            keys = rows[b][:max(lim, 0)]
+            if idx is not None:
+                t = idx[b, i].long()
+                keys = rows[b][t[(t >= 0) & (t < lim)]]
+            got, gl = O[b, i].double(), lse[b, i].double()
+            if len(keys) == 0:
+                assert not got.any() and bool((gl == -math.inf).all())
+                continue
+            q = Q[b, i].double()
+            l = scale * (q @ keys.T)
+            ref_l = torch.logsumexp(l, -1)
+            p = torch.exp(l - ref_l[:, None])
+            ref = p @ keys[:, :DC]
+            el = D * 2.0 ** -23 * scale * (q.abs() @ keys.abs().T).amax(-1)
+            pv = p @ keys[:, :DC].abs()
+            nk = len(keys)
+            tol = 2.0 ** -8 * ref.abs() + (4 * el[:, None] + 2.0 ** -8 + 2.0 ** -17 + nk * 2.0 ** -22) * pv
+            assert bool(((got - ref).abs() <= tol).all()), (b, i, float(((got - ref).abs() / tol).max()))
+            assert bool(((gl - ref_l).abs() <= 2 * el + 2.0 ** -17 + nk * 2.0 ** -23
+                         + 2.0 ** -22 * ref_l.abs()).all()), (b, i, float((gl - ref_l).abs().max()))
+            err2 += float(((got - ref) ** 2).sum())
+            ref2 += float((ref ** 2).sum())
+    assert err2 <= (2.0 ** -7) ** 2 * ref2, math.sqrt(err2 / max(ref2, 1e-300))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("B,Sq,H,lens,page", [
+    (1, 1, 1, [1], 16), (1, 1, 128, [1], 1), (1, 1, 16, [489], 64), (3, 1, 128, [47, 48, 49], 7),
+    (4, 1, 20, [0, 1, 97, 0], 16), (2, 4, 16, [3, 130], 16), (2, 3, 128, [2, 700], 100),
+    (1, 7, 5, [7], 64), (5, 2, 64, [96, 1000, 1, 31, 2049], 32), (1, 1, 128, [20000], 64),
+    (2, 1, 33, [-5, 64], 16), (1, 70, 3, [200], 16)])
+def test_latent_attn(dsa, fmt, B, Sq, H, lens, page):
+    cache, table, rows = make_cache(dsa, lens, page, fmt, 11)
+    no_error(dsa)
+    Q = torch.randn(B, Sq, H, D, generator=gen(12), device="cuda").to(torch.bfloat16)
+    scale = 192 ** -0.5
+    O = torch.full((B, Sq, H, DC), math.nan, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((B, Sq, H), math.nan, device="cuda")
+    dsa.dsa_latent_attn(Q, cache, table, i32(lens), scale, fmt=fmt, O=O, lse=lse)
+    want = dsa.DSA_STAGE_LATENT | dsa.DSA_DEVERR_BAD_PAGE if min(lens) < 0 else 0
+    assert dsa.dsa_get_last_device_error() == want
+    attn_check(O, lse, Q, rows, lens, scale)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("B,Sq,H,lens,k", [
+    (1, 1, 128, [300], 1), (2, 1, 16, [64, 5000], 48), (3, 2, 128, [1, 0, 777], 100),
+    (1, 1, 7, [40], 64), (40, 1, 128, [2500] * 40, 2048), (1, 130, 2, [130], 33),
+    (2, 5, 64, [900, 3], 17)])
+def test_latent_attn_selected(dsa, fmt, B, Sq, H, lens, k):
+    """Lists as the top-k gives them (ascending, -1 behind), and lists with holes, entries above
+    the diagonal and rows that list nothing."""
+    cache, table, rows = make_cache(dsa, lens, 64, fmt, 21)
+    g = gen(22)
+    Q = torch.randn(B, Sq, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    idx = torch.full((B, Sq, k), -1, dtype=torch.int32)
+    for b, n in enumerate(lens):
+        for i in range(Sq):
+            lim = n - Sq + i + 1
+            pick = torch.randperm(max(n if (i + b) % 3 == 1 else lim, 0))[:k].sort().values
+            idx[b, i, :len(pick)] = pick.to(torch.int32)
+            if (i + b) % 3 == 2:
+                idx[b, i, ::2] = -1
+            if (i + b) % 7 == 6:
+                idx[b, i] = -1
+    idx = idx.cuda()
+    O, lse = dsa.dsa_latent_attn(Q, cache, table, i32(lens), 192 ** -0.5, fmt=fmt, idx=idx)
+    no_error(dsa)
+    attn_check(O, lse, Q, rows, lens, 192 ** -0.5, idx)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_latent_attn_bad_lists_pages_and_lengths(dsa, fmt):
+    """What points outside the cache is recorded and skipped; the rest of the row is computed."""
+    lens = [200, 100]
+    cache, table, rows = make_cache(dsa, lens, 16, fmt, 31)
+    Q = torch.randn(2, 1, 16, D, generator=gen(32), device="cuda").to(torch.bfloat16)
+    idx = i32([[[3, 5, 200, 9, -2, 2 ** 31 - 1, -1, 199]], [[0, 1, 2, 99, 100, -1, -1, -1]]])
+    O, lse = dsa.dsa_latent_attn(Q, cache, table, i32(lens), 0.07, fmt=fmt, idx=idx)
+    assert dsa.dsa_get_last_device_error() == dsa.DSA_STAGE_LATENT | dsa.DSA_DEVERR_BAD_INDEX
+    ok = idx.clone()
+    ok[(ok >= i32(lens)[:, None, None]) | (ok < -1)] = -1
+    attn_check(O, lse, Q, rows, lens, 0.07, ok)
+    # a page outside the cache: its 16 keys are not there
+    bad = table.clone()
+    bad[0, 2], bad[1, 6] = -3, cache.shape[0]
+    O, lse = dsa.dsa_latent_attn(Q, cache, bad, i32(lens), 0.07, fmt=fmt)
+    assert dsa.dsa_get_last_device_error() == dsa.DSA_STAGE_LATENT | dsa.DSA_DEVERR_BAD_PAGE
+    left = [torch.cat([rows[0][:32], rows[0][48:]]), rows[1][:96]]
+    attn_check(O, lse, Q, left, [len(x) for x in left], 0.07)
+    # a length behind the page table is cut to it
+    full = torch.arange(4, dtype=torch.int32, device="cuda").view(1, 4)
+    dsa.dsa_cache_write(rows[0][:64].to(torch.bfloat16), i32(range(64)), cache, DC, fmt=fmt)
+    kept = dsa.dsa_cache_read(cache, i32(range(64)), DC, DR, fmt=fmt).double()
+    O, lse = dsa.dsa_latent_attn(Q[:1], cache, full, i32([10 ** 9]), 0.07, fmt=fmt)
+    assert dsa.dsa_get_last_device_error() == dsa.DSA_STAGE_LATENT | dsa.DSA_DEVERR_BAD_PAGE
+    attn_check(O, lse, Q[:1], [kept], [64], 0.07)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_latent_attn_large_and_small_logits(dsa, fmt):
+    """Logits far apart (the running maximum moves by more than any exponent holds), all equal, and
+    a key far above the rest at the very end."""
+    n = 700
+    cache, table, rows = make_cache(dsa, [n], 64, fmt, 41)
+    Q = torch.randn(1, 1, 16, D, generator=gen(42), device="cuda")
+    Q[0, 0, 0] = 0.0
+    Q[0, 0, 1] = rows[0][n - 1] * 4
+    Q[0, 0, 2] = rows[0][0] * 4
+    Q[0, 0, 3] = -rows[0][n - 1] * 4
+    Q[0, 0, 4:8] *= 1e-3
+    Q = Q.to(torch.bfloat16)
+    for scale in (0.07, 3.0):
+        O, lse = dsa.dsa_latent_attn(Q, cache, table, i32([n]), scale, fmt=fmt)
+        attn_check(O, lse, Q, rows, [n], scale)
+    # all logits zero: n weights of one
+    assert bool((lse[0, 0, 0] - math.log(n)).abs() <= 2.0 ** -17 + n * 2.0 ** -23)
+
+
+def test_latent_attn_non_finite_rows_outside(dsa):
+    """NaN in rows behind the sequence, in unlisted rows and in pages of others changes nothing;
+    an infinity in a seen row shows in the result of that sequence alone."""
+    lens = [100, 90]
+    cache, table, rows = make_cache(dsa, lens, 64, "bf16", 51)
+    Q = torch.randn(2, 1, 16, D, generator=gen(52), device="cuda").to(torch.bfloat16)
+    O, lse = dsa.dsa_latent_attn(Q, cache, table, i32(lens), 0.07, fmt="bf16")
+    attn_check(O, lse, Q, rows, lens, 0.07)
+    at = int(table[0, 0]) * 64 + 5
+    bad = cache.clone().view(-1, 1152).view(torch.bfloat16)
+    bad[at, 3] = math.nan
+    bad = bad.view(torch.uint8).view_as(cache)
+    O2, lse2 = dsa.dsa_latent_attn(Q, bad, table, i32(lens), 0.07, fmt="bf16")
+    assert torch.equal(O2[1], O[1]) and torch.equal(lse2[1], lse[1])
+    assert bool(torch.isnan(lse2[0]).all()) and bool(torch.isnan(O2[0]).all())
+    idx = i32([[[0, 1, 2, 3, 4, 6, 7, -1]], [[0, 1, 2, 3, 4, 5, 6, 7]]])
+    O3, lse3 = dsa.dsa_latent_attn(Q, bad, table, i32(lens), 0.07, fmt="bf16", idx=idx)
+    attn_check(O3, lse3, Q, rows, lens, 0.07, idx)
+
+
+def test_latent_attn_same_bits_every_time_and_on_any_stream(dsa):
+    """No atomics: repeated, concurrent (own workspaces) and captured calls give the same bits."""
+    lens = [3000, 1, 700]
+    cache, table, _ = make_cache(dsa, lens, 64, "e4m3", 61)
+    Q = torch.randn(3, 2, 32, D, generator=gen(62), device="cuda").to(torch.bfloat16)
+    n = i32(lens)
+    O, lse = dsa.dsa_latent_attn(Q, cache, table, n, 0.07)
+    torch.cuda.synchronize()
+    outs, streams = [], [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(4):
+        for st in streams:
+            with torch.cuda.stream(st):
+                outs.append(dsa.dsa_latent_attn(Q, cache, table, n, 0.07))
+    torch.cuda.synchronize()
+    for o, e in outs:
+        assert torch.equal(o, O) and torch.equal(e, lse)
+    ws = torch.empty(max(dsa.latent_attn_workspace_bytes(3, 2, 32, DC, DR), 16), dtype=torch.uint8,
+                     device="cuda")
+    graphs, got = [], []
+    for _ in range(2):   # two graphs on one workspace, replayed in turn
+        g = torch.cuda.CUDAGraph()
+        o, e = torch.empty_like(O), torch.empty_like(lse)
+        with torch.cuda.graph(g):
+            dsa.dsa_latent_attn(Q, cache, table, n, 0.07, O=o, lse=e, ws=ws)
+        graphs.append(g)
+        got.append((o, e))
+    for _ in range(3):
+        ws.fill_(0xff)
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for o, e in got:
+        assert torch.equal(o, O) and torch.equal(e, lse)
+    # a replay reads the lengths and the table of that moment
+    n.copy_(i32([5, 3000 // 64 * 64 + 1, 0]))
+    table[1, :47] = table[0, :47].clone()
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    O2, lse2 = dsa.dsa_latent_attn(Q, cache, table, n, 0.07)
+    assert torch.equal(O2, got[0][0]) and torch.equal(lse2, got[0][1])
+    no_error(dsa)
+
+
+def test_latent_attn_slots_past_32_bits(dsa):
+    """A cache of more than 2^31 bytes: rows at its far end."""
+    page, pages = 64, 60000   # 60000 * 64 * 1152 bytes = 4.4e9
+    cache = torch.empty(pages, page, 1152, dtype=torch.uint8, device="cuda")
+    table = i32([[pages - 1, pages - 2, 0]])
+    n = 150
+    kv = torch.randn(n, D, generator=gen(71), device="cuda").to(torch.bfloat16)
+    at = torch.arange(n, device="cuda")
+    slots = (table[0].long()[at // page] * page + at % page).to(torch.int32)
+    dsa.dsa_cache_write(kv, slots, cache, DC, fmt="bf16")
+    assert torch.equal(dsa.dsa_cache_read(cache, slots, DC, DR, fmt="bf16"), kv)
+    Q = torch.randn(1, 1, 16, D, generator=gen(72), device="cuda").to(torch.bfloat16)
+    O, lse = dsa.dsa_latent_attn(Q, cache, table, i32([n]), 0.07, fmt="bf16")
+    no_error(dsa)
+    attn_check(O, lse, Q, [kv.double()], [n], 0.07)
+
+
+def test_latent_attn_refusals(dsa):
+    cache, table, _ = make_cache(dsa, [64], 64, "e4m3", 81)
+    Q = torch.zeros(1, 1, 16, D, dtype=torch.bfloat16, device="cuda")
+    good = dict(Q=Q, cache=cache, page_table=table, lens=i32([64]), scale=0.1)
+    dsa.dsa_latent_attn(**good)
+    idx = i32([[[0, 1]]])
+    for bad in (dict(fmt="bf16"), dict(fmt="fp4"), dict(scale=0.0), dict(lens=i32([64, 64])),
+                dict(lens=i32([64]).long()), dict(page_table=table[0]), dict(Q=Q.float()),
+                dict(Q=Q[..., :500].contiguous()), dict(Q=torch.cat([Q] * 9, 2)),
+                dict(cache=cache.view(-1, 656)), dict(idx=idx[..., :0]), dict(idx=idx[0]),
+                dict(idx=idx.long()), dict(lens=i32([64]).cpu()), dict(O=Q), dict(Dc=256),
+                dict(Q=Q.expand(1, 2, 16, D)), dict(lse=torch.empty(1, 16, 1, device="cuda"))):
+        with pytest.raises((TypeError, ValueError, dsa.DsaError)):
+            dsa.dsa_latent_attn(**{**good, **bad})
+    no_error(dsa)
+
+
+# --------------------------------------------------------------------------- used together
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_decode_steps(dsa, fmt):
+    """A prompt, then tokens one by one: rotary positions into the rows, the rows into the cache,
+    attention over it; each token against the same attention computed from scratch."""
+    B, H, page, steps = 3, 16, 16, 4
+    prompt = [33, 1, 64]
+    inv, m = dsa.rope_frequencies(DR, scaling="yarn", factor=4.0)
+    g = gen(91)
+    total = [p + steps for p in prompt]
+    raw = [torch.randn(n, 1, D, generator=g, device="cuda").to(torch.bfloat16) for n in total]
+    table = torch.arange(B * 5, dtype=torch.int32, device="cuda").flip(0).view(B, 5)
+    cache = torch.zeros(B * 5, page, dsa.cache_row_bytes(DC, DR, fmt), dtype=torch.uint8, device="cuda")
+
+    def store(b, first, last):
+        pos = torch.arange(first, last, dtype=torch.int32, device="cuda")
+        kv = dsa.dsa_rope(raw[b][first:last].contiguous(), pos, inv, off=DC, mscale=m)
+        slots = (table[b].long()[pos.long() // page] * page + pos % page).to(torch.int32)
+        dsa.dsa_cache_write(kv.view(-1, D), slots, cache, DC, fmt=fmt)
+        return slots
+
+    all_slots = [[store(b, 0, prompt[b])] for b in range(B)]
+    for s in range(steps):
+        lens = [p + s + 1 for p in prompt]
+        for b in range(B):
+            all_slots[b].append(store(b, lens[b] - 1, lens[b]))
+        q = torch.randn(B, 1, H, D, generator=g, device="cuda").to(torch.bfloat16)
+        q = dsa.dsa_rope(q, i32([[n - 1] for n in lens]), inv, off=DC, mscale=m)
+        O, lse = dsa.dsa_latent_attn(q, cache, table, i32(lens), 192 ** -0.5, fmt=fmt)
+        rows = [dsa.dsa_cache_read(cache, torch.cat(all_slots[b]), DC, DR, fmt=fmt).double()
+                for b in range(B)]
+        attn_check(O, lse, q, rows, lens, 192 ** -0.5)
+    no_error(dsa)
+
+
+def test_prompt_with_the_selection_of_the_top_k(dsa):
+    """A prompt in the absorbed form: the indexer's scores and the top-k of the whole sequence
+    give the lists, all of its tokens attend as the newest ones of the sequence."""
+    S, H, k = 200, 8, 32
+    g = gen(95)
+    bf = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    scores = dsa.dsa_index_scores(bf(1, S, 64, 128), bf(1, S, 128),
+                                  torch.rand(1, S, 64, generator=g, device="cuda"))
+    idx, _ = dsa.dsa_topk(scores, k, S=S)
+    cache, table, rows = make_cache(dsa, [S], 64, "bf16", 96)
+    Q = bf(1, S, H, D)
+    O, lse = dsa.dsa_latent_attn(Q, cache, table, i32([S]), 192 ** -0.5, fmt="bf16", idx=idx)
+    no_error(dsa)
+    attn_check(O, lse, Q, rows, [S], 192 ** -0.5, idx)
