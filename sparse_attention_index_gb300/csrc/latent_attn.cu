@@ -21,14 +21,21 @@
 // one range is written out there; the others leave (O, m, l) in the workspace and
 // latent_join_kernel adds them up. Lengths are read on the device only.
 //
-// Warp-specialised CTA, 416 threads:
-//   warps 0-3   softmax / output: one (token, head) row per thread
-//   warp  4     TMEM owner and single-thread UMMA issuer
-//   warps 5-12  gather, six keys of each chunk per warp: page lookup two chunks ahead, then
-//               16-byte cp.async into 128B-swizzled tiles. An e4m3 row goes through a raw ring
-//               (each thread copies in what it will convert itself, so no barrier is needed)
-//               and is widened to bf16, exactly, since its scales are powers of two.
-// TMEM: [Q: 144][S/P: 2 x 48][pad 16][O: 256] = 512 columns.
+// Warp-specialised CTA, 480 threads (four warps a scheduler at most: 128 registers each):
+//   warps 0-7   softmax / output, one (token, head) row per thread: warps 0-3 the even chunks,
+//               warps 4-7 the odd ones. A chunk's way through a softmax warp is a chain of
+//               latencies (S out of TMEM, the peer's half of it, the exponentials), about three
+//               times what its products take, so two of them run side by side. They share the
+//               running maximum, which passes from chunk to chunk in order; each keeps the sum
+//               of its own chunks.
+//   warp  8     TMEM owner and single-thread UMMA issuer; S runs two chunks ahead of P V
+//   warps 9-14  gather, eight keys of each chunk per warp: the slots of four chunks are looked up
+//               at once, one key per lane, a batch ahead for the page and two for the list entry;
+//               then 16-byte cp.async into 128B-swizzled tiles. e4m3 rows are loaded into
+//               registers two chunks ahead and widened to bf16, exactly, since their scales are
+//               powers of two.
+// P goes to the tensor cores through shared memory, so that a chunk's S columns are free again
+// once they have been read. TMEM: [Q: 144][S: 2 x 48][pad 16][O: 256] = 512 columns.
 
 #include <mutex>
 
@@ -47,7 +54,10 @@ constexpr int kAtoms = 5;                // 64-dim atoms per key; the last one h
 constexpr uint32_t kAtom = kNK * 128;
 constexpr uint32_t kStage = kAtoms * kAtom;
 constexpr uint32_t kExch = 128 * kNK * 4;   // one buffer of the peer's partial S
-constexpr int kGatherWarp0 = 5, kGatherWarps = 8;
+constexpr uint32_t kPTile = 128 * 32;       // P of 16 keys: one k-step of P V
+constexpr uint32_t kPBuf = kNK / 16 * kPTile;
+constexpr int kIssueWarp = 8;
+constexpr int kGatherWarp0 = 9, kGatherWarps = 6;
 constexpr int kGatherThreads = 32 * kGatherWarps;
 constexpr int kKeysPerWarp = kNK / kGatherWarps;
 constexpr int kThreads = 32 * (kGatherWarp0 + kGatherWarps);
@@ -58,43 +68,44 @@ constexpr float kRescaleLog2 = 8.f;      // refresh the running max when it grow
 constexpr int kErrIdx = DSA_STAGE_LATENT | DSA_DEVERR_BAD_INDEX;
 constexpr int kErrPage = DSA_STAGE_LATENT | DSA_DEVERR_BAD_PAGE;
 constexpr int kErrTime = DSA_STAGE_LATENT | DSA_DEVERR_TIMEOUT;
-static_assert(kKeysPerWarp * kGatherWarps == kNK, "six keys per gather warp");
+static_assert(kKeysPerWarp == 8, "the keys of a gather warp are one byte of the chunk's mask");
 
-// e4m3: 48 keys x 16 pieces of 16 codes, three per gather thread, each with its scale, and
-// 48 x 4 pieces of positional dims
+// e4m3: 48 keys x 16 pieces of 16 codes, four per gather thread, kAhead chunks ahead
 constexpr int kCodeReps = kNK * (kHalf / 16) / kGatherThreads;
-constexpr uint32_t kRawScale = kCodeReps * kGatherThreads * 16;
-constexpr uint32_t kRawRope = kRawScale + kCodeReps * kGatherThreads * 4;
-constexpr uint32_t kRaw = kRawRope + kNK * (kHalfR / 8) * 16;
-constexpr int kRawStages = 4;
+constexpr int kAhead = 2;
 
-template <bool FP8>
-struct Layout {
-  static constexpr int kStages = FP8 ? 3 : 5;
-  static constexpr uint32_t kExchOff = kStages * kStage;
-  static constexpr uint32_t kRawOff = kExchOff + 2 * kExch;
-  static constexpr uint32_t kTailOff = kRawOff + (FP8 ? kRawStages * kRaw : 0);
-};
+constexpr int kStages = 5;
+constexpr uint32_t kExchOff = kStages * kStage;    // the peer's partial S of an even / odd chunk
+constexpr uint32_t kPOff = kExchOff + 2 * kExch;   // P of an even / odd chunk
+constexpr uint32_t kTailOff = kPOff + 2 * kPBuf;
+constexpr size_t kSmemMost = 232448;               // of a block
 
 struct Header {
   int item;    // tile
-  int c;       // chunk of the tile
+  int cf;      // 8 * (chunk of the tile) + 1: its first chunk here, 2: its last one here, 4: the
+               // whole tile is here
   int lim0;    // keys that the tile's first row sees (every cached key); unused with lists
-  int flags;   // 1: first chunk of the tile here, 2: last one here, 4: the whole tile is here
-  uint8_t valid[kGatherWarps];   // six keys each
+  uint32_t valid[2];   // the chunk's 48 keys: a byte from each gather warp
 };
 
 struct Tail {
-  Header hdr[5];
-  uint64_t kv_full[5], kv_empty[5];
-  uint64_t s_full[2], s_empty[2], p_full[2], x_full[2];
+  Header hdr[kStages];
+  uint64_t kv_full[kStages], kv_empty[kStages];
+  // by parity of the chunk; x_full / x_free (the peer's partial S is there / was read by the
+  // peer) and turn (the chunk has settled the running maximum) also by softmax warp
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
+  uint64_t x_full[2][4], x_free[2][4], turn[2][4];
   uint64_t q_full, o_free, drain;
+  float mref[128];            // running maximum of each row (raw logits)
+  float lsum[2][2][128];      // [parity][every second chunk of it]: the sum of its chunks so far
   uint32_t tmem_base;
   int abort_flag;
   long long sums[kThreads / 32];
   // this cluster's range: its first tile, that tile's first chunk here, chunks in all
   int item0, c0, n;
 };
+
+static_assert(kTailOff + sizeof(Tail) <= kSmemMost, "shared memory of a block");
 
 struct Params {
   LatentArgs a;
@@ -239,7 +250,15 @@ __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) 
   return ok != 0;
 }
 
-// mbar_wait for data that the peer CTA sends
+// Tells the peer that its data has been read. Relaxed: a release at cluster scope would wait for
+// everything this warp has in flight. `used` is worked out from the data, so the reads are over.
+__device__ __forceinline__ void arrive_peer(uint32_t bar, float used) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0]; // %1" ::"r"(bar),
+               "f"(used)
+               : "memory");
+}
+
+// mbar_wait for what the peer CTA sends
 __device__ __forceinline__ bool wait_peer(uint64_t* bar, uint32_t parity, volatile int* abort,
                                           int* err) {
   const uint32_t a = smem_u32(bar);
@@ -273,10 +292,6 @@ __device__ __forceinline__ float ex2f(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
@@ -327,9 +342,8 @@ __device__ __forceinline__ void enter_item(const Params& p, int item, Cursor& k)
 template <bool FP8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     latent_attn_kernel(const Params p) {
-  using L = Layout<FP8>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  Tail* tail = reinterpret_cast<Tail*>(smem + L::kTailOff);
+  Tail* tail = reinterpret_cast<Tail*>(smem + kTailOff);
   volatile int* abort_flag = &tail->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -342,25 +356,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < L::kStages; ++i) {
+    const int act_threads = 32 * p.act_warps;   // softmax threads of a chunk
+    for (int i = 0; i < kStages; ++i) {
       // every gather thread when its part has landed, and one per gather warp for the header
       mbar_init(&tail->kv_full[i], kGatherThreads + kGatherWarps);
       mbar_init(&tail->kv_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tail->s_full[i], 1);
-      mbar_init(&tail->s_empty[i], 1);
-      mbar_init(&tail->p_full[i], 128);
-      mbar_init(&tail->x_full[i], 1);
+      mbar_init(&tail->s_free[i], act_threads);
+      mbar_init(&tail->p_full[i], act_threads);
+      mbar_init(&tail->pv_done[i], 1);
+      for (int w = 0; w < 4; ++w) {
+        mbar_init(&tail->x_full[i][w], 1);
+        mbar_init(&tail->x_free[i][w], 1);
+        mbar_init(&tail->turn[i][w], 1);
+      }
     }
-    mbar_init(&tail->q_full, 128);
-    mbar_init(&tail->o_free, 128);
+    mbar_init(&tail->q_full, act_threads);
+    mbar_init(&tail->o_free, act_threads);
     mbar_init(&tail->drain, 1);
     tail->abort_flag = 0;
     tail->n = 0;
     fence_mbar_init();
   }
-  if (warp == 4) {
+  if (warp == kIssueWarp) {
     tmem_alloc(&tail->tmem_base, 512);
     tmem_relinquish();
   }
@@ -389,98 +409,112 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // nothing here (both CTAs agree)
   } else if (warp >= kGatherWarp0) {
     // ================================================================ gather
-    const int gw = warp - kGatherWarp0, gt = threadIdx.x - 32 * kGatherWarp0;
-    const int mykey = gw * kKeysPerWarp + lane;   // lanes 0-5: the chunk's key of this lane
-    const bool holder = lane < kKeysPerWarp;
+    const int gw = warp - kGatherWarp0;
+    const int mykey = gw * kKeysPerWarp + (lane & 7);
     const long long row_bytes = FP8 ? kDc + 16 + 2 * kDr : 2 * kD;
     Cursor k;
     enter_item(p, item0, k);
     k.c = c0;
-    int made = 0;   // chunks handed out by next()
-    // the lane's position in the next chunk (-1: no key), with the chunk's header
-    struct Ahead {
-      int pos, b, item, c, lim0, flags;
+    int made = 0;   // chunks handed out
+    // Three steps for the keys of four chunks, lane 8 i + j the warp's key j of the i-th of them:
+    // the chunk and its list entry, the page of its position, its slot.
+    struct Entry {
+      int raw, len, keys, b, item, cf, lim0;
     };
-    auto next = [&]() {
-      Ahead h;
-      h.pos = -1;
-      h.b = k.b;
-      h.item = k.item;
-      h.c = k.c;
-      h.flags = 0;
-      h.lim0 = 0;
-      if (made >= n) return h;
-      const bool first = made == 0 || k.c == 0;
-      const bool last = made == n - 1 || k.c == k.nch - 1;
-      h.flags = (first ? 1 : 0) | (last ? 2 : 0);
-      // the whole tile is in this range: its first chunk was here, and its last one is
-      if (k.c <= made && k.nch - k.c <= n - made) h.flags |= 4;
-      h.lim0 = k.len - p.a.Sq + 1 + (p.a.idx ? 0 : (k.mt * 128) / p.a.H);
-      if (holder) {
-        const int j = k.c * kNK + mykey;
-        if (p.a.idx) {
-          if (j < p.a.k) {
-            const int s = __ldg(p.a.idx + static_cast<long long>(k.item) * p.a.k + j);
-            if (s < -1 || s >= k.len)
-              report_error(err, kErrIdx);
-            else if (s < k.keys)
-              h.pos = s;
-          }
-        } else if (j < k.keys) {
-          h.pos = j;
+    struct Paged {
+      int page, pos, item, cf, lim0;
+    };
+    struct Slot {
+      int slot, item, cf, lim0;
+    };
+    auto look = [&]() {
+      Entry e = {-1, 0, 0, 0, 0, 0, 0};
+#pragma unroll 1
+      for (int i = 0; i < 4 && made < n; ++i) {
+        int cf = 8 * k.c + (made == 0 || k.c == 0 ? 1 : 0) +
+                 (made == n - 1 || k.c == k.nch - 1 ? 2 : 0);
+        // the whole tile is in this range: its first chunk was here, and its last one is
+        if (k.c <= made && k.nch - k.c <= n - made) cf += 4;
+        if ((lane >> 3) == i) {
+          e.len = k.len;
+          e.keys = k.keys;
+          e.b = k.b;
+          e.item = k.item;
+          e.cf = cf;
+          e.lim0 = k.len - p.a.Sq + 1 + (p.a.idx ? 0 : (k.mt * 128) / p.a.H);
+          const int j = k.c * kNK + mykey;
+          e.raw = j < (p.a.idx ? p.a.k : k.keys) ? j : -1;
+        }
+        ++made;
+        if (made < n && ++k.c == k.nch) {
+          enter_item(p, k.item + 1, k);
+          k.c = 0;
         }
       }
-      ++made;
-      if (made < n && ++k.c == k.nch) {
-        enter_item(p, k.item + 1, k);
-        k.c = 0;
-      }
-      return h;
+      if (p.a.idx && e.raw >= 0)
+        e.raw = __ldg(p.a.idx + static_cast<long long>(e.item) * p.a.k + e.raw);
+      return e;
     };
-    // the page of a position, then its slot
-    auto page_of = [&](const Ahead& h) {
-      return h.pos >= 0 ? __ldg(p.a.page_table + static_cast<long long>(h.b) * p.a.max_pages +
-                                h.pos / p.a.page_size)
-                        : -1;
-    };
-    auto slot_of = [&](const Ahead& h, int page) {
-      if (h.pos < 0) return -1;
-      if (page < 0 || page >= p.a.num_pages) {
-        report_error(err, kErrPage);
-        return -1;
+    auto page_of = [&](const Entry& e) {
+      Paged q = {-1, -1, e.item, e.cf, e.lim0};
+      if (e.raw < -1 || e.raw >= e.len) {
+        if (e.raw != -1) report_error(err, kErrIdx);
+      } else if (e.raw < e.keys) {
+        q.pos = e.raw;
       }
-      return page * p.a.page_size + h.pos % p.a.page_size;
+      if (q.pos >= 0)
+        q.page = __ldg(p.a.page_table + static_cast<long long>(e.b) * p.a.max_pages +
+                       q.pos / p.a.page_size);
+      return q;
+    };
+    auto slot_of = [&](const Paged& q) {
+      Slot r = {-1, q.item, q.cf, q.lim0};
+      if (q.pos >= 0) {
+        if (q.page < 0 || q.page >= p.a.num_pages)
+          report_error(err, kErrPage);
+        else
+          r.slot = q.page * p.a.page_size + q.pos % p.a.page_size;
+      }
+      return r;
+    };
+    Entry e0 = look();
+    Paged q0 = page_of(e0);
+    e0 = look();
+    Slot now = slot_of(q0);
+    q0 = page_of(e0);
+    e0 = look();
+    auto next_batch = [&]() {
+      now = slot_of(q0);
+      q0 = page_of(e0);
+      e0 = look();
     };
     const uint32_t base = smem_u32(smem);
-    Ahead h0 = next();
-    int page0 = page_of(h0);
-    Ahead h1 = next();
-    int slot = slot_of(h0, page0);
 
     if (!FP8) {
       for (int g = 0; g < n; ++g) {
-        const int page1 = page_of(h1);
-        const Ahead h2 = next();
-        const int st = g % L::kStages;
-        if (!__all_sync(0xffffffffu, mbar_wait(&tail->kv_empty[st], ((g / L::kStages) & 1) ^ 1u,
-                                               abort_flag, err, kErrTime)))
+        const int b8 = (g & 3) * 8;   // the lanes with this chunk's keys
+        if (b8 == 0 && g > 0) next_batch();
+        const int st = g % kStages;
+        const uint32_t par = ((g / kStages) & 1) ^ 1u;
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait(&tail->kv_empty[st], par, abort_flag, err, kErrTime)))
           break;
-        const uint32_t bal = __ballot_sync(0xffffffffu, holder && slot >= 0);
-        if (lane == 0) {
+        const uint32_t bal = __ballot_sync(0xffffffffu, now.slot >= 0);
+        if (lane == b8) {
           Header& h = tail->hdr[st];
-          h.valid[gw] = static_cast<uint8_t>(bal);
+          reinterpret_cast<uint8_t*>(h.valid)[gw] = static_cast<uint8_t>(bal >> b8);
           if (gw == 0) {
-            h.item = h0.item;
-            h.c = h0.c;
-            h.lim0 = h0.lim0;
-            h.flags = h0.flags;
+            h.item = now.item;
+            h.cf = now.cf;
+            h.lim0 = now.lim0;
           }
-          mbar_arrive(&tail->kv_full[st]);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tail->kv_full[st]);   // the header
         const uint32_t stage = base + st * kStage;
 #pragma unroll
         for (int i = 0; i < kKeysPerWarp; ++i) {
-          const int s = __shfl_sync(0xffffffffu, slot, i);
+          const int s = __shfl_sync(0xffffffffu, now.slot, b8 + i);
           const int key = gw * kKeysPerWarp + i;
           const uint8_t* src = p.a.cache + (s >= 0 ? s : 0) * row_bytes + rank * (2 * kHalf);
           cp_async_16(stage + (lane >> 3) * kAtom + key * 128 + (((lane & 7) ^ (key & 7)) << 4),
@@ -488,95 +522,83 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         {
           const int i = lane >> 2, pc = lane & 3;   // four pieces of positional dims per key
-          const int s = __shfl_sync(0xffffffffu, slot, i < kKeysPerWarp ? i : 0);
+          const int s = __shfl_sync(0xffffffffu, now.slot, b8 + i);
           const int key = gw * kKeysPerWarp + i;
           const uint8_t* src =
               p.a.cache + (s >= 0 ? s : 0) * row_bytes + 2 * kDc + rank * (2 * kHalfR);
-          if (i < kKeysPerWarp)
-            cp_async_16(stage + 4 * kAtom + key * 128 + ((pc ^ (key & 7)) << 4), src + pc * 16,
-                        s >= 0 ? 16u : 0u);
+          cp_async_16(stage + 4 * kAtom + key * 128 + ((pc ^ (key & 7)) << 4), src + pc * 16,
+                      s >= 0 ? 16u : 0u);
         }
+        // arrives, by the copy hardware, once this thread's copies have landed
         cp_async_mbar_arrive(&tail->kv_full[st]);
-        slot = slot_of(h1, page1);
-        h0 = h1;
-        h1 = h2;
       }
       cp_async_wait<0>();
     } else {
-      // raw ring: chunk g's codes, scales and positional dims in slots of this thread's own
-      const uint32_t raw = base + L::kRawOff;
-      auto fetch = [&](int g, int sl) {
-        const uint32_t rs = raw + (g % kRawStages) * kRaw;
+      // a chunk's codes, scales and positional dims on their way, with its header and key mask
+      struct Raw {
+        uint4 code[kCodeReps], rope;
+        uint32_t scale[kCodeReps], valid;
+        int item, cf, lim0;
+      };
+      auto fetch = [&](Raw& r, int g) {
+        const int b8 = (g & 3) * 8;   // the lanes with this chunk's keys
+        if (b8 == 0 && g > 0) next_batch();
+        r.item = __shfl_sync(0xffffffffu, now.item, b8);
+        r.cf = __shfl_sync(0xffffffffu, now.cf, b8);
+        r.lim0 = __shfl_sync(0xffffffffu, now.lim0, b8);
+        r.valid = __ballot_sync(0xffffffffu, now.slot >= 0) >> b8;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int j = 0; j < kCodeReps; ++j) {
           const int i = 2 * j + (lane >> 4), pc = lane & 15;   // two keys per instruction
-          const int s = __shfl_sync(0xffffffffu, sl, i);
-          const uint8_t* src = p.a.cache + (s >= 0 ? s : 0) * row_bytes;
-          const uint32_t at = static_cast<uint32_t>(j) * kGatherThreads + gt;
-          cp_async_16(rs + at * 16, src + rank * kHalf + pc * 16, s >= 0 ? 16u : 0u);
-          cp_async_4(rs + kRawScale + at * 4, src + kDc + (rank * 2 + (pc >> 3)) * 4);
-        }
-        const int i = lane >> 2, pc = lane & 3;
-        const int s = __shfl_sync(0xffffffffu, sl, i < kKeysPerWarp ? i : 0);
-        const uint8_t* src =
-            p.a.cache + (s >= 0 ? s : 0) * row_bytes + kDc + 16 + rank * (2 * kHalfR) + pc * 16;
-        if (i < kKeysPerWarp)
-          cp_async_16(rs + kRawRope + (gw * kKeysPerWarp * 4 + lane) * 16, src, s >= 0 ? 16u : 0u);
-        cp_async_commit();
-      };
-      // chunks fetched ahead: their headers and key masks wait in registers
-      Ahead hq[kRawStages - 1];
-      uint32_t vq[kRawStages - 1];
-#pragma unroll
-      for (int d = 0; d < kRawStages - 1; ++d) {
-        hq[d] = h0;
-        vq[d] = __ballot_sync(0xffffffffu, holder && slot >= 0);
-        if (d < n)
-          fetch(d, slot);
-        else
-          cp_async_commit();
-        const int page1 = page_of(h1);
-        const Ahead h2 = next();
-        slot = slot_of(h1, page1);
-        h0 = h1;
-        h1 = h2;
-      }
-      for (int g = 0; g < n; ++g) {
-        const int page1 = page_of(h1);
-        const Ahead h2 = next();
-        const uint32_t bal = __ballot_sync(0xffffffffu, holder && slot >= 0);
-        if (g + kRawStages - 1 < n)
-          fetch(g + kRawStages - 1, slot);
-        else
-          cp_async_commit();
-        const int st = g % L::kStages;
-        if (!__all_sync(0xffffffffu, mbar_wait(&tail->kv_empty[st], ((g / L::kStages) & 1) ^ 1u,
-                                               abort_flag, err, kErrTime)))
-          break;
-        if (lane == 0) {
-          Header& h = tail->hdr[st];
-          h.valid[gw] = static_cast<uint8_t>(vq[0]);
-          if (gw == 0) {
-            h.item = hq[0].item;
-            h.c = hq[0].c;
-            h.lim0 = hq[0].lim0;
-            h.flags = hq[0].flags;
+          const int sk = __shfl_sync(0xffffffffu, now.slot, b8 + i);
+          const uint8_t* src = p.a.cache + (sk >= 0 ? sk : 0) * row_bytes;
+          r.code[j] = zero;
+          r.scale[j] = 0x3f800000u;
+          if (sk >= 0) {
+            r.code[j] = __ldg(reinterpret_cast<const uint4*>(src + rank * kHalf) + pc);
+            r.scale[j] = __ldg(reinterpret_cast<const uint32_t*>(src + kDc) + rank * 2 + (pc >> 3));
           }
-          mbar_arrive(&tail->kv_full[st]);
         }
-        cp_async_wait<kRawStages - 1>();
-        const uint8_t* rs = smem + L::kRawOff + (g % kRawStages) * kRaw;
-        uint8_t* stage = smem + st * kStage;
+        const int i = lane >> 2, pc = lane & 3;   // four pieces of positional dims per key
+        const int sk = __shfl_sync(0xffffffffu, now.slot, b8 + i);
+        r.rope = zero;
+        if (sk >= 0)
+          r.rope = __ldg(reinterpret_cast<const uint4*>(p.a.cache + sk * row_bytes + kDc + 16 +
+                                                        rank * (2 * kHalfR)) + pc);
+      };
+      Raw raw[kAhead];
 #pragma unroll
-        for (int j = 0; j < kCodeReps; ++j) {
-          const int i = 2 * j + (lane >> 4), pc = lane & 15, key = gw * kKeysPerWarp + i;
-          const int at = j * kGatherThreads + gt;
-          const uint4 q = *reinterpret_cast<const uint4*>(rs + at * 16);
-          const uint32_t sc = *reinterpret_cast<const uint32_t*>(rs + kRawScale + at * 4);
-          uint4 w[2];
-          if ((vq[0] >> i) & 1u) {
+      for (int d = 0; d < kAhead; ++d) fetch(raw[d], d);
+      bool go = true;
+      for (int g0 = 0; go && g0 < n; g0 += kAhead) {
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) {
+          const int g = g0 + d;
+          if (!go || g >= n) break;
+          Raw& r = raw[d];
+          const int st = g % kStages;
+          if (!__all_sync(0xffffffffu, mbar_wait(&tail->kv_empty[st], ((g / kStages) & 1) ^ 1u,
+                                                 abort_flag, err, kErrTime))) {
+            go = false;
+            break;
+          }
+          if (lane == 0) {
+            Header& h = tail->hdr[st];
+            reinterpret_cast<uint8_t*>(h.valid)[gw] = static_cast<uint8_t>(r.valid);
+            if (gw == 0) {
+              h.item = r.item;
+              h.cf = r.cf;
+              h.lim0 = r.lim0;
+            }
+            mbar_arrive(&tail->kv_full[st]);
+          }
+          uint8_t* stage = smem + st * kStage;
+#pragma unroll
+          for (int j = 0; j < kCodeReps; ++j) {
+            const int pc = lane & 15, key = gw * kKeysPerWarp + 2 * j + (lane >> 4);
             // 2^k as bf16 bits; 2^(120 + k), or 2^127 and the rest of it
-            const uint32_t e = sc >> 16;
+            const uint32_t e = r.scale[j] >> 16;
             uint32_t up = e + (120u << 7), more = 0x3f80u;
             if (e > (134u << 7)) {   // k > 7, or NaN
               up = e > 0x7f80u ? e : 254u << 7;
@@ -584,77 +606,75 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             up |= up << 16;
             more |= more << 16;
-            widen4(q.x, up, more, w[0].x, w[0].y);
-            widen4(q.y, up, more, w[0].z, w[0].w);
-            widen4(q.z, up, more, w[1].x, w[1].y);
-            widen4(q.w, up, more, w[1].z, w[1].w);
-          } else {
-            w[0] = w[1] = make_uint4(0, 0, 0, 0);
+            uint4 w[2];
+            widen4(r.code[j].x, up, more, w[0].x, w[0].y);
+            widen4(r.code[j].y, up, more, w[0].z, w[0].w);
+            widen4(r.code[j].z, up, more, w[1].x, w[1].y);
+            widen4(r.code[j].w, up, more, w[1].z, w[1].w);
+            // the two 16-byte halves, in the other order in every second atom: eight lanes then
+            // store to eight different bank groups
+            uint8_t* row = stage + (pc >> 2) * kAtom + key * 128;
+            const int sw = (pc >> 2) & 1, c = (pc & 3) * 2;
+            *reinterpret_cast<uint4*>(row + (((c + sw) ^ (key & 7)) << 4)) = sw ? w[1] : w[0];
+            *reinterpret_cast<uint4*>(row + (((c + 1 - sw) ^ (key & 7)) << 4)) = sw ? w[0] : w[1];
           }
-          // the two 16-byte halves, in the other order in every second atom: eight lanes then
-          // store to eight different bank groups
-          uint8_t* row = stage + (pc >> 2) * kAtom + key * 128;
-          const int sw = (pc >> 2) & 1, c = (pc & 3) * 2;
-          *reinterpret_cast<uint4*>(row + (((c + sw) ^ (key & 7)) << 4)) = sw ? w[1] : w[0];
-          *reinterpret_cast<uint4*>(row + (((c + 1 - sw) ^ (key & 7)) << 4)) = sw ? w[0] : w[1];
+          {
+            const int key = gw * kKeysPerWarp + (lane >> 2), pc = lane & 3;
+            *reinterpret_cast<uint4*>(stage + 4 * kAtom + key * 128 + ((pc ^ (key & 7)) << 4)) =
+                r.rope;
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&tail->kv_full[st]);
+          fetch(r, g + kAhead);   // no keys behind the end
         }
-        if (lane < 4 * kKeysPerWarp) {
-          const int key = gw * kKeysPerWarp + (lane >> 2), pc = lane & 3;
-          *reinterpret_cast<uint4*>(stage + 4 * kAtom + key * 128 + ((pc ^ (key & 7)) << 4)) =
-              *reinterpret_cast<const uint4*>(rs + kRawRope + (gw * kKeysPerWarp * 4 + lane) * 16);
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(&tail->kv_full[st]);
-        slot = slot_of(h1, page1);
-#pragma unroll
-        for (int d = 0; d + 1 < kRawStages - 1; ++d) {
-          hq[d] = hq[d + 1];
-          vq[d] = vq[d + 1];
-        }
-        hq[kRawStages - 2] = h0;
-        vq[kRawStages - 2] = bal;
-        h0 = h1;
-        h1 = h2;
       }
-      cp_async_wait<0>();
     }
-  } else if (warp == 4) {
+  } else if (warp == kIssueWarp) {
     // ================================================================ UMMA issuer
     if (lane == 0) {
       constexpr uint32_t idesc_s = umma_idesc_bf16_mn(128, kNK, false);
       constexpr uint32_t idesc_pv = umma_idesc_bf16_mn(128, kHalf, true);
       const uint32_t base = smem_u32(smem);
       uint32_t q_par = 0, of_par = 1;
-      int pend_flags = 0;
-      // PV of chunk g (its P is awaited here)
-      auto pv = [&](int g, int flags) {
-        const int sb = g & 1, st = g % L::kStages;
+      int done = 0;          // chunks whose P V has been issued
+      uint32_t firsts = 0;   // bit g % 32: chunk g is the first of its tile here
+      // P V of the next chunk (its P is awaited here)
+      auto pv = [&]() {
+        const int g = done, sb = g & 1, st = g % kStages;
+        const bool first = (firsts >> (g & 31)) & 1u;
         if (!mbar_wait(&tail->p_full[sb], (g >> 1) & 1, abort_flag, err, kErrTime)) return false;
-        if (flags & 1) {   // the previous tile's O has been read out
+        if (first) {   // the previous tile's O has been read out
           if (!mbar_wait(&tail->o_free, of_par, abort_flag, err, kErrTime)) return false;
           of_par ^= 1u;
         }
         tc_fence_after();
+        const uint64_t p0 = umma_sdesc(base + kPOff + sb * kPBuf, 256, kLayoutSw32);
         const uint64_t v0 = umma_sdesc_lbo(base + st * kStage, kAtom, 1024, kLayoutSw128);
 #pragma unroll
         for (int ks = 0; ks < kNK / 16; ++ks)
-          umma_bf16_ts(tmem + kColO, tmem + kColS + sb * kNK + ks * 8, umma_desc_adv(v0, ks * 2048),
-                       idesc_pv, ((flags & 1) && ks == 0) ? 0u : 1u);
+          umma_bf16(tmem + kColO, umma_desc_adv(p0, ks * kPTile), umma_desc_adv(v0, ks * 2048),
+                    idesc_pv, (first && ks == 0) ? 0u : 1u);
         umma_commit(&tail->kv_empty[st]);
-        umma_commit(&tail->s_empty[sb]);
+        umma_commit(&tail->pv_done[sb]);
+        ++done;
         return true;
       };
-      for (int g = 0; g < n; ++g) {
-        const int st = g % L::kStages, sb = g & 1;
-        if (!mbar_wait(&tail->kv_full[st], (g / L::kStages) & 1, abort_flag, err, kErrTime)) break;
-        const int flags = tail->hdr[st].flags;
-        if (flags & 1) {
-          if (!mbar_wait(&tail->q_full, q_par, abort_flag, err, kErrTime)) break;
+      bool ok = true;
+      for (int g = 0; ok && g < n; ++g) {
+        const int st = g % kStages, sb = g & 1;
+        ok = mbar_wait(&tail->kv_full[st], (g / kStages) & 1, abort_flag, err, kErrTime);
+        if (!ok) break;
+        const bool first = (tail->hdr[st].cf & 1) != 0;
+        firsts = first ? firsts | (1u << (g & 31)) : firsts & ~(1u << (g & 31));
+        if (first) {
+          // Q comes once the previous tile's last P is out, which may wait for the P V before it
+          while (ok && done < g) ok = pv();
+          ok = ok && mbar_wait(&tail->q_full, q_par, abort_flag, err, kErrTime);
           q_par ^= 1u;
         }
-        if (!mbar_wait(&tail->s_empty[sb], ((g >> 1) & 1) ^ 1u, abort_flag, err, kErrTime)) break;
-        // cp.async wrote the rows through the generic proxy
-        fence_proxy_async_smem();
+        ok = ok && mbar_wait(&tail->s_free[sb], ((g >> 1) & 1) ^ 1u, abort_flag, err, kErrTime);
+        if (!ok) break;
+        if (!FP8) fence_proxy_async_smem();   // cp.async wrote the rows through the generic proxy
         tc_fence_after();
         const uint64_t k0 = umma_sdesc(base + st * kStage, 1024, kLayoutSw128);
 #pragma unroll
@@ -663,11 +683,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                        umma_desc_adv(k0, (kk >> 2) * kAtom + (kk & 3) * 32), idesc_s,
                        kk > 0 ? 1u : 0u);
         umma_commit(&tail->s_full[sb]);
-        if (g > 0 && !(pend_flags & 2) && !pv(g - 1, pend_flags)) break;
-        // a tile's last chunk: its PV right away, so that O is complete before the next tile
-        if ((flags & 2) && !pv(g, flags)) break;
-        pend_flags = flags;
+        while (ok && done < g - 1) ok = pv();
       }
+      while (ok && done < n) ok = pv();
       umma_commit(&tail->drain);
       const uint32_t a = smem_u32(&tail->drain);
       const unsigned long long t0 = globaltimer_ns();
@@ -678,15 +696,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else {
+  } else if ((warp & 3) < p.act_warps) {
     // ================================================================ softmax / output
-    const int hrow = threadIdx.x;   // TMEM lane = row of the tile
-    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
-    const bool act = warp < p.act_warps;
+    // (a warp whose 32 rows no tile has takes no part: its lanes of S and O hold anything)
+    const int wg = warp >> 2, quarter = warp & 3;   // chunks wg, wg + 2, ...; TMEM lanes
+    const int hrow = threadIdx.x & 127;             // TMEM lane = row of the tile
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const float c2 = p.scale_log2;
     const int H = p.a.H;
     const uint32_t peer = rank ^ 1u;
-    const uint32_t x_bytes = p.act_warps * 32 * kNK * 4;
     // the tile's first row of Q / O / lse, and the rows it has
     auto rows_at = [&](int item, int& rows) {
       if (p.a.idx) {
@@ -699,50 +717,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     // this CTA's dims of the row of Q, packed bf16 pairs, into the thread's TMEM lane
     auto load_q = [&](int item) {
-      if (act) {
-        int rows;
-        const long long r0 = rows_at(item, rows);
-        const bool in = hrow < rows;
-        const uint4* src = reinterpret_cast<const uint4*>(p.a.Q + (in ? r0 + hrow : 0) * kD);
-        const uint4 zero = make_uint4(0, 0, 0, 0);
+      int rows;
+      const long long r0 = rows_at(item, rows);
+      const bool in = hrow < rows;
+      const uint4* src = reinterpret_cast<const uint4*>(p.a.Q + (in ? r0 + hrow : 0) * kD);
+      const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int a = 0; a < kSteps / 2; ++a) {   // 32 dims: 16 columns
-          uint32_t w[16];
+      for (int a = 0; a < kSteps / 2; ++a) {   // 32 dims: 16 columns
+        uint32_t w[16];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int at = a < kHalf / 32 ? rank * (kHalf / 8) + a * 4 + q
-                                          : kDc / 8 + rank * (kHalfR / 8) + q;
-            const uint4 x = in ? __ldg(src + at) : zero;
-            w[4 * q] = x.x; w[4 * q + 1] = x.y; w[4 * q + 2] = x.z; w[4 * q + 3] = x.w;
-          }
-          tmem_st_x16(tmem + lane_off + kColQ + a * 16, w);
+        for (int q = 0; q < 4; ++q) {
+          const int at = a < kHalf / 32 ? rank * (kHalf / 8) + a * 4 + q
+                                        : kDc / 8 + rank * (kHalfR / 8) + q;
+          const uint4 x = in ? __ldg(src + at) : zero;
+          w[4 * q] = x.x; w[4 * q + 1] = x.y; w[4 * q + 2] = x.z; w[4 * q + 3] = x.w;
         }
-        tmem_st_wait();
+        tmem_st_x16(tmem + lane_off + kColQ + a * 16, w);
       }
+      tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&tail->q_full);
     };
 
-    load_q(item0);
-    float m = -INFINITY, l = 0.f;   // running max (raw logits) and sum
-    int rows = 0, lim = 0;
+    if (wg == 0) load_q(item0);
+    const uint32_t sbase = tmem + lane_off + kColS + wg * kNK;
+    const uint32_t xb = smem_u32(smem + kExchOff + wg * kExch) + hrow * 16;
+    const uint32_t x_dst = peer_addr(xb, peer);
+    const uint32_t x_bar = peer_addr(smem_u32(&tail->x_full[wg][quarter]), peer);
+    const uint32_t x_ack = peer_addr(smem_u32(&tail->x_free[wg][quarter]), peer);
+    const float4* xr = reinterpret_cast<const float4*>(smem + kExchOff + wg * kExch) + hrow;
+    // P: this row's 32 bytes of each k-step's tile, 32B-swizzled
+    uint8_t* prow_s = smem + kPOff + wg * kPBuf + hrow * 32;
+    const int psw = ((hrow >> 2) & 1) << 4;
+
+    float m = -INFINITY, l = 0.f;   // the running max last seen (raw logits), own chunks' sum
+    int rows = 0, lim = 0, cur = -1;
     long long r0 = 0;
-    for (int g = 0; g < n; ++g) {
-      const int sb = g & 1, st = g % L::kStages;
+    for (int g = wg; g < n; g += 2) {
+      const int st = g % kStages;
       const uint32_t par = (g >> 1) & 1;
-      if (threadIdx.x == 0) mbar_arrive_expect_tx(&tail->x_full[sb], x_bytes);
-      bool ok = mbar_wait(&tail->s_full[sb], par, abort_flag, err, kErrTime);
+      if (lane == 0) mbar_arrive_expect_tx(&tail->x_full[wg][quarter], 32 * kNK * 4);
+      bool ok = mbar_wait(&tail->s_full[wg], par, abort_flag, err, kErrTime);
       // acquires the gather warps' header writes
-      ok = ok && mbar_wait(&tail->kv_full[st], (g / L::kStages) & 1, abort_flag, err, kErrTime);
+      ok = ok && mbar_wait(&tail->kv_full[st], (g / kStages) & 1, abort_flag, err, kErrTime);
+      // the peer has read what was sent two chunks ago
+      ok = ok && wait_peer(&tail->x_free[wg][quarter], par ^ 1u, abort_flag, err);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      const Header& h = tail->hdr[st];
-      const int item = h.item, flags = h.flags, c = h.c;
-      unsigned long long vm = 0;
+      float s[kNK];
+      uint32_t lo[32], hi[16];
+      tmem_ld_x32(sbase, lo);
+      tmem_ld_16(sbase + 32, hi);
+      tmem_ld_wait();
+      tc_fence_before();
 #pragma unroll
-      for (int w = 0; w < kGatherWarps; ++w)
-        vm |= static_cast<unsigned long long>(h.valid[w]) << (w * kKeysPerWarp);
-      if (flags & 1) {
+      for (int j = 0; j < 32; j += 4)
+        st_peer(x_dst + j * 512, x_bar, lo[j], lo[j + 1], lo[j + 2], lo[j + 3]);
+#pragma unroll
+      for (int j = 0; j < 16; j += 4)
+        st_peer(x_dst + (32 + j) * 512, x_bar, hi[j], hi[j + 1], hi[j + 2], hi[j + 3]);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) s[j] = __uint_as_float(lo[j]);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) s[32 + j] = __uint_as_float(hi[j]);
+      mbar_arrive(&tail->s_free[wg]);
+      const Header& h = tail->hdr[st];
+      const int item = h.item, flags = h.cf & 7, c = h.cf >> 3;
+      unsigned long long vm =
+          h.valid[0] | static_cast<unsigned long long>(h.valid[1] & 0xffffu) << 32;
+      if (item != cur) {
+        cur = item;
         m = -INFINITY;
         l = 0.f;
         r0 = rows_at(item, rows);
@@ -753,62 +797,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int left = lim - c * kNK;   // keys of the chunk that the row sees
         if (left < kNK) vm = left <= 0 ? 0ull : vm & ((1ull << left) - 1);
       }
-      if (act) {
-        const uint32_t sbase = tmem + lane_off + kColS + sb * kNK;
-        float s[kNK];
-        {
-          uint32_t lo[32], hi[16];
-          tmem_ld_x32(sbase, lo);
-          tmem_ld_16(sbase + 32, hi);
-          tmem_ld_wait();
+      if (!__all_sync(0xffffffffu,
+                      wait_peer(&tail->x_full[wg][quarter], par, abort_flag, err)))
+        break;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) s[j] = __uint_as_float(lo[j]);
+      for (int j = 0; j < kNK / 4; ++j) {
+        const float4 x = xr[j * 128];
+        s[4 * j] += x.x;
+        s[4 * j + 1] += x.y;
+        s[4 * j + 2] += x.z;
+        s[4 * j + 3] += x.w;
+      }
+      const bool all = vm == (1ull << kNK) - 1;
+      if (!all) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) s[32 + j] = __uint_as_float(hi[j]);
-        }
-        // partial sums to the peer, and the peer's
-        {
-          const uint32_t xb = smem_u32(smem + L::kExchOff + sb * kExch) + hrow * 16;
-          const uint32_t dst = peer_addr(xb, peer);
-          const uint32_t bar = peer_addr(smem_u32(&tail->x_full[sb]), peer);
+        for (int j = 0; j < kNK; ++j) s[j] = ((vm >> j) & 1u) ? s[j] : -INFINITY;
+      }
+      float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int j = 0; j < kNK / 4; ++j)
-            st_peer(dst + j * 2048, bar, __float_as_uint(s[4 * j]), __float_as_uint(s[4 * j + 1]),
-                    __float_as_uint(s[4 * j + 2]), __float_as_uint(s[4 * j + 3]));
-        }
-        if (!__all_sync(0xffffffffu, wait_peer(&tail->x_full[sb], par, abort_flag, err))) break;
-        const float4* xr =
-            reinterpret_cast<const float4*>(smem + L::kExchOff + sb * kExch) + hrow;
-        float mx = -INFINITY;
-        const bool all = vm == (1ull << kNK) - 1;
-#pragma unroll
-        for (int j = 0; j < kNK / 4; ++j) {
-          const float4 x = xr[j * 128];
-          s[4 * j] += x.x;
-          s[4 * j + 1] += x.y;
-          s[4 * j + 2] += x.z;
-          s[4 * j + 3] += x.w;
-        }
-        if (all) {
-#pragma unroll
-          for (int j = 0; j < kNK; ++j) mx = fmaxf(mx, s[j]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < kNK; ++j)
-            if ((vm >> j) & 1u) mx = fmaxf(mx, s[j]);
-        }
-        if (flags & 1) {
-          m = mx;
-        } else if (__any_sync(0xffffffffu,
-                              mx > m && (m == -INFINITY || (mx - m) * c2 > kRescaleLog2))) {
-          // refresh the warp's running maxima: rescale O (every earlier PV is done) and l
+      for (int j = 4; j < kNK; ++j) m4[j & 3] = fmaxf(m4[j & 3], s[j]);
+      const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+      __syncwarp();
+      if (lane == 0) arrive_peer(x_ack, mx);
+
+      // in the order of the chunks: the running maximum
+      if (g > 0 && !__all_sync(0xffffffffu, mbar_wait(&tail->turn[wg ^ 1][quarter],
+                                                      ((g - 1) >> 1) & 1, abort_flag, err,
+                                                      kErrTime)))
+        break;
+      float mn = mx, mr = -INFINITY;
+      if (!(flags & 1)) {
+        mr = tail->mref[hrow];
+        mn = mr;
+        if (__any_sync(0xffffffffu,
+                       mx > mr && (mr == -INFINITY || (mx - mr) * c2 > kRescaleLog2))) {
+          // refresh the warp's running maxima: rescale O (once every earlier P V is done)
           const int pg = g - 1;
-          if (!__all_sync(0xffffffffu, mbar_wait(&tail->s_empty[pg & 1], (pg >> 1) & 1, abort_flag,
-                                                 err, kErrTime)))
+          if (!__all_sync(0xffffffffu, mbar_wait(&tail->pv_done[pg & 1], (pg >> 1) & 1,
+                                                 abort_flag, err, kErrTime)))
             break;
           tc_fence_after();
-          const float mnew = fmaxf(m, mx);
-          const float f = m == -INFINITY ? 0.f : exp2f((m - mnew) * c2);
+          mn = fmaxf(mr, mx);
+          const float f = mr == -INFINITY ? 0.f : exp2f((mr - mn) * c2);
 #pragma unroll 1
           for (int d0 = 0; d0 < kHalf; d0 += 16) {
             uint32_t ov[16];
@@ -819,91 +849,104 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tmem_st_x16(tmem + lane_off + kColO + d0, ov);
           }
           tmem_st_wait();
-          l *= f;
-          m = mnew;
         }
-        // P = exp2(S*c2 - m*c2) over the valid keys, bf16 pairs in the S buffer's first columns
-        const float base = m == -INFINITY ? 0.f : m * c2;
-        float ls = 0.f;
-#pragma unroll
-        for (int part = 0; part < 3; ++part) {
-          uint32_t pk[8];
-#pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const int jj = part * 16 + j;
-            float e0 = ex2f(fmaf(s[jj], c2, -base));
-            float e1 = ex2f(fmaf(s[jj + 1], c2, -base));
-            if (!all) {
-              e0 = ((vm >> jj) & 1u) ? e0 : 0.f;
-              e1 = ((vm >> (jj + 1)) & 1u) ? e1 : 0.f;
-            }
-            ls += e0 + e1;
-            pk[j >> 1] = pack_bf16(e0, e1);
-          }
-          asm volatile(
-              "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
-                  sbase + part * 8),
-              "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3]), "r"(pk[4]), "r"(pk[5]), "r"(pk[6]),
-              "r"(pk[7])
-              : "memory");
-        }
-        tmem_st_wait();
-        l += ls;
+      }
+      tail->mref[hrow] = mn;
+      float other = 0.f;
+      if ((flags & 3) == 2) {
+        // the tile ends here: the other warps' sum, from their chunk before this one (scaled by
+        // the maximum of then, mr). It is awaited before the turn passes on, since their next
+        // chunk takes the barrier further.
+        if (!__all_sync(0xffffffffu, mbar_wait(&tail->p_full[wg ^ 1], ((g - 1) >> 1) & 1,
+                                               abort_flag, err, kErrTime)))
+          break;
+        other = tail->lsum[wg ^ 1][((g - 1) >> 1) & 1][hrow];
+        if (mr != -INFINITY) other *= exp2f((mr - mn) * c2);
       }
       tc_fence_before();
-      mbar_arrive(&tail->p_full[sb]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&tail->turn[wg][quarter]);
+      if (m != mn) {
+        l *= m == -INFINITY ? 0.f : exp2f((m - mn) * c2);
+        m = mn;
+      }
+      // the P buffer's previous chunk has gone through the tensor cores
+      if (g >= 2 && !__all_sync(0xffffffffu, mbar_wait(&tail->pv_done[wg], par ^ 1u, abort_flag,
+                                                       err, kErrTime)))
+        break;
+      // P = exp2(S*c2 - m*c2) over the valid keys (exp2(-inf) = 0 elsewhere)
+      const float base = m == -INFINITY ? 0.f : m * c2;
+      float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int t = 0; t < kNK / 16; ++t) {
+        uint32_t pk[8];
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+          const float e0 = ex2f(fmaf(s[t * 16 + j], c2, -base));
+          const float e1 = ex2f(fmaf(s[t * 16 + j + 1], c2, -base));
+          ls[j & 2] += e0;
+          ls[(j & 2) + 1] += e1;
+          pk[j >> 1] = pack_bf16(e0, e1);
+        }
+        uint8_t* dst = prow_s + t * kPTile;
+        *reinterpret_cast<uint4*>(dst + psw) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        *reinterpret_cast<uint4*>(dst + (psw ^ 16)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+      }
+      l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+      tail->lsum[wg][par][hrow] = l;
+      l += other;
+      fence_proxy_async_smem();
+      mbar_arrive(&tail->p_full[wg]);
       if (!(flags & 2)) continue;
 
       // the tile's last chunk here: every S of it is done, the next tile's Q may replace its own
       if (g + 1 < n) load_q(item + 1);
-      if (act) {
-        if (!__all_sync(0xffffffffu,
-                        mbar_wait(&tail->s_empty[sb], par, abort_flag, err, kErrTime)))
-          break;
-        tc_fence_after();
-        const long long row = r0 + hrow;
-        if (flags & 4) {
-          const float inv = l == 0.f ? 0.f : 1.f / l;   // NaN stays NaN
-          uint4* out = reinterpret_cast<uint4*>(p.a.O + row * kDc + rank * kHalf);
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait(&tail->pv_done[wg], par, abort_flag, err, kErrTime)))
+        break;
+      tc_fence_after();
+      const long long row = r0 + hrow;
+      if (flags & 4) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;   // NaN stays NaN
+        uint4* out = reinterpret_cast<uint4*>(p.a.O + row * kDc + rank * kHalf);
 #pragma unroll 1
-          for (int d0 = 0; d0 < kHalf; d0 += 32) {
-            uint32_t ov[32];
-            tmem_ld_x32(tmem + lane_off + kColO + d0, ov);
-            tmem_ld_wait();
-            if (hrow < rows) {
+        for (int d0 = 0; d0 < kHalf; d0 += 32) {
+          uint32_t ov[32];
+          tmem_ld_x32(tmem + lane_off + kColO + d0, ov);
+          tmem_ld_wait();
+          if (hrow < rows) {
 #pragma unroll
-              for (int d = 0; d < 32; d += 8) {
-                uint4 w;
-                w.x = pack_bf16(__uint_as_float(ov[d]) * inv, __uint_as_float(ov[d + 1]) * inv);
-                w.y = pack_bf16(__uint_as_float(ov[d + 2]) * inv, __uint_as_float(ov[d + 3]) * inv);
-                w.z = pack_bf16(__uint_as_float(ov[d + 4]) * inv, __uint_as_float(ov[d + 5]) * inv);
-                w.w = pack_bf16(__uint_as_float(ov[d + 6]) * inv, __uint_as_float(ov[d + 7]) * inv);
-                out[(d0 + d) / 8] = w;
-              }
+            for (int d = 0; d < 32; d += 8) {
+              uint4 w;
+              w.x = pack_bf16(__uint_as_float(ov[d]) * inv, __uint_as_float(ov[d + 1]) * inv);
+              w.y = pack_bf16(__uint_as_float(ov[d + 2]) * inv, __uint_as_float(ov[d + 3]) * inv);
+              w.z = pack_bf16(__uint_as_float(ov[d + 4]) * inv, __uint_as_float(ov[d + 5]) * inv);
+              w.w = pack_bf16(__uint_as_float(ov[d + 6]) * inv, __uint_as_float(ov[d + 7]) * inv);
+              out[(d0 + d) / 8] = w;
             }
           }
-          if (rank == 0 && hrow < rows)
-            p.a.lse[row] = l == 0.f ? -INFINITY : (m * c2 + log2f(l)) * 0.69314718055994530942f;
-        } else {
-          // part 0 of this cluster: a tile begun before its range; part 1: one that goes on behind
-          const int part = 2 * cluster + (item == item0 && c0 > 0 ? 0 : 1);
-          float4* out = p.part + static_cast<long long>(part) * (kDc / 4) * p.prow +
-                        static_cast<long long>(rank * (kHalf / 4)) * p.prow + hrow;
-#pragma unroll 1
-          for (int d0 = 0; d0 < kHalf; d0 += 32) {
-            uint32_t ov[32];
-            tmem_ld_x32(tmem + lane_off + kColO + d0, ov);
-            tmem_ld_wait();
-#pragma unroll
-            for (int d = 0; d < 32; d += 4)
-              out[static_cast<long long>((d0 + d) / 4) * p.prow] =
-                  make_float4(__uint_as_float(ov[d]), __uint_as_float(ov[d + 1]),
-                              __uint_as_float(ov[d + 2]), __uint_as_float(ov[d + 3]));
-          }
-          if (rank == 0)
-            p.ml[static_cast<long long>(part) * p.prow + hrow] =
-                make_float2(m == -INFINITY ? -INFINITY : m * c2, l);
         }
+        if (rank == 0 && hrow < rows)
+          p.a.lse[row] = l == 0.f ? -INFINITY : (m * c2 + log2f(l)) * 0.69314718055994530942f;
+      } else {
+        // part 0 of this cluster: a tile begun before its range; part 1: one that goes on behind
+        const int part = 2 * cluster + (item == item0 && c0 > 0 ? 0 : 1);
+        float4* out = p.part + static_cast<long long>(part) * (kDc / 4) * p.prow +
+                      static_cast<long long>(rank * (kHalf / 4)) * p.prow + hrow;
+#pragma unroll 1
+        for (int d0 = 0; d0 < kHalf; d0 += 32) {
+          uint32_t ov[32];
+          tmem_ld_x32(tmem + lane_off + kColO + d0, ov);
+          tmem_ld_wait();
+#pragma unroll
+          for (int d = 0; d < 32; d += 4)
+            out[static_cast<long long>((d0 + d) / 4) * p.prow] =
+                make_float4(__uint_as_float(ov[d]), __uint_as_float(ov[d + 1]),
+                            __uint_as_float(ov[d + 2]), __uint_as_float(ov[d + 3]));
+        }
+        if (rank == 0)
+          p.ml[static_cast<long long>(part) * p.prow + hrow] =
+              make_float2(m == -INFINITY ? -INFINITY : m * c2, l);
       }
       tc_fence_before();
       mbar_arrive(&tail->o_free);
@@ -919,7 +962,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 4) tmem_dealloc(tmem, 512);
+  if (warp == kIssueWarp) tmem_dealloc(tmem, 512);
   cluster_sync_all();   // no CTA leaves while its peer may still write to it
 }
 
@@ -1025,7 +1068,7 @@ int resident_clusters(size_t smem) {
 
 template <bool FP8>
 int launch(Params p, cudaStream_t stream) {
-  const size_t smem = Layout<FP8>::kTailOff + sizeof(Tail);
+  const size_t smem = kTailOff + sizeof(Tail);
   if (cudaFuncSetAttribute(latent_attn_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem)) != cudaSuccess)
     return DSA_ERR_CUDA;
