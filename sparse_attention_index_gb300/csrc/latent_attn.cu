@@ -21,19 +21,21 @@
 // one range is written out there; the others leave (O, m, l) in the workspace and
 // latent_join_kernel adds them up. Lengths are read on the device only.
 //
-// Warp-specialised CTA, 480 threads (four warps a scheduler at most: 128 registers each):
+// Warp-specialised CTA, 512 threads (four warps a scheduler, 128 registers a thread):
 //   warps 0-7   softmax / output, one (token, head) row per thread: warps 0-3 the even chunks,
 //               warps 4-7 the odd ones. A chunk's way through a softmax warp is a chain of
 //               latencies (S out of TMEM, the peer's half of it, the exponentials), about three
 //               times what its products take, so two of them run side by side. They share the
 //               running maximum, which passes from chunk to chunk in order; each keeps the sum
 //               of its own chunks.
-//   warp  8     TMEM owner and single-thread UMMA issuer; S runs two chunks ahead of P V
-//   warps 9-14  gather, eight keys of each chunk per warp: the slots of four chunks are looked up
+//   warps 8, 9  single-thread UMMA issuers, one for S and one for P V: the waits and commits of
+//               a single one took as long as the products (18 of them for S, and one with few
+//               columns takes 45 cycles whatever they are). Warp 8 owns TMEM.
+//   warps 10-15 gather, eight keys of each chunk per warp: the slots of four chunks are looked up
 //               at once, one key per lane, a batch ahead for the page and two for the list entry;
-//               then 16-byte cp.async into 128B-swizzled tiles. e4m3 rows are loaded into
-//               registers two chunks ahead and widened to bf16, exactly, since their scales are
-//               powers of two.
+//               then 16-byte cp.async into 128B-swizzled tiles. e4m3 rows go through a raw ring
+//               two chunks ahead and are widened to bf16, exactly, since their scales are powers
+//               of two.
 // P goes to the tensor cores through shared memory, so that a chunk's S columns are free again
 // once they have been read. TMEM: [Q: 144][S: 2 x 48][pad 16][O: 256] = 512 columns.
 
@@ -56,8 +58,8 @@ constexpr uint32_t kStage = kAtoms * kAtom;
 constexpr uint32_t kExch = 128 * kNK * 4;   // one buffer of the peer's partial S
 constexpr uint32_t kPTile = 128 * 32;       // P of 16 keys: one k-step of P V
 constexpr uint32_t kPBuf = kNK / 16 * kPTile;
-constexpr int kIssueWarp = 8;
-constexpr int kGatherWarp0 = 9, kGatherWarps = 6;
+constexpr int kIssueWarp = 8, kIssuePvWarp = 9;
+constexpr int kGatherWarp0 = 10, kGatherWarps = 6;
 constexpr int kGatherThreads = 32 * kGatherWarps;
 constexpr int kKeysPerWarp = kNK / kGatherWarps;
 constexpr int kThreads = 32 * (kGatherWarp0 + kGatherWarps);
@@ -70,15 +72,25 @@ constexpr int kErrPage = DSA_STAGE_LATENT | DSA_DEVERR_BAD_PAGE;
 constexpr int kErrTime = DSA_STAGE_LATENT | DSA_DEVERR_TIMEOUT;
 static_assert(kKeysPerWarp == 8, "the keys of a gather warp are one byte of the chunk's mask");
 
-// e4m3: 48 keys x 16 pieces of 16 codes, four per gather thread, kAhead chunks ahead
+// e4m3: 48 keys x 16 pieces of 16 codes and 48 x 4 of positional dims, four and one per gather
+// thread, and two scales per key, in a ring of raw chunks
 constexpr int kCodeReps = kNK * (kHalf / 16) / kGatherThreads;
+constexpr uint32_t kRawRope = kCodeReps * kGatherThreads * 16;
+constexpr uint32_t kRawScale = kRawRope + kGatherThreads * 16;
+constexpr uint32_t kRaw = kRawScale + kNK * 8;
 constexpr int kAhead = 2;
+static_assert(kNK * (kHalfR / 8) == kGatherThreads, "one piece of positional dims per thread");
 
-constexpr int kStages = 5;
-constexpr uint32_t kExchOff = kStages * kStage;    // the peer's partial S of an even / odd chunk
-constexpr uint32_t kPOff = kExchOff + 2 * kExch;   // P of an even / odd chunk
-constexpr uint32_t kTailOff = kPOff + 2 * kPBuf;
-constexpr size_t kSmemMost = 232448;               // of a block
+template <bool FP8>
+struct Layout {
+  static constexpr int kStages = FP8 ? 4 : 5;
+  static constexpr uint32_t kExchOff = kStages * kStage;   // the peer's S of an even / odd chunk
+  static constexpr uint32_t kPOff = kExchOff + 2 * kExch;  // P of an even / odd chunk
+  static constexpr uint32_t kRawOff = kPOff + 2 * kPBuf;
+  static constexpr uint32_t kTailOff = kRawOff + (FP8 ? kAhead * kRaw : 0);
+};
+constexpr int kMaxStages = 5;
+constexpr size_t kSmemMost = 232448;   // of a block
 
 struct Header {
   int item;    // tile
@@ -89,13 +101,13 @@ struct Header {
 };
 
 struct Tail {
-  Header hdr[kStages];
-  uint64_t kv_full[kStages], kv_empty[kStages];
+  Header hdr[kMaxStages];
+  uint64_t kv_full[kMaxStages], kv_empty[kMaxStages];
   // by parity of the chunk; x_full / x_free (the peer's partial S is there / was read by the
   // peer) and turn (the chunk has settled the running maximum) also by softmax warp
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2];
   uint64_t x_full[2][4], x_free[2][4], turn[2][4];
-  uint64_t q_full, o_free, drain;
+  uint64_t q_full, o_free, drain[2];
   float mref[128];            // running maximum of each row (raw logits)
   float lsum[2][2][128];      // [parity][every second chunk of it]: the sum of its chunks so far
   uint32_t tmem_base;
@@ -105,7 +117,10 @@ struct Tail {
   int item0, c0, n;
 };
 
-static_assert(kTailOff + sizeof(Tail) <= kSmemMost, "shared memory of a block");
+static_assert(Layout<false>::kTailOff + sizeof(Tail) <= kSmemMost &&
+                  Layout<true>::kTailOff + sizeof(Tail) <= kSmemMost &&
+                  Layout<true>::kTailOff % 8 == 0,
+              "shared memory of a block");
 
 struct Params {
   LatentArgs a;
@@ -294,6 +309,11 @@ __device__ __forceinline__ float ex2f(float x) {
   return y;
 }
 
+__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
+               : "memory");
+}
+
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
                                    *reinterpret_cast<const __nv_bfloat162*>(&b));
@@ -342,8 +362,11 @@ __device__ __forceinline__ void enter_item(const Params& p, int item, Cursor& k)
 template <bool FP8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     latent_attn_kernel(const Params p) {
+  using L = Layout<FP8>;
+  constexpr int kStages = L::kStages;
+  constexpr uint32_t kExchOff = L::kExchOff, kPOff = L::kPOff;
   extern __shared__ __align__(1024) uint8_t smem[];
-  Tail* tail = reinterpret_cast<Tail*>(smem + kTailOff);
+  Tail* tail = reinterpret_cast<Tail*>(smem + L::kTailOff);
   volatile int* abort_flag = &tail->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
@@ -375,7 +398,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     mbar_init(&tail->q_full, act_threads);
     mbar_init(&tail->o_free, act_threads);
-    mbar_init(&tail->drain, 1);
+    mbar_init(&tail->drain[0], 1);
+    mbar_init(&tail->drain[1], 1);
     tail->abort_flag = 0;
     tail->n = 0;
     fence_mbar_init();
@@ -534,49 +558,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       cp_async_wait<0>();
     } else {
-      // a chunk's codes, scales and positional dims on their way, with its header and key mask
-      struct Raw {
-        uint4 code[kCodeReps], rope;
-        uint32_t scale[kCodeReps], valid;
+      // Raw ring: a thread copies in the codes and positional dims that it converts itself; the
+      // scales are the warp's.
+      uint8_t* const raw = smem + L::kRawOff;
+      const int gt = gw * 32 + lane;
+      struct Ahead {
+        uint32_t valid;
         int item, cf, lim0;
       };
-      auto fetch = [&](Raw& r, int g) {
+      auto fetch = [&](Ahead& r, int g) {
         const int b8 = (g & 3) * 8;   // the lanes with this chunk's keys
         if (b8 == 0 && g > 0) next_batch();
         r.item = __shfl_sync(0xffffffffu, now.item, b8);
         r.cf = __shfl_sync(0xffffffffu, now.cf, b8);
         r.lim0 = __shfl_sync(0xffffffffu, now.lim0, b8);
-        r.valid = __ballot_sync(0xffffffffu, now.slot >= 0) >> b8;
-        const uint4 zero = make_uint4(0, 0, 0, 0);
+        r.valid = (__ballot_sync(0xffffffffu, now.slot >= 0) >> b8) & 0xffu;
+        const uint32_t rs = smem_u32(raw) + (g % kAhead) * kRaw;
 #pragma unroll
         for (int j = 0; j < kCodeReps; ++j) {
-          const int i = 2 * j + (lane >> 4), pc = lane & 15;   // two keys per instruction
-          const int sk = __shfl_sync(0xffffffffu, now.slot, b8 + i);
-          const uint8_t* src = p.a.cache + (sk >= 0 ? sk : 0) * row_bytes;
-          r.code[j] = zero;
-          r.scale[j] = 0x3f800000u;
-          if (sk >= 0) {
-            r.code[j] = __ldg(reinterpret_cast<const uint4*>(src + rank * kHalf) + pc);
-            r.scale[j] = __ldg(reinterpret_cast<const uint32_t*>(src + kDc) + rank * 2 + (pc >> 3));
-          }
+          const int pc = lane & 15;   // two keys per instruction
+          const int s = __shfl_sync(0xffffffffu, now.slot, b8 + 2 * j + (lane >> 4));
+          cp_async_16(rs + (j * kGatherThreads + gt) * 16,
+                      p.a.cache + (s >= 0 ? s : 0) * row_bytes + rank * kHalf + pc * 16,
+                      s >= 0 ? 16u : 0u);
         }
-        const int i = lane >> 2, pc = lane & 3;   // four pieces of positional dims per key
-        const int sk = __shfl_sync(0xffffffffu, now.slot, b8 + i);
-        r.rope = zero;
-        if (sk >= 0)
-          r.rope = __ldg(reinterpret_cast<const uint4*>(p.a.cache + sk * row_bytes + kDc + 16 +
-                                                        rank * (2 * kHalfR)) + pc);
+        const int s = __shfl_sync(0xffffffffu, now.slot, b8 + (lane >> 2));
+        const uint8_t* row = p.a.cache + (s >= 0 ? s : 0) * row_bytes + kDc;
+        cp_async_16(rs + kRawRope + gt * 16, row + 16 + rank * (2 * kHalfR) + (lane & 3) * 16,
+                    s >= 0 ? 16u : 0u);
+        if ((lane & 3) == 0)
+          cp_async_8(rs + kRawScale + (gw * kKeysPerWarp + (lane >> 2)) * 8, row + rank * 8,
+                     s >= 0 ? 8u : 0u);
+        cp_async_commit();
       };
-      Raw raw[kAhead];
+      Ahead ahead[kAhead];
 #pragma unroll
-      for (int d = 0; d < kAhead; ++d) fetch(raw[d], d);
+      for (int d = 0; d < kAhead; ++d) fetch(ahead[d], d);
       bool go = true;
       for (int g0 = 0; go && g0 < n; g0 += kAhead) {
 #pragma unroll
         for (int d = 0; d < kAhead; ++d) {
           const int g = g0 + d;
           if (!go || g >= n) break;
-          Raw& r = raw[d];
+          Ahead r = ahead[d];
+          cp_async_wait<kAhead - 1>();
+          __syncwarp();
+          const uint8_t* rs = raw + d * kRaw;
+          uint4 code[kCodeReps];
+          uint32_t scale[kCodeReps];
+#pragma unroll
+          for (int j = 0; j < kCodeReps; ++j) {
+            code[j] = *reinterpret_cast<const uint4*>(rs + (j * kGatherThreads + gt) * 16);
+            scale[j] = *reinterpret_cast<const uint32_t*>(
+                rs + kRawScale + (gw * kKeysPerWarp + 2 * j + (lane >> 4)) * 8 +
+                ((lane >> 3) & 1) * 4);
+          }
+          const uint4 rope = *reinterpret_cast<const uint4*>(rs + kRawRope + gt * 16);
+          __syncwarp();
+          fetch(ahead[d], g + kAhead);   // no keys behind the end
           const int st = g % kStages;
           if (!__all_sync(0xffffffffu, mbar_wait(&tail->kv_empty[st], ((g / kStages) & 1) ^ 1u,
                                                  abort_flag, err, kErrTime))) {
@@ -597,8 +636,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < kCodeReps; ++j) {
             const int pc = lane & 15, key = gw * kKeysPerWarp + 2 * j + (lane >> 4);
-            // 2^k as bf16 bits; 2^(120 + k), or 2^127 and the rest of it
-            const uint32_t e = r.scale[j] >> 16;
+            // 2^k as bf16 bits; 2^(120 + k), or 2^127 and the rest of it. (A key that is not
+            // there has codes and scale bits of zero.)
+            const uint32_t e = scale[j] >> 16;
             uint32_t up = e + (120u << 7), more = 0x3f80u;
             if (e > (134u << 7)) {   // k > 7, or NaN
               up = e > 0x7f80u ? e : 254u << 7;
@@ -607,10 +647,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             up |= up << 16;
             more |= more << 16;
             uint4 w[2];
-            widen4(r.code[j].x, up, more, w[0].x, w[0].y);
-            widen4(r.code[j].y, up, more, w[0].z, w[0].w);
-            widen4(r.code[j].z, up, more, w[1].x, w[1].y);
-            widen4(r.code[j].w, up, more, w[1].z, w[1].w);
+            widen4(code[j].x, up, more, w[0].x, w[0].y);
+            widen4(code[j].y, up, more, w[0].z, w[0].w);
+            widen4(code[j].z, up, more, w[1].x, w[1].y);
+            widen4(code[j].w, up, more, w[1].z, w[1].w);
             // the two 16-byte halves, in the other order in every second atom: eight lanes then
             // store to eight different bank groups
             uint8_t* row = stage + (pc >> 2) * kAtom + key * 128;
@@ -621,75 +661,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           {
             const int key = gw * kKeysPerWarp + (lane >> 2), pc = lane & 3;
             *reinterpret_cast<uint4*>(stage + 4 * kAtom + key * 128 + ((pc ^ (key & 7)) << 4)) =
-                r.rope;
+                rope;
           }
           fence_proxy_async_smem();
           mbar_arrive(&tail->kv_full[st]);
-          fetch(r, g + kAhead);   // no keys behind the end
         }
       }
+      cp_async_wait<0>();
     }
-  } else if (warp == kIssueWarp) {
-    // ================================================================ UMMA issuer
+  } else if (warp == kIssueWarp || warp == kIssuePvWarp) {
+    // ================================================================ UMMA issuers
     if (lane == 0) {
-      constexpr uint32_t idesc_s = umma_idesc_bf16_mn(128, kNK, false);
-      constexpr uint32_t idesc_pv = umma_idesc_bf16_mn(128, kHalf, true);
       const uint32_t base = smem_u32(smem);
-      uint32_t q_par = 0, of_par = 1;
-      int done = 0;          // chunks whose P V has been issued
-      uint32_t firsts = 0;   // bit g % 32: chunk g is the first of its tile here
-      // P V of the next chunk (its P is awaited here)
-      auto pv = [&]() {
-        const int g = done, sb = g & 1, st = g % kStages;
-        const bool first = (firsts >> (g & 31)) & 1u;
-        if (!mbar_wait(&tail->p_full[sb], (g >> 1) & 1, abort_flag, err, kErrTime)) return false;
-        if (first) {   // the previous tile's O has been read out
-          if (!mbar_wait(&tail->o_free, of_par, abort_flag, err, kErrTime)) return false;
-          of_par ^= 1u;
-        }
-        tc_fence_after();
-        const uint64_t p0 = umma_sdesc(base + kPOff + sb * kPBuf, 256, kLayoutSw32);
-        const uint64_t v0 = umma_sdesc_lbo(base + st * kStage, kAtom, 1024, kLayoutSw128);
+      if (warp == kIssueWarp) {
+        constexpr uint32_t idesc = umma_idesc_bf16_mn(128, kNK, false);
+        uint32_t q_par = 0;
+        for (int g = 0; g < n; ++g) {
+          const int st = g % kStages, sb = g & 1;
+          if (!mbar_wait(&tail->kv_full[st], (g / kStages) & 1, abort_flag, err, kErrTime)) break;
+          if (tail->hdr[st].cf & 1) {
+            if (!mbar_wait(&tail->q_full, q_par, abort_flag, err, kErrTime)) break;
+            q_par ^= 1u;
+          }
+          if (!mbar_wait(&tail->s_free[sb], ((g >> 1) & 1) ^ 1u, abort_flag, err, kErrTime)) break;
+          if (!FP8) fence_proxy_async_smem();   // cp.async wrote the rows by the generic proxy
+          tc_fence_after();
+          const uint64_t k0 = umma_sdesc(base + st * kStage, 1024, kLayoutSw128);
 #pragma unroll
-        for (int ks = 0; ks < kNK / 16; ++ks)
-          umma_bf16(tmem + kColO, umma_desc_adv(p0, ks * kPTile), umma_desc_adv(v0, ks * 2048),
-                    idesc_pv, (first && ks == 0) ? 0u : 1u);
-        umma_commit(&tail->kv_empty[st]);
-        umma_commit(&tail->pv_done[sb]);
-        ++done;
-        return true;
-      };
-      bool ok = true;
-      for (int g = 0; ok && g < n; ++g) {
-        const int st = g % kStages, sb = g & 1;
-        ok = mbar_wait(&tail->kv_full[st], (g / kStages) & 1, abort_flag, err, kErrTime);
-        if (!ok) break;
-        const bool first = (tail->hdr[st].cf & 1) != 0;
-        firsts = first ? firsts | (1u << (g & 31)) : firsts & ~(1u << (g & 31));
-        if (first) {
-          // Q comes once the previous tile's last P is out, which may wait for the P V before it
-          while (ok && done < g) ok = pv();
-          ok = ok && mbar_wait(&tail->q_full, q_par, abort_flag, err, kErrTime);
-          q_par ^= 1u;
+          for (int kk = 0; kk < kSteps; ++kk)
+            umma_bf16_ts(tmem + kColS + sb * kNK, tmem + kColQ + kk * 8,
+                         umma_desc_adv(k0, (kk >> 2) * kAtom + (kk & 3) * 32), idesc,
+                         kk > 0 ? 1u : 0u);
+          umma_commit(&tail->s_full[sb]);
         }
-        ok = ok && mbar_wait(&tail->s_free[sb], ((g >> 1) & 1) ^ 1u, abort_flag, err, kErrTime);
-        if (!ok) break;
-        if (!FP8) fence_proxy_async_smem();   // cp.async wrote the rows through the generic proxy
-        tc_fence_after();
-        const uint64_t k0 = umma_sdesc(base + st * kStage, 1024, kLayoutSw128);
+      } else {
+        constexpr uint32_t idesc = umma_idesc_bf16_mn(128, kHalf, true);
+        uint32_t o_par = 1;
+        for (int g = 0; g < n; ++g) {
+          const int st = g % kStages, sb = g & 1;
+          if (!mbar_wait(&tail->kv_full[st], (g / kStages) & 1, abort_flag, err, kErrTime)) break;
+          const bool first = (tail->hdr[st].cf & 1) != 0;
+          if (!FP8) fence_proxy_async_smem();
+          if (first) {   // the previous tile's O has been read out
+            if (!mbar_wait(&tail->o_free, o_par, abort_flag, err, kErrTime)) break;
+            o_par ^= 1u;
+          }
+          if (!mbar_wait(&tail->p_full[sb], (g >> 1) & 1, abort_flag, err, kErrTime)) break;
+          tc_fence_after();
+          const uint64_t p0 = umma_sdesc(base + kPOff + sb * kPBuf, 256, kLayoutSw32);
+          const uint64_t v0 = umma_sdesc_lbo(base + st * kStage, kAtom, 1024, kLayoutSw128);
 #pragma unroll
-        for (int kk = 0; kk < kSteps; ++kk)
-          umma_bf16_ts(tmem + kColS + sb * kNK, tmem + kColQ + kk * 8,
-                       umma_desc_adv(k0, (kk >> 2) * kAtom + (kk & 3) * 32), idesc_s,
-                       kk > 0 ? 1u : 0u);
-        umma_commit(&tail->s_full[sb]);
-        while (ok && done < g - 1) ok = pv();
+          for (int ks = 0; ks < kNK / 16; ++ks)
+            umma_bf16(tmem + kColO, umma_desc_adv(p0, ks * kPTile), umma_desc_adv(v0, ks * 2048),
+                      idesc, (first && ks == 0) ? 0u : 1u);
+          umma_commit(&tail->kv_empty[st]);
+          umma_commit(&tail->pv_done[sb]);
+        }
       }
-      while (ok && done < n) ok = pv();
-      umma_commit(&tail->drain);
-      const uint32_t a = smem_u32(&tail->drain);
+      uint64_t* drain = &tail->drain[warp == kIssueWarp ? 0 : 1];
+      umma_commit(drain);
       const unsigned long long t0 = globaltimer_ns();
-      while (!mbar_try_wait(a, 0)) {
+      while (!mbar_try_wait(smem_u32(drain), 0)) {
         if (globaltimer_ns() - t0 > kWaitLimitNs) {
           report_error(err, kErrTime);
           break;
@@ -1068,7 +1100,7 @@ int resident_clusters(size_t smem) {
 
 template <bool FP8>
 int launch(Params p, cudaStream_t stream) {
-  const size_t smem = kTailOff + sizeof(Tail);
+  const size_t smem = Layout<FP8>::kTailOff + sizeof(Tail);
   if (cudaFuncSetAttribute(latent_attn_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem)) != cudaSuccess)
     return DSA_ERR_CUDA;
