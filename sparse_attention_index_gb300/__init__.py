@@ -724,16 +724,26 @@ def _code(value, table: dict, name: str) -> int:
 def _arg(t, name: str, dtype, shape, device) -> int:
     """A tensor argument: its type, shape and device checked, its address returned."""
     p = _dev(t, name, dtype)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the other arguments on {device}")
     return p
 
 
-def _on(stream, device) -> int:
-    """The stream of a call on `device`: its current one where none is given."""
-    return _stream(torch.cuda.current_stream(device) if stream is None else stream)
+def _call(fn, where: str, device, stream, *args):
+    """fn(*args, stream) on `device`, on its current stream where none is given. (A single-token
+    call is short beside the host's work, so the current device and stream are asked for their
+    numbers alone, without building torch's objects.)"""
+    i = device.index
+    s = torch._C._cuda_getCurrentRawStream(i) if stream is None else _stream(stream)
+    if i == torch.cuda.current_device():
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(i):
+            rc = fn(*args, s)
+    if rc != 0:
+        raise DsaError(rc, where)
 
 
 def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None,
@@ -799,19 +809,18 @@ def dsa_rope(x, pos, inv_freq, off: int = 0, layout: str = "interleaved", mscale
     rot = 2 * inv_freq.numel()
     if out is None:
         out = torch.empty_like(x)
-    args = (xp, _arg(out, "out", x.dtype, x.shape, x.device),
-            DSA_F32 if x.dtype == torch.float32 else DSA_BF16,
-            _arg(pos, "pos", torch.int32, x.shape[:-2], x.device),
-            _arg(inv_freq, "inv_freq", torch.float32, (rot // 2,), x.device), pos.numel(), H, D,
-            off, rot, code, float(mscale), int(bool(inverse)))
-    with torch.cuda.device(x.device):
-        _check(lib.dsa_rope(*args, _on(stream, x.device)), "dsa_rope")
+    dev = x.device
+    _call(lib.dsa_rope, "dsa_rope", dev, stream, xp, _arg(out, "out", x.dtype, x.shape, dev),
+          DSA_F32 if x.dtype == torch.float32 else DSA_BF16,
+          _arg(pos, "pos", torch.int32, x.shape[:-2], dev),
+          _arg(inv_freq, "inv_freq", torch.float32, (rot // 2,), dev), pos.numel(), H, D, off, rot,
+          code, mscale, 1 if inverse else 0)
     return out
 
 
 def cache_row_bytes(Dc: int, Dr: int, fmt: str = "e4m3") -> int:
     """Bytes of one cache row (0: dims that the cache does not support)."""
-    return int(lib.dsa_cache_row_bytes(_code(fmt, _CACHE_FORMATS, "fmt"), Dc, Dr))
+    return lib.dsa_cache_row_bytes(_code(fmt, _CACHE_FORMATS, "fmt"), Dc, Dr)
 
 
 def _cache_arg(cache, Dc, Dr, fmt, device) -> tuple[int, int]:
@@ -837,9 +846,8 @@ def dsa_cache_write(kv, slots, cache, Dc: int, fmt: str = "e4m3", stream=None):
     T, Dr = kv.shape[0], kv.shape[1] - Dc
     cp, num = _cache_arg(cache, Dc, Dr, fmt, kv.device)
     sp = _arg(slots, "slots", torch.int32, (T,), kv.device)
-    with torch.cuda.device(kv.device):
-        _check(lib.dsa_cache_write(kp, sp, T, Dc, Dr, _CACHE_FORMATS[fmt], cp, num,
-                                   _on(stream, kv.device)), "dsa_cache_write")
+    _call(lib.dsa_cache_write, "dsa_cache_write", kv.device, stream, kp, sp, T, Dc, Dr,
+          _CACHE_FORMATS[fmt], cp, num)
     return cache
 
 
@@ -853,9 +861,8 @@ def dsa_cache_read(cache, slots, Dc: int, Dr: int, fmt: str = "e4m3", kv=None, s
     if kv is None:
         kv = torch.empty((N, Dc + Dr), dtype=torch.bfloat16, device=dev)
     kp = _arg(kv, "kv", torch.bfloat16, (N, Dc + Dr), dev)
-    with torch.cuda.device(dev):
-        _check(lib.dsa_cache_read(cp, num, _CACHE_FORMATS[fmt], sp, N, Dc, Dr, kp,
-                                  _on(stream, dev)), "dsa_cache_read")
+    _call(lib.dsa_cache_read, "dsa_cache_read", dev, stream, cp, num, _CACHE_FORMATS[fmt], sp, N,
+          Dc, Dr, kp)
     return kv
 
 
@@ -905,11 +912,8 @@ def dsa_latent_attn(Q, cache, page_table, lens, scale: float, fmt: str = "e4m3",
         ws = torch.empty((need,), dtype=torch.uint8, device=dev)
     if ws is not None and ws.device != dev:
         raise ValueError(f"ws is on {ws.device}, the other arguments on {dev}")
-    with torch.cuda.device(dev):
-        rc = lib.dsa_latent_attn(qp, cp, _CACHE_FORMATS[fmt], cache.shape[0], cache.shape[1], tp,
-                                 page_table.shape[1], lp, ip, k, B, Sq, H, Dc, Dr, float(scale),
-                                 op, ep, None if ws is None else _dev(ws, "ws"),
-                                 0 if ws is None else ws.numel() * ws.element_size(),
-                                 _on(stream, dev))
-    _check(rc, "dsa_latent_attn")
+    _call(lib.dsa_latent_attn, "dsa_latent_attn", dev, stream, qp, cp, _CACHE_FORMATS[fmt],
+          cache.shape[0], cache.shape[1], tp, page_table.shape[1], lp, ip, k, B, Sq, H, Dc, Dr,
+          scale, op, ep, None if ws is None else _dev(ws, "ws"),
+          0 if ws is None else ws.numel() * ws.element_size())
     return O, lse

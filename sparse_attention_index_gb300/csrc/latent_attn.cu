@@ -114,7 +114,7 @@ struct Tail {
   int abort_flag;
   long long sums[kThreads / 32];
   // this cluster's range: its first tile, that tile's first chunk here, chunks in all
-  int item0, c0, n;
+  int item0, c0, n, each;
 };
 
 static_assert(Layout<false>::kTailOff + sizeof(Tail) <= kSmemMost &&
@@ -133,6 +133,8 @@ struct Params {
   float scale_log2;
   float4* part;     // [2 * clusters][128 groups of 4 dims][prow]
   float2* ml;       // [2 * clusters][prow]: running max (scaled, log2) and sum
+  int2* joins;      // [clusters]: the tile that begins in a cluster's range and goes on behind it
+                    // (-1: none), and the last cluster that works on it
 };
 
 // ------------------------------------------------------------------ the split
@@ -164,65 +166,55 @@ __device__ __forceinline__ int item_chunks(const Params& p, int item) {
   return chunks_of(tile_keys(p, seq_len(p.a, b, false), item - b * p.tiles));
 }
 
-struct Place {
-  int item;
-  long long start;   // first chunk of the tile among all chunks
-};
-
-// Chunks of all tiles; with at >= 0, also the tile that chunk `at` lies in. Every thread of the
-// block calls it.
-__device__ __forceinline__ long long total_chunks(const Params& p, long long* sums) {
-  if (p.a.idx) return static_cast<long long>(p.items) * p.list_chunks;
-  const int q = (p.items + blockDim.x - 1) / blockDim.x;
-  const int i0 = min(p.items, static_cast<int>(threadIdx.x) * q), i1 = min(p.items, i0 + q);
-  long long s = 0;
-  for (int i = i0; i < i1; ++i) s += item_chunks(p, i);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
-  __syncthreads();
-  s = 0;
-  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) s += sums[w];
-  return s;
-}
-
-// the tile that chunk `at` lies in, in the one thread that finds it (true there)
-__device__ __forceinline__ bool find_item(const Params& p, long long at, const long long* sums,
-                                          Place& out) {
+// What a cluster takes of the chunks of all tiles: [c0, ...) of tile item0, n chunks in all, `each`
+// per cluster. Every thread of the block calls it; the thread that finds the tile returns true.
+__device__ __forceinline__ bool my_chunks(const Params& p, int cluster, long long* sums, int& item0,
+                                          int& c0, int& n, long long& each) {
+  long long total, before = 0, s = 0;
+  int i0 = 0, i1 = 0;
   if (p.a.idx) {
-    out.item = static_cast<int>(at / p.list_chunks);
-    out.start = static_cast<long long>(out.item) * p.list_chunks;
+    total = static_cast<long long>(p.items) * p.list_chunks;
+  } else {
+    const int q = (p.items + kThreads - 1) / kThreads;
+    i0 = min(p.items, static_cast<int>(threadIdx.x) * q);
+    i1 = min(p.items, i0 + q);
+    for (int i = i0; i < i1; ++i) s += item_chunks(p, i);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long incl = s;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) before += sums[w];
+      total += sums[w];
+    }
+    before += incl - s;
+  }
+  each = max((total + p.clusters - 1) / p.clusters, static_cast<long long>(kMinChunks));
+  const long long g0 = each * cluster;
+  if (g0 >= total) return false;
+  n = static_cast<int>(min(each, total - g0));
+  if (p.a.idx) {
+    item0 = static_cast<int>(g0 / p.list_chunks);
+    c0 = static_cast<int>(g0 - static_cast<long long>(item0) * p.list_chunks);
     return threadIdx.x == 0;
   }
-  const int q = (p.items + blockDim.x - 1) / blockDim.x;
-  const int i0 = min(p.items, static_cast<int>(threadIdx.x) * q), i1 = min(p.items, i0 + q);
-  const int lane = threadIdx.x & 31;
-  long long s = 0;
-  for (int i = i0; i < i1; ++i) s += item_chunks(p, i);
-  long long incl = s;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  long long before = incl - s;
-  for (int w = 0; w < static_cast<int>(threadIdx.x >> 5); ++w) before += sums[w];
-  if (at < before || at >= before + s) return false;
+  if (g0 < before || g0 >= before + s) return false;
   for (int i = i0; i < i1; ++i) {
-    const int n = item_chunks(p, i);
-    if (at < before + n) {
-      out.item = i;
-      out.start = before;
+    const int m = item_chunks(p, i);
+    if (g0 < before + m) {
+      item0 = i;
+      c0 = static_cast<int>(g0 - before);
       return true;
     }
-    before += n;
+    before += m;
   }
   return false;
-}
-
-__device__ __forceinline__ long long chunks_each(const Params& p, long long total) {
-  return max((total + p.clusters - 1) / p.clusters, static_cast<long long>(kMinChunks));
 }
 
 // ------------------------------------------------------------------ small helpers
@@ -233,8 +225,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
@@ -408,29 +403,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tmem_alloc(&tail->tmem_base, 512);
     tmem_relinquish();
   }
+  // thread 0 has made this CTA's barriers; the peer's are ready once cluster_wait returns
+  cluster_arrive();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   {
-    // this cluster's range of chunks
-    const long long total = total_chunks(p, tail->sums);
-    const long long each = chunks_each(p, total);
-    const long long g0 = each * cluster;
-    if (g0 < total) {
-      Place at;
-      if (find_item(p, g0, tail->sums, at)) {
-        tail->item0 = at.item;
-        tail->c0 = static_cast<int>(g0 - at.start);
-        tail->n = static_cast<int>(min(each, total - g0));
-      }
+    int i0, c, m;
+    long long each;
+    if (my_chunks(p, cluster, tail->sums, i0, c, m, each)) {
+      tail->item0 = i0;
+      tail->c0 = c;
+      tail->n = m;
+      tail->each = static_cast<int>(each);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  cluster_sync_all();   // the peer's barriers are ready
   const uint32_t tmem = tail->tmem_base;
   const int n = tail->n, item0 = tail->item0, c0 = tail->c0;
 
   if (n == 0) {
     // nothing here (both CTAs agree)
+    if (threadIdx.x == 0 && rank == 0) p.joins[cluster] = make_int2(-1, 0);
+    cluster_wait();
   } else if (warp >= kGatherWarp0) {
     // ================================================================ gather
     const int gw = warp - kGatherWarp0;
@@ -469,8 +464,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int j = k.c * kNK + mykey;
           e.raw = j < (p.a.idx ? p.a.k : k.keys) ? j : -1;
         }
-        ++made;
-        if (made < n && ++k.c == k.nch) {
+        if (++made == n) {
+          // a tile that begins here and goes on in later clusters
+          const int left = k.nch - 1 - k.c;
+          if (gw == 0 && lane == 0 && rank == 0)
+            p.joins[cluster] = left > 0 && k.c < n
+                                   ? make_int2(k.item, cluster + (left + tail->each - 1) / tail->each)
+                                   : make_int2(-1, 0);
+        } else if (++k.c == k.nch) {
           enter_item(p, k.item + 1, k);
           k.c = 0;
         }
@@ -501,23 +502,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       return r;
     };
-    Entry e0 = look();
-    Paged q0 = page_of(e0);
-    e0 = look();
-    Slot now = slot_of(q0);
-    q0 = page_of(e0);
-    e0 = look();
+    Entry e0 = {-1, 0, 0, 0, 0, 0, 0};
+    Paged q0 = {-1, -1, 0, 0, 0};
+    Slot now = {-1, 0, 0, 0};
+    int steps = 3;   // to the first batch's slots
     auto next_batch = [&]() {
-      now = slot_of(q0);
-      q0 = page_of(e0);
-      e0 = look();
+#pragma unroll 1
+      for (; steps > 0; --steps) {
+        now = slot_of(q0);
+        q0 = page_of(e0);
+        e0 = look();
+      }
+      steps = 1;
     };
     const uint32_t base = smem_u32(smem);
 
     if (!FP8) {
       for (int g = 0; g < n; ++g) {
         const int b8 = (g & 3) * 8;   // the lanes with this chunk's keys
-        if (b8 == 0 && g > 0) next_batch();
+        if (b8 == 0) next_batch();
         const int st = g % kStages;
         const uint32_t par = ((g / kStages) & 1) ^ 1u;
         if (!__all_sync(0xffffffffu,
@@ -568,7 +571,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       auto fetch = [&](Ahead& r, int g) {
         const int b8 = (g & 3) * 8;   // the lanes with this chunk's keys
-        if (b8 == 0 && g > 0) next_batch();
+        if (b8 == 0) next_batch();
         r.item = __shfl_sync(0xffffffffu, now.item, b8);
         r.cf = __shfl_sync(0xffffffffu, now.cf, b8);
         r.lim0 = __shfl_sync(0xffffffffu, now.lim0, b8);
@@ -591,21 +594,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                      s >= 0 ? 8u : 0u);
         cp_async_commit();
       };
-      Ahead ahead[kAhead];
-#pragma unroll
-      for (int d = 0; d < kAhead; ++d) fetch(ahead[d], d);
-      bool go = true;
-      for (int g0 = 0; go && g0 < n; g0 += kAhead) {
-#pragma unroll
-        for (int d = 0; d < kAhead; ++d) {
-          const int g = g0 + d;
-          if (!go || g >= n) break;
-          Ahead r = ahead[d];
+      static_assert(kAhead == 2, "two chunks on their way");
+      Ahead a0 = {0, 0, 0, 0}, a1 = a0;
+      for (int f = 0; f < n + kAhead; ++f) {
+        const int g = f - kAhead;
+        const Ahead r = a0;
+        uint4 code[kCodeReps], rope;
+        uint32_t scale[kCodeReps];
+        if (g >= 0) {
           cp_async_wait<kAhead - 1>();
           __syncwarp();
-          const uint8_t* rs = raw + d * kRaw;
-          uint4 code[kCodeReps];
-          uint32_t scale[kCodeReps];
+          const uint8_t* rs = raw + (g % kAhead) * kRaw;
 #pragma unroll
           for (int j = 0; j < kCodeReps; ++j) {
             code[j] = *reinterpret_cast<const uint4*>(rs + (j * kGatherThreads + gt) * 16);
@@ -613,15 +612,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 rs + kRawScale + (gw * kKeysPerWarp + 2 * j + (lane >> 4)) * 8 +
                 ((lane >> 3) & 1) * 4);
           }
-          const uint4 rope = *reinterpret_cast<const uint4*>(rs + kRawRope + gt * 16);
+          rope = *reinterpret_cast<const uint4*>(rs + kRawRope + gt * 16);
           __syncwarp();
-          fetch(ahead[d], g + kAhead);   // no keys behind the end
+        }
+        a0 = a1;
+        fetch(a1, f);   // no keys behind the end
+        if (g >= 0) {
           const int st = g % kStages;
           if (!__all_sync(0xffffffffu, mbar_wait(&tail->kv_empty[st], ((g / kStages) & 1) ^ 1u,
-                                                 abort_flag, err, kErrTime))) {
-            go = false;
+                                                 abort_flag, err, kErrTime)))
             break;
-          }
           if (lane == 0) {
             Header& h = tail->hdr[st];
             reinterpret_cast<uint8_t*>(h.valid)[gw] = static_cast<uint8_t>(r.valid);
@@ -669,6 +669,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       cp_async_wait<0>();
     }
+    cluster_wait();
   } else if (warp == kIssueWarp || warp == kIssuePvWarp) {
     // ================================================================ UMMA issuers
     if (lane == 0) {
@@ -728,6 +729,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
     }
+    cluster_wait();
   } else if ((warp & 3) < p.act_warps) {
     // ================================================================ softmax / output
     // (a warp whose 32 rows no tile has takes no part: its lanes of S and O hold anything)
@@ -772,6 +774,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
 
     if (wg == 0) load_q(item0);
+    cluster_wait();   // the peer is ready to receive
     const uint32_t sbase = tmem + lane_off + kColS + wg * kNK;
     const uint32_t xb = smem_u32(smem + kExchOff + wg * kExch) + hrow * 16;
     const uint32_t x_dst = peer_addr(xb, peer);
@@ -989,78 +992,80 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       while (globaltimer_ns() - t0 < 100000ull) {
       }
     }
+  } else {
+    cluster_wait();
   }
 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == kIssueWarp) tmem_dealloc(tmem, 512);
-  cluster_sync_all();   // no CTA leaves while its peer may still write to it
+  cluster_arrive();
+  cluster_wait();   // no CTA leaves while its peer may still write to it
 }
 
-// Joins the parts of a tile that several clusters worked on: block (c, y) the tile that begins in
-// cluster c's range and goes on behind it, dims [32 y, 32 y + 32). One row per thread.
-__global__ void __launch_bounds__(128) latent_join_kernel(const Params p) {
-  __shared__ long long sums[4];
-  __shared__ int item_s;
-  __shared__ long long start_s, end_s;
-  const int cluster = blockIdx.x;
-  const long long total = total_chunks(p, sums);
-  const long long each = chunks_each(p, total);
-  const long long g0 = each * cluster, g1 = g0 + each;
-  if (g1 >= total) return;
-  Place at;
-  if (find_item(p, g1 - 1, sums, at)) {
-    item_s = at.item;
-    start_s = at.start;
-    end_s = at.start + item_chunks(p, at.item);
-  }
-  __syncthreads();
-  if (start_s < g0 || end_s <= g1) return;
-  const int last = static_cast<int>((end_s - 1) / each);
+// Joins the parts of a tile that several clusters worked on: block (c, y, z) the tile that begins
+// in cluster c's range and goes on behind it, rows [32 y, 32 y + 32) (one per lane) and dims
+// [128 z, 128 z + 128) (16 per warp). The parts' maxima are fetched side by side first, then two
+// parts' dims at a time: one after the other, their latencies took longer than the attention of a
+// short cache.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const Params p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  float2* ml = reinterpret_cast<float2*>(smem);   // [parts][32]
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int2 tile = __ldcg(p.joins + blockIdx.x);
+  if (tile.x < 0) return;
+  const int first = blockIdx.x, parts = tile.y - first + 1;
   int rows = p.a.H;
-  long long r0 = static_cast<long long>(item_s) * p.a.H;
+  long long r0 = static_cast<long long>(tile.x) * p.a.H;
   if (!p.a.idx) {
-    const int b = item_s / p.tiles, mt = item_s - b * p.tiles;
+    const int b = tile.x / p.tiles, mt = tile.x - b * p.tiles;
     rows = tile_rows(p, mt);
     r0 = static_cast<long long>(b) * p.a.Sq * p.a.H + mt * 128;
   }
-  const int row = threadIdx.x;
-  if (row >= rows) return;
+  if (static_cast<int>(blockIdx.y) * 32 >= rows) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y * 32 + lane;
   // part 1 of the first cluster, part 0 of the others
+  auto part_of = [&](int i) { return static_cast<long long>(2 * (first + i) + (i == 0)); };
+  for (int i = warp; i < parts; i += kJoinThreads / 32)
+    ml[i * 32 + lane] = __ldcg(p.ml + part_of(i) * p.prow + row);
+  __syncthreads();
   float top = -INFINITY;
-  for (int c = cluster; c <= last; ++c)
-    top = fmaxf(top, p.ml[static_cast<long long>(2 * c + (c == cluster)) * p.prow + row].x);
+  for (int i = 0; i < parts; ++i) top = fmaxf(top, ml[i * 32 + lane].x);
+  const int d4 = blockIdx.z * 32 + warp * 4;
   float l = 0.f;
-  float4 o[8];
+  float4 o[4];
 #pragma unroll
-  for (int d = 0; d < 8; ++d) o[d] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = cluster; c <= last; ++c) {
-    const long long part = 2 * c + (c == cluster);
-    const float2 ml = p.ml[part * p.prow + row];
-    // a part without a key has m = -inf and l = 0 (and O = 0); one with a NaN keeps it in l
-    const float w = ml.x == -INFINITY ? (ml.y == 0.f ? 0.f : 1.f) : exp2f(ml.x - top);
-    if (w == 0.f) continue;
-    l += w * ml.y;
-    const float4* src = p.part + part * (kDc / 4) * p.prow + blockIdx.y * 8 * p.prow + row;
+  for (int d = 0; d < 4; ++d) o[d] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+  for (int i = 0; i < parts; ++i) {
+    const float4* src = p.part + (part_of(i) * (kDc / 4) + d4) * p.prow + row;
+    float4 x[4];
 #pragma unroll
-    for (int d = 0; d < 8; ++d) {
-      const float4 x = src[d * p.prow];
-      o[d].x += w * x.x;
-      o[d].y += w * x.y;
-      o[d].z += w * x.z;
-      o[d].w += w * x.w;
+    for (int d = 0; d < 4; ++d) x[d] = __ldcg(src + d * p.prow);
+    // a part without a key has m = -inf, l = 0 and O = 0; one with a NaN keeps it in l
+    const float2 q = ml[i * 32 + lane];
+    const float w = q.x == -INFINITY ? (q.y == 0.f ? 0.f : 1.f) : exp2f(q.x - top);
+    l += w * q.y;
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+      o[d].x += w * x[d].x;
+      o[d].y += w * x[d].y;
+      o[d].z += w * x[d].z;
+      o[d].w += w * x[d].w;
     }
   }
+  if (row >= rows) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint4* out = reinterpret_cast<uint4*>(p.a.O + (r0 + row) * kDc + blockIdx.y * 32);
+  uint4* out = reinterpret_cast<uint4*>(p.a.O + (r0 + row) * kDc + d4 * 4);
 #pragma unroll
-  for (int d = 0; d < 4; ++d)
+  for (int d = 0; d < 2; ++d)
     out[d] = make_uint4(pack_bf16(o[2 * d].x * inv, o[2 * d].y * inv),
                         pack_bf16(o[2 * d].z * inv, o[2 * d].w * inv),
                         pack_bf16(o[2 * d + 1].x * inv, o[2 * d + 1].y * inv),
                         pack_bf16(o[2 * d + 1].z * inv, o[2 * d + 1].w * inv));
-  if (blockIdx.y == 0)
+  if (blockIdx.z == 0 && warp == 0)
     p.a.lse[r0 + row] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994530942f;
 }
 
@@ -1069,7 +1074,8 @@ int part_rows(int Sq, int H, int k) {
   return static_cast<int>(rows < 128 ? (rows + 31) / 32 * 32 : 128);
 }
 
-// clusters of the kernel that fit on the current device at once
+// Clusters of the kernel that fit on the current device at once; the first call on a device also
+// raises the kernel's shared-memory limit there.
 template <bool FP8>
 int resident_clusters(size_t smem) {
   constexpr int kMaxDevices = 64;
@@ -1080,6 +1086,9 @@ int resident_clusters(size_t smem) {
   std::lock_guard<std::mutex> guard(lock);
   if (known[dev] == 0) {
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (cudaFuncSetAttribute(latent_attn_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem)) != cudaSuccess)
+      return 0;
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = 2;
@@ -1101,9 +1110,6 @@ int resident_clusters(size_t smem) {
 template <bool FP8>
 int launch(Params p, cudaStream_t stream) {
   const size_t smem = Layout<FP8>::kTailOff + sizeof(Tail);
-  if (cudaFuncSetAttribute(latent_attn_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
-    return DSA_ERR_CUDA;
   p.clusters = resident_clusters<FP8>(smem);
   if (p.clusters < 1) return DSA_ERR_CUDA;
   // no more clusters than the longest possible sequences have work for
@@ -1112,11 +1118,22 @@ int launch(Params p, cudaStream_t stream) {
   const long long wanted = (p.items * most + kMinChunks - 1) / kMinChunks;
   if (wanted < p.clusters) p.clusters = static_cast<int>(wanted);
   p.ml = reinterpret_cast<float2*>(p.part + 2ll * p.clusters * (kDc / 4) * p.prow);
+  p.joins = reinterpret_cast<int2*>(p.ml + 2ll * p.clusters * p.prow);
   latent_attn_kernel<FP8><<<2 * p.clusters, kThreads, smem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
   if (p.clusters == 1) return DSA_OK;   // nothing is split
-  latent_join_kernel<<<dim3(p.clusters, kDc / 32), 128, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  // its blocks may be set up while the last clusters finish; they wait for the parts
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.clusters - 1, p.prow / 32, kDc / 128);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.clusters) * 32 * sizeof(float2);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, latent_join_kernel, p) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
 }  // namespace
@@ -1124,7 +1141,8 @@ int launch(Params p, cudaStream_t stream) {
 size_t latent_attn_workspace(int B, int Sq, int H, int k) {
   (void)B;
   const size_t rows = static_cast<size_t>(part_rows(Sq, H, k));
-  return 2ull * kMaxClusters * rows * (kDc * sizeof(float) + sizeof(float2));
+  return 2ull * kMaxClusters * rows * (kDc * sizeof(float) + sizeof(float2)) +
+         kMaxClusters * sizeof(int2);
 }
 
 int launch_latent_attn(const LatentArgs& a, int fmt, cudaStream_t stream) {

@@ -158,18 +158,17 @@ int launch(const RopeParams& p, cudaStream_t stream) {
   // tokens that a block's vectors touch
   const long long ntok = (kThreads * V + p.vpt - 2) / p.vpt + 1;
   const size_t smem = nf * sizeof(unsigned long long) + ntok * nf * sizeof(float2);
-  auto kern = rope_kernel<T, HALF, V>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem)) != cudaSuccess)
-    return DSA_ERR_CUDA;
+  // at most 1024 * 8 / D vectors' tokens of D / 2 angles and two partial ones: below 48 KB
   const long long blocks = (p.total + kThreads * V - 1) / (kThreads * V);
   if (blocks > 0x7fffffffLL) return DSA_ERR_UNSUPPORTED;
-  kern<<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(p);
+  rope_kernel<T, HALF, V><<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
 template <typename T, bool HALF>
 int launch_v(const RopeParams& p, cudaStream_t stream) {
+  // few vectors: one per thread, so that they spread over the SMs
+  if (p.total <= 152 * 4 * kThreads) return launch<T, HALF, 1>(p, stream);
   return launch<T, HALF, 4>(p, stream);
 }
 
