@@ -94,8 +94,8 @@ constexpr size_t kSmemMost = 232448;   // of a block
 
 struct Header {
   int item;    // tile
-  int cf;      // 8 * (chunk of the tile) + 1: its first chunk here, 2: its last one here, 4: the
-               // whole tile is here
+  int cf;      // 16 * (chunk of the tile) + 1: its first chunk here, 2: its last one here, 4: the
+               // whole tile is here, 8: the next chunk is its last one here
   int lim0;    // keys that the tile's first row sees (every cached key); unused with lists
   uint32_t valid[2];   // the chunk's 48 keys: a byte from each gather warp
 };
@@ -130,6 +130,7 @@ struct Params {
   int clusters;
   int act_warps;    // softmax warps with rows
   int prow;         // rows of a workspace part (32 * act_warps)
+  int page_shift;   // log2 of the page size, -1 where it is no power of two
   float scale_log2;
   float4* part;     // [2 * clusters][128 groups of 4 dims][prow]
   float2* ml;       // [2 * clusters][prow]: running max (scaled, log2) and sum
@@ -317,40 +318,33 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 
 // Four e4m3 bytes to bf16. The 7 magnitude bits, moved to the top of the bf16 mantissa and the
 // bottom of its exponent, are the value times 2^-120 (biases 127 and 7; the subnormals of one are
-// subnormals of the other), so one exact multiply by 2^(120 + k) widens and scales. `up` holds
-// that power twice, `more` what it lacks above 2^127 (1 but for k > 7).
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t up, uint32_t more, uint32_t& lo,
-                                       uint32_t& hi) {
+// subnormals of the other), so one exact multiply by 2^(120 + k), twice in `up`, widens and scales.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t up, uint32_t& lo, uint32_t& hi) {
   const uint32_t t0 = __byte_perm(w, 0, 0x1404), t1 = __byte_perm(w, 0, 0x3424);
   lo = mul_bf16x2((t0 & 0x80008000u) | ((t0 >> 4) & 0x07f007f0u), up);
   hi = mul_bf16x2((t1 & 0x80008000u) | ((t1 >> 4) & 0x07f007f0u), up);
-  if (more != 0x3f803f80u) {
-    lo = mul_bf16x2(lo, more);
-    hi = mul_bf16x2(hi, more);
-  }
 }
 
 // ------------------------------------------------------------------ the kernel
 
 // where a gather warp stands in its cluster's chunks
 struct Cursor {
-  int item, c, nch, len, keys, b, mt;
+  int item, c, nch, len, keys, b, lim0;
 };
 
 __device__ __forceinline__ void enter_item(const Params& p, int item, Cursor& k) {
   k.item = item;
+  k.b = item / (p.a.idx ? p.a.Sq : p.tiles);
+  const int at = item - k.b * (p.a.idx ? p.a.Sq : p.tiles);   // the token, or the tile
+  k.len = seq_len(p.a, k.b, true);
   if (p.a.idx) {
-    k.b = item / p.a.Sq;
-    k.mt = item - k.b * p.a.Sq;   // the token
-    k.len = seq_len(p.a, k.b, true);
-    k.keys = max(0, k.len - p.a.Sq + k.mt + 1);
+    k.keys = max(0, k.len - p.a.Sq + at + 1);
     k.nch = p.list_chunks;
+    k.lim0 = 0;
   } else {
-    k.b = item / p.tiles;
-    k.mt = item - k.b * p.tiles;
-    k.len = seq_len(p.a, k.b, true);
-    k.keys = tile_keys(p, k.len, k.mt);
+    k.keys = tile_keys(p, k.len, at);
     k.nch = chunks_of(k.keys);
+    k.lim0 = k.len - p.a.Sq + 1 + (at * 128) / p.a.H;
   }
 }
 
@@ -441,39 +435,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int raw, len, keys, b, item, cf, lim0;
     };
     struct Paged {
-      int page, pos, item, cf, lim0;
+      int page, off, item, cf, lim0;   // off: row of the page, -1 without a key
     };
     struct Slot {
       int slot, item, cf, lim0;
     };
     auto look = [&]() {
       Entry e = {-1, 0, 0, 0, 0, 0, 0};
-#pragma unroll 1
-      for (int i = 0; i < 4 && made < n; ++i) {
-        int cf = 8 * k.c + (made == 0 || k.c == 0 ? 1 : 0) +
-                 (made == n - 1 || k.c == k.nch - 1 ? 2 : 0);
+      // chunk k.c + i of the tile, the (made + i)-th of the range
+      auto take = [&](int i) {
+        const int c = k.c + i, m = made + i;
+        const int to_go = min(n - 1 - m, k.nch - 1 - c);   // chunks of the tile behind it
+        e.cf = 16 * c + (m == 0 || c == 0 ? 1 : 0) + (to_go == 0 ? 2 : 0) + (to_go == 1 ? 8 : 0);
         // the whole tile is in this range: its first chunk was here, and its last one is
-        if (k.c <= made && k.nch - k.c <= n - made) cf += 4;
-        if ((lane >> 3) == i) {
-          e.len = k.len;
-          e.keys = k.keys;
-          e.b = k.b;
-          e.item = k.item;
-          e.cf = cf;
-          e.lim0 = k.len - p.a.Sq + 1 + (p.a.idx ? 0 : (k.mt * 128) / p.a.H);
-          const int j = k.c * kNK + mykey;
-          e.raw = j < (p.a.idx ? p.a.k : k.keys) ? j : -1;
-        }
-        if (++made == n) {
-          // a tile that begins here and goes on in later clusters
-          const int left = k.nch - 1 - k.c;
-          if (gw == 0 && lane == 0 && rank == 0)
-            p.joins[cluster] = left > 0 && k.c < n
-                                   ? make_int2(k.item, cluster + (left + tail->each - 1) / tail->each)
-                                   : make_int2(-1, 0);
-        } else if (++k.c == k.nch) {
-          enter_item(p, k.item + 1, k);
-          k.c = 0;
+        if (c <= m && k.nch - c <= n - m) e.cf += 4;
+        e.len = k.len;
+        e.keys = k.keys;
+        e.b = k.b;
+        e.item = k.item;
+        e.lim0 = k.lim0;
+        const int j = c * kNK + mykey;
+        e.raw = j < (p.a.idx ? p.a.k : k.keys) ? j : -1;
+      };
+      if (made + 4 < n && k.c + 4 < k.nch) {
+        take(lane >> 3);
+        made += 4;
+        k.c += 4;
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < 4 && made < n; ++i) {
+          if ((lane >> 3) == i) take(0);
+          if (++made == n) {
+            // a tile that begins here and goes on in later clusters
+            const int left = k.nch - 1 - k.c;
+            if (gw == 0 && lane == 0 && rank == 0)
+              p.joins[cluster] =
+                  left > 0 && k.c < n
+                      ? make_int2(k.item, cluster + (left + tail->each - 1) / tail->each)
+                      : make_int2(-1, 0);
+          } else if (++k.c == k.nch) {
+            enter_item(p, k.item + 1, k);
+            k.c = 0;
+          }
         }
       }
       if (p.a.idx && e.raw >= 0)
@@ -484,21 +487,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       Paged q = {-1, -1, e.item, e.cf, e.lim0};
       if (e.raw < -1 || e.raw >= e.len) {
         if (e.raw != -1) report_error(err, kErrIdx);
-      } else if (e.raw < e.keys) {
-        q.pos = e.raw;
+      } else if (e.raw >= 0 && e.raw < e.keys) {
+        const int pg = p.page_shift >= 0 ? e.raw >> p.page_shift : e.raw / p.a.page_size;
+        q.off = e.raw - pg * p.a.page_size;
+        q.page = __ldg(p.a.page_table + static_cast<long long>(e.b) * p.a.max_pages + pg);
       }
-      if (q.pos >= 0)
-        q.page = __ldg(p.a.page_table + static_cast<long long>(e.b) * p.a.max_pages +
-                       q.pos / p.a.page_size);
       return q;
     };
     auto slot_of = [&](const Paged& q) {
       Slot r = {-1, q.item, q.cf, q.lim0};
-      if (q.pos >= 0) {
+      if (q.off >= 0) {
         if (q.page < 0 || q.page >= p.a.num_pages)
           report_error(err, kErrPage);
         else
-          r.slot = q.page * p.a.page_size + q.pos % p.a.page_size;
+          r.slot = q.page * p.a.page_size + q.off;
       }
       return r;
     };
@@ -572,9 +574,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto fetch = [&](Ahead& r, int g) {
         const int b8 = (g & 3) * 8;   // the lanes with this chunk's keys
         if (b8 == 0) next_batch();
-        r.item = __shfl_sync(0xffffffffu, now.item, b8);
-        r.cf = __shfl_sync(0xffffffffu, now.cf, b8);
-        r.lim0 = __shfl_sync(0xffffffffu, now.lim0, b8);
+        if (gw == 0) {
+          r.item = __shfl_sync(0xffffffffu, now.item, b8);
+          r.cf = __shfl_sync(0xffffffffu, now.cf, b8);
+          r.lim0 = __shfl_sync(0xffffffffu, now.lim0, b8);
+        }
         r.valid = (__ballot_sync(0xffffffffu, now.slot >= 0) >> b8) & 0xffu;
         const uint32_t rs = smem_u32(raw) + (g % kAhead) * kRaw;
 #pragma unroll
@@ -599,7 +603,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int f = 0; f < n + kAhead; ++f) {
         const int g = f - kAhead;
         const Ahead r = a0;
-        uint4 code[kCodeReps], rope;
+        // The halves of a piece in the other order in every second atom: eight lanes then store
+        // to eight different bank groups.
+        const int sw = (lane >> 2) & 1;
+        uint2 code[kCodeReps][2];
+        uint4 rope;
         uint32_t scale[kCodeReps];
         if (g >= 0) {
           cp_async_wait<kAhead - 1>();
@@ -607,7 +615,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint8_t* rs = raw + (g % kAhead) * kRaw;
 #pragma unroll
           for (int j = 0; j < kCodeReps; ++j) {
-            code[j] = *reinterpret_cast<const uint4*>(rs + (j * kGatherThreads + gt) * 16);
+            const uint8_t* at = rs + (j * kGatherThreads + gt) * 16;
+            code[j][0] = *reinterpret_cast<const uint2*>(at + 8 * sw);
+            code[j][1] = *reinterpret_cast<const uint2*>(at + 8 - 8 * sw);
             scale[j] = *reinterpret_cast<const uint32_t*>(
                 rs + kRawScale + (gw * kKeysPerWarp + 2 * j + (lane >> 4)) * 8 +
                 ((lane >> 3) & 1) * 4);
@@ -636,27 +646,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < kCodeReps; ++j) {
             const int pc = lane & 15, key = gw * kKeysPerWarp + 2 * j + (lane >> 4);
-            // 2^k as bf16 bits; 2^(120 + k), or 2^127 and the rest of it. (A key that is not
-            // there has codes and scale bits of zero.)
+            // 2^k as bf16 bits to 2^(120 + k). (A key that is not there has codes and scale bits
+            // of zero.)
             const uint32_t e = scale[j] >> 16;
-            uint32_t up = e + (120u << 7), more = 0x3f80u;
-            if (e > (134u << 7)) {   // k > 7, or NaN
-              up = e > 0x7f80u ? e : 254u << 7;
-              more = e > 0x7f80u ? e : e - (7u << 7);
-            }
-            up |= up << 16;
-            more |= more << 16;
+            uint32_t up = (e + (120u << 7)) * 0x10001u;
+            const bool wide = e > (134u << 7);   // k > 7, or NaN: 2^127, and the rest below
+            if (wide) up = e > 0x7f80u ? 0x7fff7fffu : 0x7f007f00u;
             uint4 w[2];
-            widen4(code[j].x, up, more, w[0].x, w[0].y);
-            widen4(code[j].y, up, more, w[0].z, w[0].w);
-            widen4(code[j].z, up, more, w[1].x, w[1].y);
-            widen4(code[j].w, up, more, w[1].z, w[1].w);
-            // the two 16-byte halves, in the other order in every second atom: eight lanes then
-            // store to eight different bank groups
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              widen4(code[j][h].x, up, w[h].x, w[h].y);
+              widen4(code[j][h].y, up, w[h].z, w[h].w);
+              if (wide) {
+                const uint32_t more = (e - (7u << 7)) * 0x10001u;
+                w[h].x = mul_bf16x2(w[h].x, more);
+                w[h].y = mul_bf16x2(w[h].y, more);
+                w[h].z = mul_bf16x2(w[h].z, more);
+                w[h].w = mul_bf16x2(w[h].w, more);
+              }
+            }
             uint8_t* row = stage + (pc >> 2) * kAtom + key * 128;
-            const int sw = (pc >> 2) & 1, c = (pc & 3) * 2;
-            *reinterpret_cast<uint4*>(row + (((c + sw) ^ (key & 7)) << 4)) = sw ? w[1] : w[0];
-            *reinterpret_cast<uint4*>(row + (((c + 1 - sw) ^ (key & 7)) << 4)) = sw ? w[0] : w[1];
+            const int c = (pc & 3) * 2;
+            *reinterpret_cast<uint4*>(row + (((c + sw) ^ (key & 7)) << 4)) = w[0];
+            *reinterpret_cast<uint4*>(row + (((c + 1 - sw) ^ (key & 7)) << 4)) = w[1];
           }
           {
             const int key = gw * kKeysPerWarp + (lane >> 2), pc = lane & 3;
@@ -756,17 +768,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool in = hrow < rows;
       const uint4* src = reinterpret_cast<const uint4*>(p.a.Q + (in ? r0 + hrow : 0) * kD);
       const uint4 zero = make_uint4(0, 0, 0, 0);
+      // 96 dims at a time, so that enough loads are on their way: a row is a line of its own to
+      // every lane
 #pragma unroll
-      for (int a = 0; a < kSteps / 2; ++a) {   // 32 dims: 16 columns
-        uint32_t w[16];
+      for (int t = 0; t < kSteps / 6; ++t) {
+        uint4 x[12];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int at = a < kHalf / 32 ? rank * (kHalf / 8) + a * 4 + q
-                                        : kDc / 8 + rank * (kHalfR / 8) + q;
-          const uint4 x = in ? __ldg(src + at) : zero;
-          w[4 * q] = x.x; w[4 * q + 1] = x.y; w[4 * q + 2] = x.z; w[4 * q + 3] = x.w;
+        for (int q = 0; q < 12; ++q) {
+          const int i = 12 * t + q;   // of this CTA's 16-byte pieces of the row
+          const int at = i < kHalf / 8 ? rank * (kHalf / 8) + i
+                                       : kDc / 8 + rank * (kHalfR / 8) + i - kHalf / 8;
+          x[q] = in ? __ldg(src + at) : zero;
         }
-        tmem_st_x16(tmem + lane_off + kColQ + a * 16, w);
+#pragma unroll
+        for (int a = 0; a < 3; ++a) {
+          uint32_t w[16];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint4 v = x[4 * a + q];
+            w[4 * q] = v.x; w[4 * q + 1] = v.y; w[4 * q + 2] = v.z; w[4 * q + 3] = v.w;
+          }
+          tmem_st_x16(tmem + lane_off + kColQ + (3 * t + a) * 16, w);
+        }
       }
       tmem_st_wait();
       tc_fence_before();
@@ -817,7 +840,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int j = 0; j < 16; ++j) s[32 + j] = __uint_as_float(hi[j]);
       mbar_arrive(&tail->s_free[wg]);
       const Header& h = tail->hdr[st];
-      const int item = h.item, flags = h.cf & 7, c = h.cf >> 3;
+      const int item = h.item, flags = h.cf & 15, c = h.cf >> 4;
       unsigned long long vm =
           h.valid[0] | static_cast<unsigned long long>(h.valid[1] & 0xffffu) << 32;
       if (item != cur) {
@@ -932,10 +955,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       l += other;
       fence_proxy_async_smem();
       mbar_arrive(&tail->p_full[wg]);
+      // The next tile's Q replaces this one's once the last S of this one is done. The warps of
+      // the chunk before the last load it, since those of the last have the output to write.
+      if ((flags & 8) && g + 2 < n) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&tail->s_full[wg ^ 1], ((g + 1) >> 1) & 1, abort_flag,
+                                               err, kErrTime)))
+          break;
+        tc_fence_after();
+        load_q(item + 1);
+      }
       if (!(flags & 2)) continue;
 
-      // the tile's last chunk here: every S of it is done, the next tile's Q may replace its own
-      if (g + 1 < n) load_q(item + 1);
+      if ((flags & 1) && g + 1 < n) load_q(item + 1);   // the tile's only chunk here
       if (!__all_sync(0xffffffffu,
                       mbar_wait(&tail->pv_done[wg], par, abort_flag, err, kErrTime)))
         break;
@@ -1156,6 +1187,9 @@ int launch_latent_attn(const LatentArgs& a, int fmt, cudaStream_t stream) {
   p.prow = part_rows(a.Sq, a.H, a.k);
   p.act_warps = p.prow / 32;
   p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (a.page_size == 1 << i) p.page_shift = i;
   p.part = static_cast<float4*>(a.ws);
   return fmt == DSA_CACHE_E4M3 ? launch<true>(p, stream) : launch<false>(p, stream);
 }
