@@ -305,6 +305,30 @@ __device__ __forceinline__ float ex2f(float x) {
   return y;
 }
 
+// Two fp32 operations per instruction, and a maximum of three.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(*reinterpret_cast<unsigned long long*>(&r))
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)),
+        "l"(*reinterpret_cast<unsigned long long*>(&b)));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(*reinterpret_cast<unsigned long long*>(&r))
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)),
+        "l"(*reinterpret_cast<unsigned long long*>(&b)),
+        "l"(*reinterpret_cast<unsigned long long*>(&c)));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 __device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src, uint32_t src_bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
                : "memory");
@@ -822,7 +846,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ok = ok && wait_peer(&tail->x_free[wg][quarter], par ^ 1u, abort_flag, err);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      float s[kNK];
+      float2 s[kNK / 2];
       uint32_t lo[32], hi[16];
       tmem_ld_x32(sbase, lo);
       tmem_ld_16(sbase + 32, hi);
@@ -835,9 +859,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int j = 0; j < 16; j += 4)
         st_peer(x_dst + (32 + j) * 512, x_bar, hi[j], hi[j + 1], hi[j + 2], hi[j + 3]);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) s[j] = __uint_as_float(lo[j]);
+      for (int j = 0; j < 16; ++j)
+        s[j] = make_float2(__uint_as_float(lo[2 * j]), __uint_as_float(lo[2 * j + 1]));
 #pragma unroll
-      for (int j = 0; j < 16; ++j) s[32 + j] = __uint_as_float(hi[j]);
+      for (int j = 0; j < 8; ++j)
+        s[16 + j] = make_float2(__uint_as_float(hi[2 * j]), __uint_as_float(hi[2 * j + 1]));
       mbar_arrive(&tail->s_free[wg]);
       const Header& h = tail->hdr[st];
       const int item = h.item, flags = h.cf & 15, c = h.cf >> 4;
@@ -861,19 +887,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int j = 0; j < kNK / 4; ++j) {
         const float4 x = xr[j * 128];
-        s[4 * j] += x.x;
-        s[4 * j + 1] += x.y;
-        s[4 * j + 2] += x.z;
-        s[4 * j + 3] += x.w;
+        s[2 * j] = add2(s[2 * j], make_float2(x.x, x.y));
+        s[2 * j + 1] = add2(s[2 * j + 1], make_float2(x.z, x.w));
       }
-      const bool all = vm == (1ull << kNK) - 1;
-      if (!all) {
+      if (vm != (1ull << kNK) - 1) {
 #pragma unroll
-        for (int j = 0; j < kNK; ++j) s[j] = ((vm >> j) & 1u) ? s[j] : -INFINITY;
+        for (int j = 0; j < kNK / 2; ++j) {
+          s[j].x = ((vm >> (2 * j)) & 1u) ? s[j].x : -INFINITY;
+          s[j].y = ((vm >> (2 * j + 1)) & 1u) ? s[j].y : -INFINITY;
+        }
       }
-      float m4[4] = {s[0], s[1], s[2], s[3]};
+      float m4[4];
 #pragma unroll
-      for (int j = 4; j < kNK; ++j) m4[j & 3] = fmaxf(m4[j & 3], s[j]);
+      for (int j = 0; j < 4; ++j) m4[j] = fmaxf(s[j].x, s[j].y);
+#pragma unroll
+      for (int j = 4; j < kNK / 2; ++j) m4[j & 3] = max3(m4[j & 3], s[j].x, s[j].y);
       const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
       __syncwarp();
       if (lane == 0) arrive_peer(x_ack, mx);
@@ -934,23 +962,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         break;
       // P = exp2(S*c2 - m*c2) over the valid keys (exp2(-inf) = 0 elsewhere)
       const float base = m == -INFINITY ? 0.f : m * c2;
-      float ls[4] = {0.f, 0.f, 0.f, 0.f};
+      const float2 cc = make_float2(c2, c2), bb = make_float2(-base, -base);
+      float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
       for (int t = 0; t < kNK / 16; ++t) {
         uint32_t pk[8];
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const float e0 = ex2f(fmaf(s[t * 16 + j], c2, -base));
-          const float e1 = ex2f(fmaf(s[t * 16 + j + 1], c2, -base));
-          ls[j & 2] += e0;
-          ls[(j & 2) + 1] += e1;
-          pk[j >> 1] = pack_bf16(e0, e1);
+        for (int j = 0; j < 8; ++j) {
+          float2 e = fma2(s[t * 8 + j], cc, bb);
+          e.x = ex2f(e.x);
+          e.y = ex2f(e.y);
+          ls[j & 1] = add2(ls[j & 1], e);
+          pk[j] = pack_bf16(e.x, e.y);
         }
         uint8_t* dst = prow_s + t * kPTile;
         *reinterpret_cast<uint4*>(dst + psw) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         *reinterpret_cast<uint4*>(dst + (psw ^ 16)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
       }
-      l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+      l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
       tail->lsum[wg][par][hrow] = l;
       l += other;
       fence_proxy_async_smem();
