@@ -558,7 +558,9 @@ int dsa_cache_read(const void* cache, int64_t num_slots, int fmt, const int32_t*
  * and lse = -inf; a sequence with len <= 0 is skipped that way (padding). A length below 0 or
  * above max_pages * page_size is taken as the nearest of the two, and a page outside
  * [0, num_pages) is skipped as if its keys were not there; both are recorded as
- * DSA_STAGE_LATENT | DSA_DEVERR_BAD_PAGE. Rows of the cache that no token sees are not read.
+ * DSA_STAGE_LATENT | DSA_DEVERR_BAD_PAGE. Rows of the cache that no token sees are not read. An
+ * infinity or a NaN in a row reaches every token that sees it and, without lists and with Sq > 1,
+ * any other new token of the sequence (a masked weight of zero still multiplies it).
  *
  *   Q     bf16 [B, Sq, H, Dc + Dr]        cache      as above, num_pages * page_size slots
  *   lens  int32 [B]                       page_table int32 [B, max_pages]
@@ -567,8 +569,10 @@ int dsa_cache_read(const void* cache, int64_t num_slots, int fmt, const int32_t*
  *   ws    workspace of dsa_latent_attn_workspace_size() bytes (overwritten): the parts of
  *         rows whose keys are split over the GPU. Nothing is kept in it between calls.
  *
- * Supported: (Dc, Dr) = (512, 64), 1 <= H <= 128, scale > 0 and finite, page_size >= 1,
- * num_pages * page_size < 2^31, max_pages * page_size < 2^31.
+ * Supported: (Dc, Dr) = (512, 64), 1 <= H <= 128, 0 < scale <= 2e38, page_size >= 1,
+ * num_pages * page_size < 2^31, max_pages * page_size < 2^31, B * Sq * H < 2^31. The weights are
+ * rounded to bf16 for their product with the rows, sums are fp32 in a fixed order (the same
+ * bits every time).
  */
 size_t dsa_latent_attn_workspace_size(int B, int Sq, int H, int Dc, int Dr, int k);
 int dsa_latent_attn(const void* Q, const void* cache, int fmt, int64_t num_pages, int page_size,

@@ -814,7 +814,7 @@ def dsa_rope(x, pos, inv_freq, off: int = 0, layout: str = "interleaved", mscale
           DSA_F32 if x.dtype == torch.float32 else DSA_BF16,
           _arg(pos, "pos", torch.int32, x.shape[:-2], dev),
           _arg(inv_freq, "inv_freq", torch.float32, (rot // 2,), dev), pos.numel(), H, D, off, rot,
-          code, mscale, 1 if inverse else 0)
+          code, float(mscale), 1 if inverse else 0)
     return out
 
 
@@ -914,6 +914,6 @@ def dsa_latent_attn(Q, cache, page_table, lens, scale: float, fmt: str = "e4m3",
         raise ValueError(f"ws is on {ws.device}, the other arguments on {dev}")
     _call(lib.dsa_latent_attn, "dsa_latent_attn", dev, stream, qp, cp, _CACHE_FORMATS[fmt],
           cache.shape[0], cache.shape[1], tp, page_table.shape[1], lp, ip, k, B, Sq, H, Dc, Dr,
-          scale, op, ep, None if ws is None else _dev(ws, "ws"),
+          float(scale), op, ep, None if ws is None else _dev(ws, "ws"),
           0 if ws is None else ws.numel() * ws.element_size())
     return O, lse

@@ -566,7 +566,7 @@ int dsa_latent_attn(const void* Q, const void* cache, int fmt, int64_t num_pages
   for (const void* ptr : ptrs)
     if (!aligned16(ptr)) return DSA_ERR_INVALID_ARG;
   if (Dc != 512 || Dr != 64 || H > 128) return DSA_ERR_UNSUPPORTED;
-  if (!(scale > 0.f) || scale > 3.0e38f) return DSA_ERR_UNSUPPORTED;
+  if (!(scale > 0.f) || scale > 2.0e38f) return DSA_ERR_UNSUPPORTED;   // times log2(e) finite
   // positions, slots and query rows are counted in 32 bits
   if (num_pages >= (1LL << 31) || num_pages * page_size >= (1LL << 31) ||
       static_cast<long long>(max_pages) * page_size >= (1LL << 31) ||

@@ -64,7 +64,8 @@ constexpr int kGatherThreads = 32 * kGatherWarps;
 constexpr int kKeysPerWarp = kNK / kGatherWarps;
 constexpr int kThreads = 32 * (kGatherWarp0 + kGatherWarps);
 constexpr uint32_t kColQ = 0, kColS = 144, kColO = 256;
-constexpr int kMinChunks = 4;            // chunks that a cluster takes at least
+constexpr int kMinChunks = 3;            // chunks that a cluster takes at least: 1000 keys of
+                                         // four sequences 16.3 us, with two 18.4, four 18.6
 constexpr int kMaxClusters = 80;         // clusters that the workspace has room for
 constexpr float kRescaleLog2 = 8.f;      // refresh the running max when it grows by > 2^8
 constexpr int kErrIdx = DSA_STAGE_LATENT | DSA_DEVERR_BAD_INDEX;
@@ -1065,14 +1066,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // Joins the parts of a tile that several clusters worked on: block (c, y, z) the tile that begins
-// in cluster c's range and goes on behind it, rows [32 y, 32 y + 32) (one per lane) and dims
-// [128 z, 128 z + 128) (16 per warp). The parts' maxima are fetched side by side first, then two
-// parts' dims at a time: one after the other, their latencies took longer than the attention of a
-// short cache.
-constexpr int kJoinThreads = 256;
-__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const Params p) {
-  extern __shared__ __align__(1024) uint8_t smem[];
-  float2* ml = reinterpret_cast<float2*>(smem);   // [parts][32]
+// in cluster c's range and goes on behind it, rows [32 y, 32 y + 32), one per lane. With few parts
+// a tile each warp takes 16 of the block's 128 dims. With many (SHARE: a single long sequence has
+// one per cluster) a block has 16 dims and its warps share the parts, since one after the other
+// their latencies took longer than the attention itself: 32768 keys 39 us instead of 66. The
+// other way round 75 tiles of two parts take 30 us longer shared.
+constexpr int kJoinWarps = 8, kJoinD4 = 4;   // warps of a block, groups of four dims of a warp
+template <bool SHARE>
+__global__ void __launch_bounds__(32 * kJoinWarps) latent_join_kernel(const Params p) {
+  __shared__ float2 ml[kMaxClusters][32];
+  __shared__ float4 acc[SHARE ? kJoinWarps : 1][kJoinD4][33];
+  __shared__ float sum[32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int2 tile = __ldcg(p.joins + blockIdx.x);
   if (tile.x < 0) return;
@@ -1084,49 +1088,76 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const Params 
     rows = tile_rows(p, mt);
     r0 = static_cast<long long>(b) * p.a.Sq * p.a.H + mt * 128;
   }
-  if (static_cast<int>(blockIdx.y) * 32 >= rows) return;
+  rows -= blockIdx.y * 32;   // left from this block's first on
+  r0 += blockIdx.y * 32;
+  if (rows <= 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.y * 32 + lane;
   // part 1 of the first cluster, part 0 of the others
   auto part_of = [&](int i) { return static_cast<long long>(2 * (first + i) + (i == 0)); };
-  for (int i = warp; i < parts; i += kJoinThreads / 32)
-    ml[i * 32 + lane] = __ldcg(p.ml + part_of(i) * p.prow + row);
+  for (int i = warp; i < parts; i += kJoinWarps)
+    ml[i][lane] = __ldcg(p.ml + part_of(i) * p.prow + row);
   __syncthreads();
-  float top = -INFINITY;
-  for (int i = 0; i < parts; ++i) top = fmaxf(top, ml[i * 32 + lane].x);
-  const int d4 = blockIdx.z * 32 + warp * 4;
-  float l = 0.f;
-  float4 o[4];
+  float top = -INFINITY, l = 0.f;
+  for (int i = 0; i < parts; ++i) top = fmaxf(top, ml[i][lane].x);
+  // a part without a key has m = -inf, l = 0 and O = 0; one with a NaN keeps it in l
+  auto weight = [&](float2 q) {
+    return q.x == -INFINITY ? (q.y == 0.f ? 0.f : 1.f) : exp2f(q.x - top);
+  };
+  const int d4 = SHARE ? blockIdx.z * kJoinD4 : (blockIdx.z * kJoinWarps + warp) * kJoinD4;
+  float4 o[kJoinD4];
 #pragma unroll
-  for (int d = 0; d < 4; ++d) o[d] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-  for (int i = 0; i < parts; ++i) {
+  for (int d = 0; d < kJoinD4; ++d) o[d] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = SHARE ? warp : 0; i < parts; i += SHARE ? kJoinWarps : 1) {
     const float4* src = p.part + (part_of(i) * (kDc / 4) + d4) * p.prow + row;
-    float4 x[4];
+    float4 x[kJoinD4];
 #pragma unroll
-    for (int d = 0; d < 4; ++d) x[d] = __ldcg(src + d * p.prow);
-    // a part without a key has m = -inf, l = 0 and O = 0; one with a NaN keeps it in l
-    const float2 q = ml[i * 32 + lane];
-    const float w = q.x == -INFINITY ? (q.y == 0.f ? 0.f : 1.f) : exp2f(q.x - top);
-    l += w * q.y;
+    for (int d = 0; d < kJoinD4; ++d) x[d] = __ldcg(src + d * p.prow);
+    const float w = weight(ml[i][lane]);
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
+    for (int d = 0; d < kJoinD4; ++d) {
       o[d].x += w * x[d].x;
       o[d].y += w * x[d].y;
       o[d].z += w * x[d].z;
       o[d].w += w * x[d].w;
     }
   }
-  if (row >= rows) return;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint4* out = reinterpret_cast<uint4*>(p.a.O + (r0 + row) * kDc + d4 * 4);
+  if (!SHARE || warp == 0)
+    for (int i = 0; i < parts; ++i) l += weight(ml[i][lane]) * ml[i][lane].y;
+  if (blockIdx.z == 0 && warp == 0 && lane < rows)
+    p.a.lse[r0 + lane] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994530942f;
+  auto pack4 = [](float4 v, float inv) {
+    return make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+  };
+  if (!SHARE) {
+    if (lane >= rows) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint4* out = reinterpret_cast<uint4*>(p.a.O + (r0 + lane) * kDc + d4 * 4);
 #pragma unroll
-  for (int d = 0; d < 2; ++d)
-    out[d] = make_uint4(pack_bf16(o[2 * d].x * inv, o[2 * d].y * inv),
-                        pack_bf16(o[2 * d].z * inv, o[2 * d].w * inv),
-                        pack_bf16(o[2 * d + 1].x * inv, o[2 * d + 1].y * inv),
-                        pack_bf16(o[2 * d + 1].z * inv, o[2 * d + 1].w * inv));
-  if (blockIdx.z == 0 && warp == 0)
-    p.a.lse[r0 + row] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994530942f;
+    for (int d = 0; d < kJoinD4; d += 2) {
+      const uint2 a = pack4(o[d], inv), b = pack4(o[d + 1], inv);
+      out[d / 2] = make_uint4(a.x, a.y, b.x, b.y);
+    }
+    return;
+  }
+  if (warp == 0) sum[lane] = l;
+#pragma unroll
+  for (int d = 0; d < kJoinD4; ++d) acc[SHARE ? warp : 0][d][lane] = o[d];
+  __syncthreads();
+  // four threads per row, four dims each
+  const int out_row = threadIdx.x / kJoinD4, d = threadIdx.x % kJoinD4;
+  if (out_row >= min(rows, 32)) return;
+  float4 v = acc[0][d][out_row];
+#pragma unroll
+  for (int w = 1; w < (SHARE ? kJoinWarps : 1); ++w) {
+    const float4 x = acc[w][d][out_row];
+    v.x += x.x;
+    v.y += x.y;
+    v.z += x.z;
+    v.w += x.w;
+  }
+  *reinterpret_cast<uint2*>(p.a.O + (r0 + out_row) * kDc + (d4 + d) * 4) =
+      pack4(v, sum[out_row] == 0.f ? 0.f : 1.f / sum[out_row]);
 }
 
 int part_rows(int Sq, int H, int k) {
@@ -1187,13 +1218,16 @@ int launch(Params p, cudaStream_t stream) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.clusters - 1, p.prow / 32, kDc / 128);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(p.clusters) * 32 * sizeof(float2);
+  const bool share = p.items <= 8;   // few tiles: many parts each, or few blocks otherwise
+  cfg.gridDim = dim3(p.clusters - 1, p.prow / 32, kDc / (4 * kJoinD4) / (share ? 1 : kJoinWarps));
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, latent_join_kernel, p) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, share ? latent_join_kernel<true> : latent_join_kernel<false>,
+                            p) == cudaSuccess
+             ? DSA_OK
+             : DSA_ERR_CUDA;
 }
 
 }  // namespace
