@@ -21,6 +21,7 @@ Entry points (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -722,7 +723,10 @@ def _code(value, table: dict, name: str) -> int:
 
 
 def _arg(t, name: str, dtype, shape, device) -> int:
-    """A tensor argument: its type, shape and device checked, its address returned."""
+    """A tensor argument: its type, shape and (CUDA) device checked, its address returned."""
+    if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape
+            and t.device == device and t.is_contiguous()):
+        return t.data_ptr()
     p = _dev(t, name, dtype)
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -818,6 +822,7 @@ def dsa_rope(x, pos, inv_freq, off: int = 0, layout: str = "interleaved", mscale
     return out
 
 
+@functools.lru_cache(maxsize=None)
 def cache_row_bytes(Dc: int, Dr: int, fmt: str = "e4m3") -> int:
     """Bytes of one cache row (0: dims that the cache does not support)."""
     return lib.dsa_cache_row_bytes(_code(fmt, _CACHE_FORMATS, "fmt"), Dc, Dr)
@@ -866,6 +871,7 @@ def dsa_cache_read(cache, slots, Dc: int, Dr: int, fmt: str = "e4m3", kv=None, s
     return kv
 
 
+@functools.lru_cache(maxsize=1024)
 def latent_attn_workspace_bytes(B, Sq, H, Dc, Dr, k=0) -> int:
     return int(lib.dsa_latent_attn_workspace_size(B, Sq, H, Dc, Dr, k))
 

@@ -153,6 +153,17 @@ __device__ __forceinline__ int tile_rows(const Params& p, int mt) {
   return min(128, p.a.Sq * p.a.H - mt * 128);
 }
 
+// first row of tile `item` in Q, O and lse, and the rows it has
+__device__ __forceinline__ long long rows_of(const Params& p, int item, int& rows) {
+  if (p.a.idx) {
+    rows = p.a.H;
+    return static_cast<long long>(item) * p.a.H;
+  }
+  const int b = item / p.tiles, mt = item - b * p.tiles;
+  rows = tile_rows(p, mt);
+  return static_cast<long long>(b) * p.a.Sq * p.a.H + mt * 128;
+}
+
 // keys that the last row of a tile sees
 __device__ __forceinline__ int tile_keys(const Params& p, int len, int mt) {
   const int i1 = (mt * 128 + tile_rows(p, mt) - 1) / p.a.H;
@@ -465,6 +476,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     struct Slot {
       int slot, item, cf, lim0;
     };
+    // the next tile's Q, to be read by the softmax warps some chunks later, on its way to L2
+    auto prefetch_q = [&](int item) {
+      int rows;
+      const long long r0 = rows_of(p, item, rows);
+      for (int i = gw * 32 + lane; i < rows * 5; i += kGatherThreads) {
+        const int row = i / 5, piece = i - row * 5;
+        const uint16_t* at = p.a.Q + (r0 + row) * kD +
+                             (piece < 4 ? rank * kHalf + piece * 64 : kDc + rank * kHalfR);
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+      }
+    };
     auto look = [&]() {
       Entry e = {-1, 0, 0, 0, 0, 0, 0};
       // chunk k.c + i of the tile, the (made + i)-th of the range
@@ -501,6 +523,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           } else if (++k.c == k.nch) {
             enter_item(p, k.item + 1, k);
             k.c = 0;
+            prefetch_q(k.item);
           }
         }
       }
@@ -776,20 +799,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const float c2 = p.scale_log2;
     const int H = p.a.H;
     const uint32_t peer = rank ^ 1u;
-    // the tile's first row of Q / O / lse, and the rows it has
-    auto rows_at = [&](int item, int& rows) {
-      if (p.a.idx) {
-        rows = H;
-        return static_cast<long long>(item) * H;
-      }
-      const int b = item / p.tiles, mt = item - b * p.tiles;
-      rows = tile_rows(p, mt);
-      return static_cast<long long>(b) * p.a.Sq * H + mt * 128;
-    };
     // this CTA's dims of the row of Q, packed bf16 pairs, into the thread's TMEM lane
     auto load_q = [&](int item) {
       int rows;
-      const long long r0 = rows_at(item, rows);
+      const long long r0 = rows_of(p, item, rows);
       const bool in = hrow < rows;
       const uint4* src = reinterpret_cast<const uint4*>(p.a.Q + (in ? r0 + hrow : 0) * kD);
       const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -874,7 +887,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         cur = item;
         m = -INFINITY;
         l = 0.f;
-        r0 = rows_at(item, rows);
+        r0 = rows_of(p, item, rows);
         // keys that this row sees: the tile's first token sees lim0, each later one one more
         if (!p.a.idx) lim = h.lim0 + (static_cast<int>(r0 % H) + hrow) / H;
       }
@@ -1081,13 +1094,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) latent_join_kernel(const Para
   const int2 tile = __ldcg(p.joins + blockIdx.x);
   if (tile.x < 0) return;
   const int first = blockIdx.x, parts = tile.y - first + 1;
-  int rows = p.a.H;
-  long long r0 = static_cast<long long>(tile.x) * p.a.H;
-  if (!p.a.idx) {
-    const int b = tile.x / p.tiles, mt = tile.x - b * p.tiles;
-    rows = tile_rows(p, mt);
-    r0 = static_cast<long long>(b) * p.a.Sq * p.a.H + mt * 128;
-  }
+  int rows;
+  long long r0 = rows_of(p, tile.x, rows);
   rows -= blockIdx.y * 32;   // left from this block's first on
   r0 += blockIdx.y * 32;
   if (rows <= 0) return;
