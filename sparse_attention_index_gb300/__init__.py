@@ -17,6 +17,7 @@ Entry points (same names as the C ABI):
 * ``dsa_rope`` - rotary positions on part of each head, and their inverse (the gradient)
 * ``dsa_cache_write`` / ``dsa_cache_read`` - rows of the paged latent cache (bf16 or e4m3)
 * ``dsa_latent_attn`` - attention of the newest tokens over that cache -> (O, lse)
+* ``dsa_decode_layer`` - these together, one serving step
 """
 from __future__ import annotations
 
@@ -923,3 +924,29 @@ def dsa_latent_attn(Q, cache, page_table, lens, scale: float, fmt: str = "e4m3",
           float(scale), op, ep, None if ws is None else _dev(ws, "ws"),
           0 if ws is None else ws.numel() * ws.element_size())
     return O, lse
+
+
+def dsa_decode_layer(Q, kv, pos, inv_freq, slots, cache, page_table, lens, scale: float,
+                     fmt: str = "e4m3", idx=None, mscale: float = 1.0, layout: str = "interleaved",
+                     Dc: int = 512, ws=None, stream=None):
+    """The attention of one serving step: rotary positions on the positional dims of Q and of the
+    new rows, the rows into the cache, the new tokens' attention over it -> (O, lse).
+
+    Q [B,Sq,H,Dc+Dr] and kv [B,Sq,Dc+Dr] bf16 before their rotation (neither is changed), pos and
+    slots int32 [B,Sq] (the new tokens' positions and cache slots, -1 for padding), inv_freq fp32
+    [Dr/2]; the rest as for dsa_latent_attn, with lens counting the new tokens.
+    """
+    if not isinstance(kv, torch.Tensor) or kv.dim() != 3:
+        raise ValueError("kv must be [B, Sq, Dc + Dr]")
+    B, Sq, D = kv.shape
+    rows = dsa_rope(kv.view(B, Sq, 1, D), pos, inv_freq, off=Dc, layout=layout, mscale=mscale,
+                    stream=stream)
+    dsa_cache_write(rows.view(B * Sq, D), slots.view(B * Sq), cache, Dc, fmt=fmt, stream=stream)
+    q = dsa_rope(Q, pos, inv_freq, off=Dc, layout=layout, mscale=mscale, stream=stream)
+    out = dsa_latent_attn(q, cache, page_table, lens, scale, fmt=fmt, idx=idx, Dc=Dc, ws=ws,
+                          stream=stream)
+    if stream is not None:   # this call's own tensors are freed on the current stream
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream)
+        for t in (rows, q):
+            t.record_stream(s)
+    return out

@@ -592,3 +592,71 @@ def test_prompt_with_the_selection_of_the_top_k(dsa):
     O, lse = dsa.dsa_latent_attn(Q, cache, table, i32([S]), 192 ** -0.5, fmt="bf16", idx=idx)
     no_error(dsa)
     attn_check(O, lse, Q, rows, [S], 192 ** -0.5, idx)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("side", [False, True])
+def test_decode_layer(dsa, fmt, side):
+    """One serving step gives what its parts give, in a padded batch, on any stream."""
+    B, Sq, H, page, lens = 4, 2, 16, 16, [37, 0, 2, 160]
+    cache, table, rows = make_cache(dsa, lens, page, fmt, 101)
+    inv, m = dsa.rope_frequencies(DR, scaling="yarn", factor=8.0)
+    g = gen(102)
+    Q = torch.randn(B, Sq, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    kv = torch.randn(B, Sq, D, generator=g, device="cuda").to(torch.bfloat16)
+    n = i32(lens)
+    pos = (n[:, None] - Sq + torch.arange(Sq, device="cuda")).clamp(min=0).to(torch.int32)
+    at = pos.long()
+    slots = (table.long().gather(1, at // page) * page + at % page).to(torch.int32)
+    slots[1] = -1                                    # the padded sequence
+    Q0, kv0 = Q.clone(), kv.clone()
+    one = cache.clone()
+    stream = None
+    if side:
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+    O, lse = dsa.dsa_decode_layer(Q, kv, pos, inv, slots, one, table, n, 0.07, fmt=fmt, mscale=m,
+                                  stream=stream)
+    if side:
+        torch.cuda.current_stream().wait_stream(stream)
+    assert torch.equal(Q, Q0) and torch.equal(kv, kv0)
+    rot = dsa.dsa_rope(kv[:, :, None].contiguous(), pos, inv, off=DC, mscale=m)
+    dsa.dsa_cache_write(rot.view(-1, D), slots.view(-1), cache, DC, fmt=fmt)
+    q = dsa.dsa_rope(Q, pos, inv, off=DC, mscale=m)
+    O2, lse2 = dsa.dsa_latent_attn(q, cache, table, n, 0.07, fmt=fmt)
+    assert torch.equal(one, cache) and torch.equal(O, O2) and torch.equal(lse, lse2)
+    no_error(dsa)
+    assert not O[1].any() and bool((lse[1] == -math.inf).all())
+    new = dsa.dsa_cache_read(cache, slots.view(-1), DC, DR, fmt=fmt).double().view(B, Sq, D)
+    for b, k in enumerate(lens):
+        if k:
+            rows[b][k - Sq:] = new[b]
+    attn_check(O, lse, q, rows, lens, 0.07)
+
+
+def test_concurrent_calls(dsa):
+    """Two streams with a workspace each, e4m3 calls on one and bf16 calls on the other at once."""
+    cases = []
+    for fmt, H, lens in (("e4m3", 128, [5000, 300]), ("bf16", 16, [7, 2000, 64])):
+        cache, table, rows = make_cache(dsa, lens, 64, fmt, 111)
+        Q = torch.randn(len(lens), 1, H, D, generator=gen(112), device="cuda").to(torch.bfloat16)
+        cases.append((Q, cache, table, i32(lens), fmt, rows, lens))
+    wss = [torch.empty(dsa.latent_attn_workspace_bytes(c[0].shape[0], 1, c[0].shape[2], DC, DR),
+                       dtype=torch.uint8, device="cuda") for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = []
+    for _ in range(5):
+        for st, ws, (Q, cache, table, n, fmt, _, _) in zip(streams, wss, cases):
+            O = torch.empty(*Q.shape[:3], DC, dtype=torch.bfloat16, device="cuda")
+            outs.append((O, torch.empty(Q.shape[:3], device="cuda")))
+    torch.cuda.synchronize()
+    for i, (O, lse) in enumerate(outs):
+        Q, cache, table, n, fmt, _, _ = cases[i % 2]
+        dsa.dsa_latent_attn(Q, cache, table, n, 0.07, fmt=fmt, O=O, lse=lse, ws=wss[i % 2],
+                            stream=streams[i % 2])
+    torch.cuda.synchronize()
+    for i, (O, lse) in enumerate(outs):
+        assert torch.equal(O, outs[i % 2][0]) and torch.equal(lse, outs[i % 2][1])
+    for (O, lse), (Q, _, _, _, _, rows, lens) in zip(outs, cases):
+        attn_check(O, lse, Q, rows, lens, 0.07)
+    no_error(dsa)
