@@ -742,7 +742,7 @@ def _call(fn, where: str, device, stream, *args):
     numbers alone, without building torch's objects.)"""
     i = device.index
     s = torch._C._cuda_getCurrentRawStream(i) if stream is None else _stream(stream)
-    if i == torch.cuda.current_device():
+    if i == torch._C._cuda_getDevice():
         rc = fn(*args, s)
     else:
         with torch.cuda.device(i):

@@ -38,6 +38,10 @@
 //               of two.
 // P goes to the tensor cores through shared memory, so that a chunk's S columns are free again
 // once they have been read. TMEM: [Q: 144][S: 2 x 48][pad 16][O: 256] = 512 columns.
+//
+// Measured: four sequences of 131072 e4m3 rows, 128 heads: 237 us, 616 TFLOP/s, 1.45 TB/s; 32
+// sequences of 256 to 8192 bf16 rows: 84 us. A chunk takes about 1900 cycles in steady state (bf16;
+// 2800 with e4m3) of which the products are 1190: the hand-offs between the warps pace it.
 
 #include <mutex>
 
