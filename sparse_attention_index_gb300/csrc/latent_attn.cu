@@ -70,6 +70,8 @@ constexpr int kThreads = 32 * (kGatherWarp0 + kGatherWarps);
 constexpr uint32_t kColQ = 0, kColS = 144, kColO = 256;
 constexpr int kMinChunks = 3;            // chunks that a cluster takes at least: 1000 keys of
                                          // four sequences 16.3 us, with two 18.4, four 18.6
+constexpr int kTileCost = 5;             // chunks that a change of tiles is worth: 128 ragged
+                                         // sequences up to 2000 keys 86 us, 154 with none
 constexpr int kMaxClusters = 80;         // clusters that the workspace has room for
 constexpr float kRescaleLog2 = 8.f;      // refresh the running max when it grows by > 2^8
 constexpr int kErrIdx = DSA_STAGE_LATENT | DSA_DEVERR_BAD_INDEX;
@@ -118,8 +120,11 @@ struct Tail {
   uint32_t tmem_base;
   int abort_flag;
   long long sums[kThreads / 32];
-  // this cluster's range: its first tile, that tile's first chunk here, chunks in all
-  int item0, c0, n, each;
+  // this cluster's range: its first tile, that tile's first chunk here, the chunks of all tiles in
+  // front of the range and of its end, and a range's weight
+  int item0, c0;
+  long long first, end;
+  int each;
 };
 
 static_assert(Layout<false>::kTailOff + sizeof(Tail) <= kSmemMost &&
@@ -183,12 +188,16 @@ __device__ __forceinline__ int item_chunks(const Params& p, int item) {
   return chunks_of(tile_keys(p, seq_len(p.a, b, false), item - b * p.tiles));
 }
 
-// What a cluster takes of the chunks of all tiles: [c0, ...) of tile item0, n chunks in all, `each`
-// per cluster. Every thread of the block calls it; the thread that finds the tile returns true.
-__device__ __forceinline__ bool my_chunks(const Params& p, int cluster, long long* sums, int& item0,
-                                          int& c0, int& n, long long& each) {
-  long long total, before = 0, s = 0;
-  int i0 = 0, i1 = 0;
+// What a cluster takes of the chunks of all tiles, into the tail: [c0, ...) of tile item0, n chunks
+// in all. Every thread of the block calls it, before a barrier.
+//
+// The chunks are cut by weight: going on to another tile costs about as much as kTileCost chunks
+// (its Q, an empty pipeline, an output), so a tile weighs that much in front of its chunks. Cluster
+// c has the chunks at weights [each c, each (c + 1)). Short ranges count no such cost: they would be
+// cut into setups alone.
+__device__ __forceinline__ void my_chunks(const Params& p, int cluster, Tail* tail) {
+  long long total, before = 0, s = 0;   // chunks: of all tiles, in front of this thread's, of its own
+  int i0 = 0, i1 = 0;                   // this thread's tiles
   if (p.a.idx) {
     total = static_cast<long long>(p.items) * p.list_chunks;
   } else {
@@ -203,35 +212,51 @@ __device__ __forceinline__ bool my_chunks(const Params& p, int cluster, long lon
       const long long v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
-    if (lane == 31) sums[warp] = incl;
+    if (lane == 31) tail->sums[warp] = incl;
     __syncthreads();
     total = 0;
     for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += sums[w];
-      total += sums[w];
+      if (w < warp) before += tail->sums[w];
+      total += tail->sums[w];
     }
     before += incl - s;
   }
-  each = max((total + p.clusters - 1) / p.clusters, static_cast<long long>(kMinChunks));
-  const long long g0 = each * cluster;
-  if (g0 >= total) return false;
-  n = static_cast<int>(min(each, total - g0));
+  const int cost = (total + p.clusters - 1) / p.clusters >= 4 * kTileCost ? kTileCost : 0;
+  const long long weight = total + static_cast<long long>(cost) * p.items;
+  const long long each =
+      max((weight + p.clusters - 1) / p.clusters, static_cast<long long>(kMinChunks));
+  const long long w0 = each * cluster, w1 = min(w0 + each, weight);
+  if (threadIdx.x == 0) tail->each = static_cast<int>(each);
+  if (w0 >= weight) return;   // first and end stay 0
+  if (w1 == weight && threadIdx.x == 0) tail->end = total;
   if (p.a.idx) {
-    item0 = static_cast<int>(g0 / p.list_chunks);
-    c0 = static_cast<int>(g0 - static_cast<long long>(item0) * p.list_chunks);
-    return threadIdx.x == 0;
+    if (threadIdx.x != 0) return;
+    const int per = cost + p.list_chunks;
+    // chunks in front of weight w
+    auto chunk_at = [&](long long w, int& item, int& c) {
+      item = static_cast<int>(w / per);
+      c = max(0, static_cast<int>(w - static_cast<long long>(item) * per) - cost);
+      return static_cast<long long>(item) * p.list_chunks + c;
+    };
+    int item, c;
+    if (w1 < weight) tail->end = chunk_at(w1, item, c);
+    tail->first = chunk_at(w0, tail->item0, tail->c0);
+    return;
   }
-  if (g0 < before || g0 >= before + s) return false;
+  long long at = before + static_cast<long long>(cost) * i0;   // weight in front of tile i
   for (int i = i0; i < i1; ++i) {
-    const int m = item_chunks(p, i);
-    if (g0 < before + m) {
-      item0 = i;
-      c0 = static_cast<int>(g0 - before);
-      return true;
+    const int m = i1 - i0 == 1 ? static_cast<int>(s) : item_chunks(p, i);
+    const long long end = at + cost + m;
+    if (w0 >= at && w0 < end) {
+      const int c = max(0, static_cast<int>(w0 - at) - cost);
+      tail->item0 = i;
+      tail->c0 = c;
+      tail->first = before + c;
     }
+    if (w1 >= at && w1 < end) tail->end = before + max(0, static_cast<int>(w1 - at) - cost);
+    at = end;
     before += m;
   }
-  return false;
 }
 
 // ------------------------------------------------------------------ small helpers
@@ -430,7 +455,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&tail->drain[0], 1);
     mbar_init(&tail->drain[1], 1);
     tail->abort_flag = 0;
-    tail->n = 0;
+    tail->first = tail->end = 0;
     fence_mbar_init();
   }
   if (warp == kIssueWarp) {
@@ -440,21 +465,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // thread 0 has made this CTA's barriers; the peer's are ready once cluster_wait returns
   cluster_arrive();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  {
-    int i0, c, m;
-    long long each;
-    if (my_chunks(p, cluster, tail->sums, i0, c, m, each)) {
-      tail->item0 = i0;
-      tail->c0 = c;
-      tail->n = m;
-      tail->each = static_cast<int>(each);
-    }
-  }
+  my_chunks(p, cluster, tail);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tail->tmem_base;
-  const int n = tail->n, item0 = tail->item0, c0 = tail->c0;
+  const int n = static_cast<int>(tail->end - tail->first), item0 = tail->item0, c0 = tail->c0;
 
   if (n == 0) {
     // nothing here (both CTAs agree)
