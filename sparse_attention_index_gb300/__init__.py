@@ -736,6 +736,19 @@ def _arg(t, name: str, dtype, shape, device) -> int:
     return p
 
 
+def _empty(shape, dtype, device, stream):
+    """An output or workspace of a call on `stream`. It belongs to that stream's memory, as if the
+    call were made with the stream current: work still queued on the current one does not reach
+    it, and a workspace that is dropped at the end of a call goes to later calls on its stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream)
+                  else torch.cuda.default_stream(device))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _call(fn, where: str, device, stream, *args):
     """fn(*args, stream) on `device`, on its current stream where none is given. (A single-token
     call is short beside the host's work, so the current device and stream are asked for their
@@ -812,9 +825,9 @@ def dsa_rope(x, pos, inv_freq, off: int = 0, layout: str = "interleaved", mscale
     xp = _dev(x, "x")
     H, D = x.shape[-2:]
     rot = 2 * inv_freq.numel()
-    if out is None:
-        out = torch.empty_like(x)
     dev = x.device
+    if out is None:
+        out = _empty(x.shape, x.dtype, dev, stream)
     _call(lib.dsa_rope, "dsa_rope", dev, stream, xp, _arg(out, "out", x.dtype, x.shape, dev),
           DSA_F32 if x.dtype == torch.float32 else DSA_BF16,
           _arg(pos, "pos", torch.int32, x.shape[:-2], dev),
@@ -865,7 +878,7 @@ def dsa_cache_read(cache, slots, Dc: int, Dr: int, fmt: str = "e4m3", kv=None, s
     N, dev = slots.shape[0], slots.device
     cp, num = _cache_arg(cache, Dc, Dr, fmt, dev)
     if kv is None:
-        kv = torch.empty((N, Dc + Dr), dtype=torch.bfloat16, device=dev)
+        kv = _empty((N, Dc + Dr), torch.bfloat16, dev, stream)
     kp = _arg(kv, "kv", torch.bfloat16, (N, Dc + Dr), dev)
     _call(lib.dsa_cache_read, "dsa_cache_read", dev, stream, cp, num, _CACHE_FORMATS[fmt], sp, N,
           Dc, Dr, kp)
@@ -887,7 +900,7 @@ def dsa_latent_attn(Q, cache, page_table, lens, scale: float, fmt: str = "e4m3",
     -> (O bf16 [B,Sq,H,Dc], lse fp32 [B,Sq,H]).
 
     ws: a device byte buffer of at least latent_attn_workspace_bytes(...) (allocated here if
-    None).
+    None). What is allocated here is allocated on `stream`.
     """
     qp = _dev(Q, "Q", torch.bfloat16)
     if Q.dim() != 4 or Q.shape[3] < Dc:
@@ -909,14 +922,14 @@ def dsa_latent_attn(Q, cache, page_table, lens, scale: float, fmt: str = "e4m3",
     tp = _arg(page_table, "page_table", torch.int32, (B, page_table.shape[1]), dev)
     lp = _arg(lens, "lens", torch.int32, (B,), dev)
     if O is None:
-        O = torch.empty((B, Sq, H, Dc), dtype=torch.bfloat16, device=dev)
+        O = _empty((B, Sq, H, Dc), torch.bfloat16, dev, stream)
     if lse is None:
-        lse = torch.empty((B, Sq, H), dtype=torch.float32, device=dev)
+        lse = _empty((B, Sq, H), torch.float32, dev, stream)
     op = _arg(O, "O", torch.bfloat16, (B, Sq, H, Dc), dev)
     ep = _arg(lse, "lse", torch.float32, (B, Sq, H), dev)
     need = latent_attn_workspace_bytes(B, Sq, H, Dc, Dr, k)
     if ws is None and need > 0:
-        ws = torch.empty((need,), dtype=torch.uint8, device=dev)
+        ws = _empty((need,), torch.uint8, dev, stream)
     if ws is not None and ws.device != dev:
         raise ValueError(f"ws is on {ws.device}, the other arguments on {dev}")
     _call(lib.dsa_latent_attn, "dsa_latent_attn", dev, stream, qp, cp, _CACHE_FORMATS[fmt],
@@ -943,10 +956,5 @@ def dsa_decode_layer(Q, kv, pos, inv_freq, slots, cache, page_table, lens, scale
                     stream=stream)
     dsa_cache_write(rows.view(B * Sq, D), slots.view(B * Sq), cache, Dc, fmt=fmt, stream=stream)
     q = dsa_rope(Q, pos, inv_freq, off=Dc, layout=layout, mscale=mscale, stream=stream)
-    out = dsa_latent_attn(q, cache, page_table, lens, scale, fmt=fmt, idx=idx, Dc=Dc, ws=ws,
-                          stream=stream)
-    if stream is not None:   # this call's own tensors are freed on the current stream
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream)
-        for t in (rows, q):
-            t.record_stream(s)
-    return out
+    return dsa_latent_attn(q, cache, page_table, lens, scale, fmt=fmt, idx=idx, Dc=Dc, ws=ws,
+                           stream=stream)

@@ -1112,8 +1112,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) latent_join_kernel(const Para
   __shared__ float sum[32];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int2 tile = __ldcg(p.joins + blockIdx.x);
-  if (tile.x < 0) return;
   const int first = blockIdx.x, parts = tile.y - first + 1;
+  // nothing to join, or not written: a cluster whose waits ran out (recorded) leaves what was there
+  if (tile.x < 0 || tile.x >= p.items || tile.y <= first || tile.y >= p.clusters) return;
   int rows;
   long long r0 = rows_of(p, tile.x, rows);
   rows -= blockIdx.y * 32;   // left from this block's first on

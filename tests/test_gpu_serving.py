@@ -660,3 +660,27 @@ def test_concurrent_calls(dsa):
     for (O, lse), (Q, _, _, _, _, rows, lens) in zip(outs, cases):
         attn_check(O, lse, Q, rows, lens, 0.07)
     no_error(dsa)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_memory_of_calls_on_another_stream(dsa, handle):
+    """Workspaces and outputs that a call on a side stream allocates are not handed to work that is
+    queued on the current stream meanwhile."""
+    lens = [4000, 900]
+    cache, table, rows = make_cache(dsa, lens, 64, "bf16", 121)
+    Q = torch.randn(2, 1, 128, D, generator=gen(122), device="cuda").to(torch.bfloat16)
+    n = i32(lens)
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if handle else side
+    size = dsa.latent_attn_workspace_bytes(2, 1, 128, DC, DR)
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(8):
+        outs.append(dsa.dsa_latent_attn(Q, cache, table, n, 0.07, fmt="bf16", stream=stream))
+        for _ in range(3):
+            torch.full((size,), 0xff, dtype=torch.uint8, device="cuda")   # on the current stream
+    torch.cuda.synchronize()
+    for O, lse in outs:
+        assert torch.equal(O, outs[0][0]) and torch.equal(lse, outs[0][1])
+    attn_check(*outs[0], Q, rows, lens, 0.07)
+    no_error(dsa)
