@@ -873,32 +873,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int st = g % kStages;
       const uint32_t par = (g >> 1) & 1;
       if (lane == 0) mbar_arrive_expect_tx(&tail->x_full[wg][quarter], 32 * kNK * 4);
-      bool ok = mbar_wait(&tail->s_full[wg], par, abort_flag, err, kErrTime);
-      // acquires the gather warps' header writes
-      ok = ok && mbar_wait(&tail->kv_full[st], (g / kStages) & 1, abort_flag, err, kErrTime);
-      // the peer has read what was sent two chunks ago
-      ok = ok && wait_peer(&tail->x_free[wg][quarter], par ^ 1u, abort_flag, err);
+      // what does not wait for S first: the header (the gather warps' writes), and the peer has read
+      // what was sent two chunks ago
+      bool ok = mbar_wait(&tail->kv_full[st], (g / kStages) & 1, abort_flag, err, kErrTime);
       if (!__all_sync(0xffffffffu, ok)) break;
-      tc_fence_after();
-      float2 s[kNK / 2];
-      uint32_t lo[32], hi[16];
-      tmem_ld_x32(sbase, lo);
-      tmem_ld_16(sbase + 32, hi);
-      tmem_ld_wait();
-      tc_fence_before();
-#pragma unroll
-      for (int j = 0; j < 32; j += 4)
-        st_peer(x_dst + j * 512, x_bar, lo[j], lo[j + 1], lo[j + 2], lo[j + 3]);
-#pragma unroll
-      for (int j = 0; j < 16; j += 4)
-        st_peer(x_dst + (32 + j) * 512, x_bar, hi[j], hi[j + 1], hi[j + 2], hi[j + 3]);
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        s[j] = make_float2(__uint_as_float(lo[2 * j]), __uint_as_float(lo[2 * j + 1]));
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        s[16 + j] = make_float2(__uint_as_float(hi[2 * j]), __uint_as_float(hi[2 * j + 1]));
-      mbar_arrive(&tail->s_free[wg]);
       const Header& h = tail->hdr[st];
       const int item = h.item, flags = h.cf & 15, c = h.cf >> 4;
       unsigned long long vm =
@@ -915,9 +893,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int left = lim - c * kNK;   // keys of the chunk that the row sees
         if (left < kNK) vm = left <= 0 ? 0ull : vm & ((1ull << left) - 1);
       }
-      if (!__all_sync(0xffffffffu,
-                      wait_peer(&tail->x_full[wg][quarter], par, abort_flag, err)))
-        break;
+      ok = wait_peer(&tail->x_free[wg][quarter], par ^ 1u, abort_flag, err);
+      ok = ok && mbar_wait(&tail->s_full[wg], par, abort_flag, err, kErrTime);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      float2 s[kNK / 2];
+      uint32_t lo[32], hi[16];
+      tmem_ld_x32(sbase, lo);
+      tmem_ld_16(sbase + 32, hi);
+      tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive(&tail->s_free[wg]);
+#pragma unroll
+      for (int j = 0; j < 32; j += 4)
+        st_peer(x_dst + j * 512, x_bar, lo[j], lo[j + 1], lo[j + 2], lo[j + 3]);
+#pragma unroll
+      for (int j = 0; j < 16; j += 4)
+        st_peer(x_dst + (32 + j) * 512, x_bar, hi[j], hi[j + 1], hi[j + 2], hi[j + 3]);
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        s[j] = make_float2(__uint_as_float(lo[2 * j]), __uint_as_float(lo[2 * j + 1]));
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        s[16 + j] = make_float2(__uint_as_float(hi[2 * j]), __uint_as_float(hi[2 * j + 1]));
+      // while the peer's half is on its way: the chunk before has settled the running maximum, and
+      // the P buffer's previous chunk has gone through the tensor cores
+      ok = g == 0 || mbar_wait(&tail->turn[wg ^ 1][quarter], ((g - 1) >> 1) & 1, abort_flag, err,
+                               kErrTime);
+      if (g >= 2) ok = ok && mbar_wait(&tail->pv_done[wg], par ^ 1u, abort_flag, err, kErrTime);
+      ok = ok && wait_peer(&tail->x_full[wg][quarter], par, abort_flag, err);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const float mr = (flags & 1) ? -INFINITY : tail->mref[hrow];
 #pragma unroll
       for (int j = 0; j < kNK / 4; ++j) {
         const float4 x = xr[j * 128];
@@ -941,13 +947,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane == 0) arrive_peer(x_ack, mx);
 
       // in the order of the chunks: the running maximum
-      if (g > 0 && !__all_sync(0xffffffffu, mbar_wait(&tail->turn[wg ^ 1][quarter],
-                                                      ((g - 1) >> 1) & 1, abort_flag, err,
-                                                      kErrTime)))
-        break;
-      float mn = mx, mr = -INFINITY;
+      float mn = mx;
       if (!(flags & 1)) {
-        mr = tail->mref[hrow];
         mn = mr;
         if (__any_sync(0xffffffffu,
                        mx > mr && (mr == -INFINITY || (mx - mr) * c2 > kRescaleLog2))) {
@@ -990,10 +991,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         l *= m == -INFINITY ? 0.f : exp2f((m - mn) * c2);
         m = mn;
       }
-      // the P buffer's previous chunk has gone through the tensor cores
-      if (g >= 2 && !__all_sync(0xffffffffu, mbar_wait(&tail->pv_done[wg], par ^ 1u, abort_flag,
-                                                       err, kErrTime)))
-        break;
       // P = exp2(S*c2 - m*c2) over the valid keys (exp2(-inf) = 0 elsewhere)
       const float base = m == -INFINITY ? 0.f : m * c2;
       const float2 cc = make_float2(c2, c2), bb = make_float2(-base, -base);
