@@ -39,9 +39,11 @@
 // P goes to the tensor cores through shared memory, so that a chunk's S columns are free again
 // once they have been read. TMEM: [Q: 144][S: 2 x 48][pad 16][O: 256] = 512 columns.
 //
-// Measured: four sequences of 131072 e4m3 rows, 128 heads: 237 us, 616 TFLOP/s, 1.45 TB/s; 32
-// sequences of 256 to 8192 bf16 rows: 84 us. A chunk takes about 1900 cycles in steady state (bf16;
-// 2800 with e4m3) of which the products are 1190: the hand-offs between the warps pace it.
+// Measured (device time): four sequences of 131072 e4m3 rows, 128 heads: 221 us, 660 TFLOP/s,
+// 1.56 TB/s; 32 sequences of 256 to 8192 bf16 rows: 69 us. A chunk takes about 1900 cycles in
+// steady state (bf16; 2600 with e4m3) of which the products are 1190: with bf16 the hand-offs
+// between the warps pace it, with e4m3 a gather warp's way through a chunk (copies 600, widening
+// 650, lookups 250, the fence and the waits), all of it in reach of the same shared memory.
 
 #include <mutex>
 
@@ -86,6 +88,8 @@ constexpr uint32_t kRawRope = kCodeReps * kGatherThreads * 16;
 constexpr uint32_t kRawScale = kRawRope + kGatherThreads * 16;
 constexpr uint32_t kRaw = kRawScale + kNK * 8;
 constexpr int kAhead = 2;
+// 2^7 as bf16: the largest scale that widens in one step
+constexpr uint32_t kScaleMost = 134u << 7;
 static_assert(kNK * (kHalfR / 8) == kGatherThreads, "one piece of positional dims per thread");
 
 template <bool FP8>
@@ -370,8 +374,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-__device__ __forceinline__ void cp_async_8(uint32_t dst, const void* src, uint32_t src_bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
                : "memory");
 }
 
@@ -386,7 +390,8 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 // subnormals of the other), so one exact multiply by 2^(120 + k), twice in `up`, widens and scales.
 // The bytes come out as (0, 2) and (1, 3), which needs no byte permutation: of every four latent
 // dims the middle two are swapped in the tile, in Q's columns (load_q) and in O's, and O is written
-// the right way round. (With the dims in order: selected e4m3 keys 138.6 us, long 240.)
+// the right way round. (With the dims in order: selected e4m3 keys 138.6 us, long 240; 133 and 225
+// this way, the rest by the loads and stores around it.)
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t up, uint32_t& even, uint32_t& odd) {
   even = mul_bf16x2(((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u), up);
   odd = mul_bf16x2(((w >> 4) & 0x07f007f0u) | (w & 0x80008000u), up);
@@ -637,6 +642,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // scales are the warp's.
       uint8_t* const raw = smem + L::kRawOff;
       const int gt = gw * 32 + lane;
+      // A thread's codes: piece pc of the warp's keys odd, 2 + odd, ... Eight lanes have the four
+      // pieces of an atom of an even and an odd key, which the tile's swizzle puts in eight
+      // different bank groups.
+      const int odd = (lane >> 2) & 1, pc = (lane >> 3) * 4 + (lane & 3);
       struct Ahead {
         uint32_t valid;
         int item, cf, lim0;
@@ -653,19 +662,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t rs = smem_u32(raw) + (g % kAhead) * kRaw;
 #pragma unroll
         for (int j = 0; j < kCodeReps; ++j) {
-          const int pc = lane & 15;   // two keys per instruction
-          const int s = __shfl_sync(0xffffffffu, now.slot, b8 + 2 * j + (lane >> 4));
+          const int s = __shfl_sync(0xffffffffu, now.slot, b8 + 2 * j + odd);
           cp_async_16(rs + (j * kGatherThreads + gt) * 16,
                       p.a.cache + (s >= 0 ? s : 0) * row_bytes + rank * kHalf + pc * 16,
                       s >= 0 ? 16u : 0u);
         }
-        const int s = __shfl_sync(0xffffffffu, now.slot, b8 + (lane >> 2));
-        const uint8_t* row = p.a.cache + (s >= 0 ? s : 0) * row_bytes + kDc;
-        cp_async_16(rs + kRawRope + gt * 16, row + 16 + rank * (2 * kHalfR) + (lane & 3) * 16,
-                    s >= 0 ? 16u : 0u);
-        if ((lane & 3) == 0)
-          cp_async_8(rs + kRawScale + (gw * kKeysPerWarp + (lane >> 2)) * 8, row + rank * 8,
-                     s >= 0 ? 8u : 0u);
+        {
+          const int s = __shfl_sync(0xffffffffu, now.slot, b8 + (lane >> 2));
+          cp_async_16(rs + kRawRope + gt * 16,
+                      p.a.cache + (s >= 0 ? s : 0) * row_bytes + kDc + 16 + rank * (2 * kHalfR) +
+                          (lane & 3) * 16,
+                      s >= 0 ? 16u : 0u);
+        }
+        {
+          // scale lane & 1 of key (lane >> 1) & 7, so that the four of a thread are 16 bytes
+          const int s = __shfl_sync(0xffffffffu, now.slot, b8 + ((lane >> 1) & 7));
+          if (lane < 16)
+            cp_async_4(rs + kRawScale + gw * 64 + ((lane & 3) * 4 + (lane >> 2)) * 4,
+                       p.a.cache + (s >= 0 ? s : 0) * row_bytes + kDc + rank * 8 + (lane & 1) * 4,
+                       s >= 0 ? 4u : 0u);
+        }
         cp_async_commit();
       };
       static_assert(kAhead == 2, "two chunks on their way");
@@ -673,25 +689,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int f = 0; f < n + kAhead; ++f) {
         const int g = f - kAhead;
         const Ahead r = a0;
-        // The halves of a piece in the other order in every second atom: eight lanes then store
-        // to eight different bank groups.
-        const int sw = (lane >> 2) & 1;
-        uint2 code[kCodeReps][2];
-        uint4 rope;
-        uint32_t scale[kCodeReps];
+        uint4 code[kCodeReps], rope, scales;
         if (g >= 0) {
           cp_async_wait<kAhead - 1>();
           __syncwarp();
           const uint8_t* rs = raw + (g % kAhead) * kRaw;
 #pragma unroll
-          for (int j = 0; j < kCodeReps; ++j) {
-            const uint8_t* at = rs + (j * kGatherThreads + gt) * 16;
-            code[j][0] = *reinterpret_cast<const uint2*>(at + 8 * sw);
-            code[j][1] = *reinterpret_cast<const uint2*>(at + 8 - 8 * sw);
-            scale[j] = *reinterpret_cast<const uint32_t*>(
-                rs + kRawScale + (gw * kKeysPerWarp + 2 * j + (lane >> 4)) * 8 +
-                ((lane >> 3) & 1) * 4);
-          }
+          for (int j = 0; j < kCodeReps; ++j)
+            code[j] = *reinterpret_cast<const uint4*>(rs + (j * kGatherThreads + gt) * 16);
+          scales = *reinterpret_cast<const uint4*>(rs + kRawScale + gw * 64 +
+                                                   (odd * 2 + (lane >> 4)) * 16);
           rope = *reinterpret_cast<const uint4*>(rs + kRawRope + gt * 16);
           __syncwarp();
         }
@@ -713,32 +720,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mbar_arrive(&tail->kv_full[st]);
           }
           uint8_t* stage = smem + st * kStage;
+          // the scales' upper halves: 2^k as bf16. (A key that is not there has codes and scale
+          // bits of zero.)
+          const uint32_t e[kCodeReps] = {scales.x >> 16, scales.y >> 16, scales.z >> 16,
+                                         scales.w >> 16};
+          // keys 2 j + odd of the warp's eight: rows of 128 bytes, their pieces swizzled by 2 j
+          uint8_t* const at = stage + (lane >> 3) * kAtom + (gw * kKeysPerWarp + odd) * 128;
+          const int put = ((lane & 3) * 2 ^ odd) << 4;
+          bool wide = false;
 #pragma unroll
           for (int j = 0; j < kCodeReps; ++j) {
-            const int pc = lane & 15, key = gw * kKeysPerWarp + 2 * j + (lane >> 4);
-            // 2^k as bf16 bits to 2^(120 + k). (A key that is not there has codes and scale bits
-            // of zero.)
-            const uint32_t e = scale[j] >> 16;
-            uint32_t up = (e + (120u << 7)) * 0x10001u;
-            const bool wide = e > (134u << 7);   // k > 7, or NaN: 2^127, and the rest below
-            if (wide) up = e > 0x7f80u ? 0x7fff7fffu : 0x7f007f00u;
-            uint4 w[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              widen4(code[j][h].x, up, w[h].x, w[h].y);
-              widen4(code[j][h].y, up, w[h].z, w[h].w);
-              if (wide) {
-                const uint32_t more = (e - (7u << 7)) * 0x10001u;
-                w[h].x = mul_bf16x2(w[h].x, more);
-                w[h].y = mul_bf16x2(w[h].y, more);
-                w[h].z = mul_bf16x2(w[h].z, more);
-                w[h].w = mul_bf16x2(w[h].w, more);
-              }
+            // 2^(120 + k) twice, or 2^127 and the rest below
+            const uint32_t up = (min(e[j], kScaleMost) + (120u << 7)) * 0x10001u;
+            wide = wide || e[j] > kScaleMost;
+            uint4 w0, w1;
+            widen4(code[j].x, up, w0.x, w0.y);
+            widen4(code[j].y, up, w0.z, w0.w);
+            widen4(code[j].z, up, w1.x, w1.y);
+            widen4(code[j].w, up, w1.z, w1.w);
+            *reinterpret_cast<uint4*>(at + j * 256 + (put ^ (j * 32))) = w0;
+            *reinterpret_cast<uint4*>(at + j * 256 + (put ^ (j * 32) ^ 16)) = w1;
+            // Two keys' pieces at a time: the compiler else mixes all four and runs out of
+            // registers (16 ragged sequences up to 32768, 64 heads: 104 us, not 98).
+            if (j == 1) asm volatile("" ::: "memory");
+          }
+          if (wide) {   // a scale of more than 2^7, or of NaN
+#pragma unroll 1
+            for (int i = 0; i < 2 * kCodeReps; ++i) {
+              const int j = i >> 1;
+              const uint32_t ej = (j & 2 ? (j & 1 ? scales.w : scales.z)
+                                         : (j & 1 ? scales.y : scales.x)) >> 16;
+              if (ej <= kScaleMost) continue;
+              const uint32_t more = ej > 0x7f80u ? 0x7fff7fffu : (ej - (7u << 7)) * 0x10001u;
+              uint4* const piece = reinterpret_cast<uint4*>(at + j * 256 + (put ^ (i * 16)));
+              uint4 w = *piece;
+              w.x = mul_bf16x2(w.x, more);
+              w.y = mul_bf16x2(w.y, more);
+              w.z = mul_bf16x2(w.z, more);
+              w.w = mul_bf16x2(w.w, more);
+              *piece = w;
             }
-            uint8_t* row = stage + (pc >> 2) * kAtom + key * 128;
-            const int c = (pc & 3) * 2;
-            *reinterpret_cast<uint4*>(row + (((c + sw) ^ (key & 7)) << 4)) = w[0];
-            *reinterpret_cast<uint4*>(row + (((c + 1 - sw) ^ (key & 7)) << 4)) = w[1];
           }
           {
             const int key = gw * kKeysPerWarp + (lane >> 2), pc = lane & 3;
