@@ -464,6 +464,40 @@ def test_latent_attn_non_finite_rows_outside(dsa):
     attn_check(O3, lse3, Q, rows, lens, 0.07, idx)
 
 
+@pytest.mark.parametrize("H", [16, 128])
+@pytest.mark.parametrize("group", [0, 1, 2, 3])
+def test_latent_attn_wide_and_nan_scales(dsa, group, H):
+    """e4m3 rows of which one group of 128 dims has scales from 2^-108 to 2^106 and Q is zero there,
+    so that the weights stay ordinary ones; and a row whose group is NaN, seen and not listed."""
+    n, dims = 330, slice(128 * group, 128 * group + 128)
+    g = gen(61)
+    kv = torch.randn(n, D, generator=g, device="cuda")
+    shift = torch.tensor([0, 15, 16, 17, 18, 60, 112, -100])[torch.arange(n) % 8]
+    kv[:, dims] *= torch.exp2(shift.float())[:, None].cuda()
+    cache = torch.full((8, 64, dsa.cache_row_bytes(DC, DR, "e4m3")), 0xff, dtype=torch.uint8,
+                       device="cuda")
+    table = i32([[7, 2, 0, 5, 3, 6]])
+    at = torch.arange(n, device="cuda")
+    slots = (table[0][at // 64] * 64 + at % 64).to(torch.int32)
+    dsa.dsa_cache_write(kv.to(torch.bfloat16), slots, cache, DC, fmt="e4m3")
+    rows = [dsa.dsa_cache_read(cache, slots, DC, DR, fmt="e4m3").double()]
+    Q = torch.randn(1, 1, H, D, generator=g, device="cuda")
+    Q[..., dims] = 0.0
+    Q = Q.to(torch.bfloat16)
+    O, lse = dsa.dsa_latent_attn(Q, cache, table, i32([n]), 0.07, fmt="e4m3")
+    no_error(dsa)
+    attn_check(O, lse, Q, rows, [n], 0.07)
+    # a group of NaN: all of a row that sees it, nothing of a row that does not list it
+    kv[5, dims.start + 77] = math.nan
+    dsa.dsa_cache_write(kv[5:6].to(torch.bfloat16), slots[5:6].clone(), cache, DC, fmt="e4m3")
+    O, lse = dsa.dsa_latent_attn(Q, cache, table, i32([n]), 0.07, fmt="e4m3")
+    assert bool(torch.isnan(O).all()) and bool(torch.isnan(lse).all())
+    idx = i32([[[j for j in range(n) if j != 5]]])
+    O, lse = dsa.dsa_latent_attn(Q, cache, table, i32([n]), 0.07, fmt="e4m3", idx=idx)
+    no_error(dsa)
+    attn_check(O, lse, Q, rows, [n], 0.07, idx)
+
+
 def test_latent_attn_same_bits_every_time_and_on_any_stream(dsa):
     """No atomics: repeated, concurrent (own workspaces) and captured calls give the same bits."""
     lens = [3000, 1, 700]
