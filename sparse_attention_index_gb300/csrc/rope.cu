@@ -16,8 +16,10 @@
 // of the first half loads and turns both and the other does nothing (all that is read of a
 // rotated part is read before it is written either way, so rotating in place is safe).
 //
-// Measured: 128 heads of 192 dims, 64 of them turned, 16384 tokens, bf16: 245 us, 6.6 TB/s (one,
-// two, eight vectors per thread: 360, 261, 260 us).
+// Measured: 128 heads of 192 dims, 64 of them turned, 16384 tokens, bf16: 236 us, 6.8 TB/s (two or
+// eight vectors per thread: 260 and 257 us). 4097 tokens of 64 fp32 heads of 128 dims, 64 turned in
+// halves: 45 us, 6.0 TB/s. Reading two angles at once gives 2% in the interleaved layout and costs
+// 5% in halves (16384 tokens of 32 bf16 heads, all 128 dims: 77.2 us instead of 73.5).
 
 #include "dsa_common.cuh"
 #include "dsa_internal.h"
@@ -26,6 +28,7 @@ namespace dsa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr long long kL2Bytes = 129ll << 20;
 
 template <typename T>
 __device__ __forceinline__ void unpack(const uint4& v, float (&f)[16 / sizeof(T)]);
@@ -67,11 +70,20 @@ struct RopeParams {
   int inverse;
 };
 
+template <bool STREAM>
+__device__ __forceinline__ void store(uint4* to, const uint4& a) {
+  if (STREAM)
+    __stcs(to, a);
+  else
+    *to = a;
+}
+
 // how the vectors of the rotated part are turned
 enum Layout { kInterleaved, kHalfShuffle, kHalfPairs };
 
-// V vectors per thread, strided by the block
-template <typename T, int LAYOUT, int V>
+// V vectors per thread, strided by the block. STREAM: x and y are more than L2 holds and are marked
+// to leave it first.
+template <typename T, int LAYOUT, int V, bool STREAM>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
   constexpr int E = 16 / sizeof(T);
   extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -112,7 +124,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
         fi[i] = d - nf;
         second[i] = true;
       }
-      if (fi[i] != -2) a[i] = p.x[v];
+      if (fi[i] != -2) a[i] = STREAM ? __ldcs(p.x + v) : p.x[v];
       if (LAYOUT == kHalfPairs && fi[i] >= 0) b[i] = p.x[v + nf / E];
     }
   }
@@ -163,24 +175,26 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
           fa[e] = x * r.x - y * r.y;
           fb[e] = x * r.y + y * r.x;
         }
-        p.y[v + nf / E] = pack(fb);
+        store<STREAM>(p.y + v + nf / E, pack(fb));
       } else {
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float2 r = w[e >> 1];
-          const float x = fa[e], y = fa[e + 1];
-          fa[e] = x * r.x - y * r.y;
-          fa[e + 1] = x * r.y + y * r.x;
+        for (int e = 0; e < E; e += 4) {   // two angles at a time
+          const float4 r = *reinterpret_cast<const float4*>(w + (e >> 1));
+          const float x0 = fa[e], y0 = fa[e + 1], x1 = fa[e + 2], y1 = fa[e + 3];
+          fa[e] = x0 * r.x - y0 * r.y;
+          fa[e + 1] = x0 * r.y + y0 * r.x;
+          fa[e + 2] = x1 * r.z - y1 * r.w;
+          fa[e + 3] = x1 * r.w + y1 * r.z;
         }
       }
-      p.y[v] = pack(fa);
+      store<STREAM>(p.y + v, pack(fa));
     } else if (fi[i] == -1) {
-      p.y[v] = a[i];
+      store<STREAM>(p.y + v, a[i]);
     }
   }
 }
 
-template <typename T, int LAYOUT, int V>
+template <typename T, int LAYOUT, int V, bool STREAM>
 int launch(const RopeParams& p, cudaStream_t stream) {
   const int nf = p.rot / 2;
   // tokens that a block's vectors touch
@@ -189,15 +203,19 @@ int launch(const RopeParams& p, cudaStream_t stream) {
   // at most 1024 * 8 / D vectors' tokens of D / 2 angles and two partial ones: below 48 KB
   const long long blocks = (p.total + kThreads * V - 1) / (kThreads * V);
   if (blocks > 0x7fffffffLL) return DSA_ERR_UNSUPPORTED;
-  rope_kernel<T, LAYOUT, V><<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(p);
+  rope_kernel<T, LAYOUT, V, STREAM><<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
 template <typename T, int LAYOUT>
 int launch_v(const RopeParams& p, cudaStream_t stream) {
   // few vectors: one per thread, so that they spread over the SMs
-  if (p.total <= 152 * 4 * kThreads) return launch<T, LAYOUT, 1>(p, stream);
-  return launch<T, LAYOUT, 4>(p, stream);
+  if (p.total <= 152 * 4 * kThreads) return launch<T, LAYOUT, 1, false>(p, stream);
+  // streamed: 243.3 us down to 238.3 for 16384 tokens of 128 heads, 44.9 to 43.0 for 4097 tokens of
+  // 64 fp32 heads in halves, but 48.6 up to 49.6 for those in pairs
+  if (LAYOUT != kHalfPairs && p.total * 32 > kL2Bytes)
+    return launch<T, LAYOUT, 4, LAYOUT != kHalfPairs>(p, stream);
+  return launch<T, LAYOUT, 4, false>(p, stream);
 }
 
 }  // namespace
