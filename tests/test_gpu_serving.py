@@ -100,6 +100,25 @@ def test_rope(dsa, layout, dtype, T, H, D_, off, rot):
     no_error(dsa)
 
 
+@pytest.mark.parametrize("layout,rot", [("interleaved", 64), ("half", 64), ("half", 48)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rope_more_than_l2_holds(dsa, layout, rot, dtype):
+    T, H, D_, off = 5003, 37, 192, 128
+    g = gen(9)
+    x = torch.randn(T, H, D_, generator=g, device="cuda").to(dtype)
+    pos = torch.randint(0, 1 << 20, (T,), generator=g, device="cuda", dtype=torch.int32)
+    inv, _ = dsa.rope_frequencies(rot)
+    y = dsa.dsa_rope(x, pos, inv, off=off, layout=layout)
+    for t0 in range(0, T, 1000):
+        part = slice(t0, t0 + 1000)
+        ref, mag = rope_ref(x[part], pos[part], inv, off, rot, layout, 1.0, False)
+        rope_close(y[part], ref, mag)
+    assert torch.equal(y[..., :off], x[..., :off])
+    assert torch.equal(y[..., off + rot:], x[..., off + rot:])
+    assert torch.equal(dsa.dsa_rope(x, pos, inv, off=off, layout=layout, out=x), y)   # in place
+    no_error(dsa)
+
+
 def test_rope_far_and_negative_positions(dsa):
     pos = i32([0, 1, -1, 2 ** 31 - 1, -2 ** 31, 2 ** 30 + 12345, 999999937, 131071])
     x = torch.randn(8, 2, 64, generator=gen(1), device="cuda")
@@ -268,6 +287,28 @@ def test_cache_values_that_are_not_finite(dsa):
     want[0, :128] = want[1, 128:256] = want[2, 384:512] = True
     want[3, 512 + 9] = True
     assert torch.equal(nan, want)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_cache_many_rows(dsa, fmt):
+    """Many rows in one call give the bytes and values of calls of a few hundred each."""
+    T, page = 18003, 16
+    g = gen(71)
+    kv = torch.randn(T, D, generator=g, device="cuda").to(torch.bfloat16)
+    shape = (T // page + 3, page, dsa.cache_row_bytes(DC, DR, fmt))
+    slots = torch.randperm(shape[0] * page, generator=g, device="cuda")[:T].to(torch.int32)
+    slots[::97] = -1
+    one = torch.full(shape, 0x5a, dtype=torch.uint8, device="cuda")
+    many = one.clone()
+    dsa.dsa_cache_write(kv, slots, one, DC, fmt=fmt)
+    back = dsa.dsa_cache_read(one, slots, DC, DR, fmt=fmt)
+    for t0 in range(0, T, 400):
+        part = slice(t0, t0 + 400)
+        dsa.dsa_cache_write(kv[part], slots[part], many, DC, fmt=fmt)
+        assert torch.equal(dsa.dsa_cache_read(many, slots[part], DC, DR, fmt=fmt), back[part])
+    assert torch.equal(one, many)
+    assert not back[::97].any()
+    no_error(dsa)
 
 
 def test_cache_bad_slots(dsa):
