@@ -411,6 +411,18 @@ def test_latent_attn(dsa, fmt, B, Sq, H, lens, page):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Sq,H,page", [(1, 128, 64), (2, 100, 48), (4, 16, 100)])
+def test_latent_attn_many_ragged(dsa, fmt, Sq, H, page):
+    """Enough keys that several tiles lie in one cluster's range and one tile in several."""
+    lens = [9000 - 371 * b if b % 6 else (0, 1, 30011, 48)[b // 6 % 4] for b in range(24)]
+    cache, table, rows = make_cache(dsa, lens, page, fmt, 81)
+    Q = torch.randn(24, Sq, H, D, generator=gen(82), device="cuda").to(torch.bfloat16)
+    O, lse = dsa.dsa_latent_attn(Q, cache, table, i32(lens), 192 ** -0.5, fmt=fmt)
+    no_error(dsa)
+    attn_check(O, lse, Q, rows, lens, 192 ** -0.5)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("B,Sq,H,lens,k", [
     (1, 1, 128, [300], 1), (2, 1, 16, [64, 5000], 48), (3, 2, 128, [1, 0, 777], 100),
     (1, 1, 7, [40], 64), (40, 1, 128, [2500] * 40, 2048), (1, 130, 2, [130], 33),
