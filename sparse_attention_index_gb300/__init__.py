@@ -775,9 +775,10 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None
     * ``"ntk"``    - the base raised to base * factor ** (rot / (rot - 2)): the highest frequency
       stays, the lowest is divided by factor;
     * ``"yarn"``   - frequencies that turn at least beta_fast times within original_length
-      positions stay, those that turn at most beta_slow times are divided by factor, and the dims
-      between the two are blended linearly; mscale is attention_factor, or
-      0.1 ln(factor) + 1 where None.
+      positions stay, those that turn at most beta_slow times are divided by factor, and the
+      frequencies between the two are blended linearly in their index, from the last of the former
+      to the first of the latter or index rot - 1 (behind the last frequency, rot/2 - 1), whichever
+      comes first; mscale is attention_factor, or 0.1 ln(factor) + 1 where None.
     """
     if rot < 2 or rot % 2:
         raise ValueError("rot is a positive even number")
@@ -801,9 +802,12 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None
         def dim_of(turns):   # the (fractional) frequency index with this many turns
             return rot * math.log(original_length / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
 
+        # The ramp may end behind the last frequency (rot // 2 - 1): cut there, the low frequencies
+        # would be divided although they turn more than beta_slow times.
         lo = max(math.floor(dim_of(beta_fast)), 0)
-        hi = min(math.ceil(dim_of(beta_slow)), rot // 2 - 1)
+        hi = min(math.ceil(dim_of(beta_slow)), rot - 1)
         blend = ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        blend[i >= dim_of(beta_slow)] = 1.0   # the first one too, where all turn as seldom as that
         inv = inv * (1.0 - blend) + inv / factor * blend
         mscale = (0.1 * math.log(factor) + 1.0) if attention_factor is None else attention_factor
     return inv.float().to("cuda" if device is None else device), mscale

@@ -146,3 +146,37 @@ def test_rope_frequencies(dsa):
                 dict(rot=64, scaling="yarn", beta_fast=1.0, beta_slow=2.0)):
         with pytest.raises(ValueError):
             dsa.rope_frequencies(**bad, device="cpu")
+
+
+@pytest.mark.parametrize("rot,base,length,fast,slow", [
+    (64, 10000.0, 4096, 32.0, 1.0),        # both borders among the frequencies
+    (64, 10000.0, 65536, 32.0, 1.0),       # the ramp ends behind the last one
+    (64, 10000.0, 131072, 32.0, 1.0),
+    (64, 500.0, 131072, 32.0, 1.0),        # all of it between the last frequency and rot - 1
+    (64, 10000.0, 100, 32.0, 1.0),         # it begins in front of the first one
+    (128, 1e6, 32768, 8.0, 0.25),
+    (64, 10000.0, 1 << 30, 4.0, 1.0),      # every frequency turns more than beta_fast times
+    (32, 10000.0, 4, 32.0, 1.0)])          # every frequency turns less than beta_slow times
+def test_yarn_frequencies_against_the_ramp(dsa, rot, base, length, fast, slow):
+    """Each frequency against the published ramp: from floor(d(beta_fast)) to ceil(d(beta_slow)), cut
+    to [0, rot - 1], where d(n) is the index at which base^(-2d/rot) turns n times in `length`."""
+    factor = 8.0
+    got = dsa.rope_frequencies(rot, base, "yarn", factor, length, fast, slow, device="cpu")[0].tolist()
+    d = lambda n: rot / 2 * math.log(length / (2 * math.pi * n)) / math.log(base)  # noqa: E731
+    lo, hi = max(math.floor(d(fast)), 0), min(math.ceil(d(slow)), rot - 1)
+    for i, f in enumerate(got):
+        w = base ** (-2 * i / rot)
+        turns = length * w / (2 * math.pi)
+        if turns <= slow:
+            t = 1.0
+        elif i <= lo:
+            t = 0.0
+        else:
+            t = min(max((i - lo) / (hi - lo), 0.0), 1.0) if hi > lo else 0.0
+        want = w * (1.0 - t) + w / factor * t
+        # one rounding to fp32, and the 64-bit arithmetic in front of it
+        assert abs(f - want) <= 2.0 ** -23 * want, (i, f, want)
+        if turns > slow * 1.001 and t < 1.0:
+            assert f > w / factor, i          # not fully divided
+        if turns <= slow:
+            assert f <= w / factor * (1 + 2.0 ** -23), i
