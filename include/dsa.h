@@ -570,7 +570,9 @@ int dsa_cache_read(const void* cache, int64_t num_slots, int fmt, const int32_t*
  *         rows whose keys are split over the GPU. Nothing is kept in it between calls.
  *
  * Supported: (Dc, Dr) = (512, 64), 1 <= H <= 128, 0 < scale <= 2e38, page_size >= 1,
- * num_pages * page_size < 2^31, max_pages * page_size < 2^31, B * Sq * H < 2^31. The weights are
+ * num_pages * page_size < 2^31, max_pages * page_size < 2^31, B * Sq * H < 2^31. Q . row_j counts
+ * as an infinity where it is past fp32 (its products with scale may be: O is right all the same,
+ * and lse the nearest fp32, an infinity past its range). The weights are
  * rounded to bf16 for their product with the rows, sums are fp32 in a fixed order (the same
  * bits every time).
  */

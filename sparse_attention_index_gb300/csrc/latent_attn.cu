@@ -147,7 +147,7 @@ struct Params {
   int page_shift;   // log2 of the page size, -1 where it is no power of two
   float scale_log2;
   float4* part;     // [2 * clusters][128 groups of 4 dims][prow]
-  float2* ml;       // [2 * clusters][prow]: running max (scaled, log2) and sum
+  float2* ml;       // [2 * clusters][prow]: running max (of the logits before scale) and sum
   int2* joins;      // [clusters]: the tile that begins in a cluster's range and goes on behind it
                     // (-1: none), and the last cluster that works on it
 };
@@ -359,13 +359,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         "l"(*reinterpret_cast<unsigned long long*>(&b)));
   return r;
 }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+  asm("mul.rn.f32x2 %0, %1, %2;"
       : "=l"(*reinterpret_cast<unsigned long long*>(&r))
       : "l"(*reinterpret_cast<unsigned long long*>(&a)),
-        "l"(*reinterpret_cast<unsigned long long*>(&b)),
-        "l"(*reinterpret_cast<unsigned long long*>(&c)));
+        "l"(*reinterpret_cast<unsigned long long*>(&b)));
   return r;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -395,6 +394,11 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ void widen4(uint32_t w, uint32_t up, uint32_t& even, uint32_t& odd) {
   even = mul_bf16x2(((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u), up);
   odd = mul_bf16x2(((w >> 4) & 0x07f007f0u) | (w & 0x80008000u), up);
+}
+
+// log sum exp of a row with largest logit m (before scale) and sum l; a row without a key has l = 0
+__device__ __forceinline__ float lse_of(const Params& p, float m, float l) {
+  return l == 0.f ? -INFINITY : m * p.a.scale + log2f(l) * 0.69314718055994530942f;
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -1018,8 +1022,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         l *= m == -INFINITY ? 0.f : exp2f((m - mn) * c2);
         m = mn;
       }
-      // P = exp2(S*c2 - m*c2) over the valid keys (exp2(-inf) = 0 elsewhere)
-      const float base = m == -INFINITY ? 0.f : m * c2;
+      // P = exp2((S - m) c2) over the valid keys (exp2(-inf) = 0 elsewhere). The difference comes
+      // first: S c2 and m c2 by themselves may be past fp32, and far from zero their own roundings
+      // would move P.
+      const float base = m == -INFINITY ? 0.f : m;
       const float2 cc = make_float2(c2, c2), bb = make_float2(-base, -base);
       float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -1027,7 +1033,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t pk[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          float2 e = fma2(s[t * 8 + j], cc, bb);
+          float2 e = mul2(add2(s[t * 8 + j], bb), cc);
           e.x = ex2f(e.x);
           e.y = ex2f(e.y);
           ls[j & 1] = add2(ls[j & 1], e);
@@ -1081,7 +1087,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         if (rank == 0 && hrow < rows)
-          p.a.lse[row] = l == 0.f ? -INFINITY : (m * c2 + log2f(l)) * 0.69314718055994530942f;
+          p.a.lse[row] = lse_of(p, m, l);
       } else {
         // part 0 of this cluster: a tile begun before its range; part 1: one that goes on behind
         const int part = 2 * cluster + (item == item0 && c0 > 0 ? 0 : 1);
@@ -1099,8 +1105,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             __uint_as_float(ov[d + c2nd]), __uint_as_float(ov[d + 3]));
         }
         if (rank == 0)
-          p.ml[static_cast<long long>(part) * p.prow + hrow] =
-              make_float2(m == -INFINITY ? -INFINITY : m * c2, l);
+          p.ml[static_cast<long long>(part) * p.prow + hrow] = make_float2(m, l);
       }
       tc_fence_before();
       mbar_arrive(&tail->o_free);
@@ -1155,7 +1160,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) latent_join_kernel(const Para
   for (int i = 0; i < parts; ++i) top = fmaxf(top, ml[i][lane].x);
   // a part without a key has m = -inf, l = 0 and O = 0; one with a NaN keeps it in l
   auto weight = [&](float2 q) {
-    return q.x == -INFINITY ? (q.y == 0.f ? 0.f : 1.f) : exp2f(q.x - top);
+    return q.x == -INFINITY ? (q.y == 0.f ? 0.f : 1.f) : exp2f((q.x - top) * p.scale_log2);
   };
   const int d4 = SHARE ? blockIdx.z * kJoinD4 : (blockIdx.z * kJoinWarps + warp) * kJoinD4;
   float4 o[kJoinD4];
@@ -1179,7 +1184,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) latent_join_kernel(const Para
   if (!SHARE || warp == 0)
     for (int i = 0; i < parts; ++i) l += weight(ml[i][lane]) * ml[i][lane].y;
   if (blockIdx.z == 0 && warp == 0 && lane < rows)
-    p.a.lse[r0 + lane] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.69314718055994530942f;
+    p.a.lse[r0 + lane] = lse_of(p, top, l);
   auto pack4 = [](float4 v, float inv) {
     return make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
   };

@@ -771,3 +771,49 @@ def test_memory_of_calls_on_another_stream(dsa, handle):
         assert torch.equal(O, outs[0][0]) and torch.equal(lse, outs[0][1])
     attn_check(*outs[0], Q, rows, lens, 0.07)
     no_error(dsa)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [100, 5000])
+def test_latent_attn_logits_past_fp32(dsa, fmt, n):
+    """Logits whose product with scale, or with scale log2(e), is past fp32, from finite Q . row: the
+    differences decide, and lse is the nearest fp32 (an infinity where it is past its range). Dim 0 of
+    the keys is +-2^10 and Q is zero elsewhere, so that the weights are 0 and 1 exactly; the
+    sums of at most n rows lose n * 2^-23 of their magnitudes, O one rounding to bf16."""
+    cache, table, _ = make_cache(dsa, [n], 64, fmt, 131)
+    kv = torch.randn(n, D, generator=gen(132), device="cuda")
+    up = torch.arange(n, device="cuda") % 3 != 0
+    kv[:, 0] = torch.where(up, 1024.0, -1024.0)
+    at = torch.arange(n, device="cuda")
+    slots = (table[0].long()[at // 64] * 64 + at % 64).to(torch.int32)
+    dsa.dsa_cache_write(kv.to(torch.bfloat16), slots, cache, DC, fmt=fmt)
+    rows = dsa.dsa_cache_read(cache, slots, DC, DR, fmt=fmt).double()
+    assert bool((rows[:, 0].abs() == 1024).all())
+    q0 = [2.0 ** 100, -2.0 ** 100, 0.0, 2.0 ** 60]
+    Q = torch.zeros(1, 1, 4, D, dtype=torch.bfloat16, device="cuda")
+    Q[0, 0, :, 0] = torch.tensor(q0)
+    for scale in (1.5 * 2.0 ** 17, 2.0 ** 30, 2.0 ** 127):
+        O, lse = dsa.dsa_latent_attn(Q, cache, table, i32([n]), scale, fmt=fmt)
+        no_error(dsa)
+        for h, q in enumerate(q0):
+            seen = rows if q == 0 else rows[up if q > 0 else ~up]
+            ref, mag = seen[:, :DC].mean(0), seen[:, :DC].abs().mean(0)
+            err = (O[0, 0, h].double() - ref).abs()
+            assert bool((err <= 2.0 ** -8 * ref.abs() + n * 2.0 ** -22 * mag).all()), (scale, h)
+            want = abs(q) * 1024 * scale + math.log(len(seen))
+            got = float(lse[0, 0, h])
+            if want > torch.finfo(torch.float32).max:
+                assert got == math.inf, (scale, h, got)
+            else:
+                assert abs(got - want) <= 2.0 ** -21 * want, (scale, h, got, want)
+    # every logit far below zero: still the mean, not the zeros of a token without a key
+    neg = torch.zeros(1, 1, 4, D, dtype=torch.bfloat16, device="cuda")
+    neg[..., 0] = -2.0 ** 100
+    idx = torch.nonzero(up)[:, 0].to(torch.int32).view(1, 1, -1).contiguous()
+    O, lse = dsa.dsa_latent_attn(neg, cache, table, i32([n]), 1.5 * 2.0 ** 17, fmt=fmt, idx=idx)
+    seen = rows[up][:, :DC]
+    err = (O[0, 0].double() - seen.mean(0)).abs()
+    assert bool((err <= 2.0 ** -8 * seen.mean(0).abs() + n * 2.0 ** -22 * seen.abs().mean(0)).all())
+    want = -1.5 * 2.0 ** 127 + math.log(len(seen))
+    assert bool(((lse.double() - want).abs() <= 2.0 ** -21 * abs(want)).all())
+    no_error(dsa)
