@@ -558,9 +558,9 @@ int dsa_cache_read(const void* cache, int64_t num_slots, int fmt, const int32_t*
  * and lse = -inf; a sequence with len <= 0 is skipped that way (padding). A length below 0 or
  * above max_pages * page_size is taken as the nearest of the two, and a page outside
  * [0, num_pages) is skipped as if its keys were not there; both are recorded as
- * DSA_STAGE_LATENT | DSA_DEVERR_BAD_PAGE. Rows of the cache that no token sees are not read. An
- * infinity or a NaN in a row reaches every token that sees it and, without lists and with Sq > 1,
- * any other new token of the sequence (a masked weight of zero still multiplies it).
+ * DSA_STAGE_LATENT | DSA_DEVERR_BAD_PAGE. Rows of the cache that no token sees are not read. A NaN
+ * in a row, or an infinity that makes a logit +inf or NaN, reaches every token that sees the row
+ * (O and lse are NaN) and no other; a logit of -inf is a weight of zero.
  *
  *   Q     bf16 [B, Sq, H, Dc + Dr]        cache      as above, num_pages * page_size slots
  *   lens  int32 [B]                       page_table int32 [B, max_pages]

@@ -396,6 +396,25 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t up, uint32_t& even, 
   odd = mul_bf16x2(((w >> 4) & 0x07f007f0u) | (w & 0x80008000u), up);
 }
 
+// two bf16 with infinities and NaNs replaced by zero
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+  return w;
+}
+
+// Keys [from, to) of a chunk: infinities and NaNs of their latent dims replaced by zero (four atoms of
+// 64 dims, a row of 128 bytes of each per key), by thread t of n.
+__device__ __forceinline__ void drop_non_finite(uint8_t* stage, int from, int to, int t, int n) {
+#pragma unroll 1
+  for (int i = from * 32 + t; i < to * 32; i += n) {
+    uint4* at = reinterpret_cast<uint4*>(stage + ((i >> 3) & 3) * kAtom + (i >> 5) * 128) + (i & 7);
+    const uint4 w = *at;
+    const uint4 f = make_uint4(finite2(w.x), finite2(w.y), finite2(w.z), finite2(w.w));
+    if (f.x != w.x || f.y != w.y || f.z != w.z || f.w != w.w) *at = f;
+  }
+}
+
 // log sum exp of a row with largest logit m (before scale) and sum l; a row without a key has l = 0
 __device__ __forceinline__ float lse_of(const Params& p, float m, float l) {
   return l == 0.f ? -INFINITY : m * p.a.scale + log2f(l) * 0.69314718055994530942f;
@@ -1046,6 +1065,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
       tail->lsum[wg][par][hrow] = l;
       l += other;
+      if (p.a.Sq > 1 && !p.a.idx && (c + 1) * kNK > h.lim0) {
+        // Keys that the tile's later tokens see and its earlier ones do not: an infinity or a NaN in
+        // one would go through the earlier ones' weight of zero. S has been worked out, and a token
+        // that sees the key has it in its logit; in V it is dropped. (Here, where few registers are
+        // in use: in front of the loads of S it took four long e4m3 sequences from 218 to 237 us,
+        // here to 220; bf16 is level.)
+        const int from = h.lim0 - c * kNK;
+        drop_non_finite(smem + st * kStage, max(0, from),
+                        min(kNK, from + (static_cast<int>(r0 % H) + rows - 1) / H), hrow,
+                        32 * p.act_warps);
+      }
       fence_proxy_async_smem();
       mbar_arrive(&tail->p_full[wg]);
       // The next tile's Q replaces this one's once the last S of this one is done. The warps of

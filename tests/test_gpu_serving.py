@@ -817,3 +817,35 @@ def test_latent_attn_logits_past_fp32(dsa, fmt, n):
     want = -1.5 * 2.0 ** 127 + math.log(len(seen))
     assert bool(((lse.double() - want).abs() <= 2.0 ** -21 * abs(want)).all())
     no_error(dsa)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Sq,H,lens", [
+    (2, 16, [100, 49]), (4, 16, [49, 3, 500]), (7, 5, [7, 96]), (3, 128, [2, 50, 4000]),
+    (70, 3, [200]), (4, 33, [20011])])
+def test_latent_attn_non_finite_rows_behind_a_token(dsa, fmt, Sq, H, lens):
+    """A NaN in the row of a new token, or an infinity that gives a logit of +inf, reaches that token and
+    the later ones, and none in front of it."""
+    cache, table, rows = make_cache(dsa, lens, 16, fmt, 141)
+    Q = torch.randn(len(lens), Sq, H, D, generator=gen(142), device="cuda").to(torch.bfloat16)
+    for j, dim, value in ((Sq - 1, 3, math.nan), (1, 300, math.nan), (Sq // 2, 511, math.inf),
+                          (Sq - 1, 0, -math.inf), (1, 530, math.nan), (Sq - 1, 575, math.inf)):
+        bad = cache.clone()
+        kv = torch.randn(len(lens), D, generator=gen(143), device="cuda").to(torch.bfloat16)
+        kv[:, dim] = value
+        at = torch.tensor([n - Sq + j for n in lens], device="cuda")
+        slots = (table.long().gather(1, (at.clamp(min=0) // 16)[:, None])[:, 0] * 16 + at % 16)
+        slots = torch.where(at >= 0, slots, -1).to(torch.int32)
+        dsa.dsa_cache_write(kv, slots, bad, DC, fmt=fmt)
+        O, lse = dsa.dsa_latent_attn(Q, bad, table, i32(lens), 0.07, fmt=fmt)
+        no_error(dsa)
+        attn_check(O[:, :j], lse[:, :j], Q[:, :j], rows, [n - (Sq - j) for n in lens], 0.07)
+        for b, n in enumerate(lens):
+            for i in range(j, Sq):
+                if n - Sq + j < 0:       # no such row
+                    continue
+                if math.isnan(value) or (fmt == "e4m3" and dim < DC):
+                    assert bool(O[b, i].isnan().all()) and bool(lse[b, i].isnan().all()), (b, i)
+                else:    # a logit of +inf; one of -inf is a weight of zero
+                    up = Q[b, i, :, dim] * value > 0
+                    assert bool(O[b, i][up].isnan().all()) and bool(lse[b, i][up].isnan().all()), (b, i)
