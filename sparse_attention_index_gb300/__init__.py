@@ -38,7 +38,7 @@ DSA_STAGE_INDEXER, DSA_STAGE_TOPK, DSA_STAGE_FWD, DSA_STAGE_BWD = 0x100, 0x200, 
 DSA_DEVERR_BAD_PAGE = 0x04
 DSA_STAGE_LOSS, DSA_STAGE_LOSS_BWD = 0x500, 0x600
 DSA_STAGE_CACHE, DSA_STAGE_LATENT = 0x700, 0x800
-DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED = 0, 1, 2
+DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_WORKSPACE = 0, 1, 2, 3
 STATUS = {0: "DSA_OK", 1: "DSA_ERR_INVALID_ARG", 2: "DSA_ERR_UNSUPPORTED", 3: "DSA_ERR_WORKSPACE",
           4: "DSA_ERR_CUDA", 5: "DSA_ERR_TIMEOUT", 6: "DSA_ERR_DEVICE"}
 
@@ -894,18 +894,9 @@ def latent_attn_workspace_bytes(B, Sq, H, Dc, Dr, k=0) -> int:
     return int(lib.dsa_latent_attn_workspace_size(B, Sq, H, Dc, Dr, k))
 
 
-def dsa_latent_attn(Q, cache, page_table, lens, scale: float, fmt: str = "e4m3", idx=None,
-                    Dc: int = 512, O=None, lse=None, ws=None, stream=None):
-    """Attention of the Sq newest tokens of each sequence over the paged latent cache.
-
-    Q [B,Sq,H,Dc+Dr] bf16, cache uint8 [num_pages, page_size, row_bytes], page_table int32
-    [B, max_pages], lens int32 [B] (cached tokens, the Sq new ones among them), idx int32
-    [B,Sq,k] (the selected positions, as dsa_topk gives them) or None for every cached key
-    -> (O bf16 [B,Sq,H,Dc], lse fp32 [B,Sq,H]).
-
-    ws: a device byte buffer of at least latent_attn_workspace_bytes(...) (allocated here if
-    None). What is allocated here is allocated on `stream`.
-    """
+def _latent_args(Q, cache, page_table, lens, scale, fmt, idx, Dc, O, lse, ws, stream):
+    """dsa_latent_attn's arguments checked and its outputs and workspace made: (the C arguments,
+    O, lse, ws)."""
     qp = _dev(Q, "Q", torch.bfloat16)
     if Q.dim() != 4 or Q.shape[3] < Dc:
         raise ValueError("Q must be [B, Sq, H, Dc + Dr]")
@@ -936,11 +927,41 @@ def dsa_latent_attn(Q, cache, page_table, lens, scale: float, fmt: str = "e4m3",
         ws = _empty((need,), torch.uint8, dev, stream)
     if ws is not None and ws.device != dev:
         raise ValueError(f"ws is on {ws.device}, the other arguments on {dev}")
-    _call(lib.dsa_latent_attn, "dsa_latent_attn", dev, stream, qp, cp, _CACHE_FORMATS[fmt],
-          cache.shape[0], cache.shape[1], tp, page_table.shape[1], lp, ip, k, B, Sq, H, Dc, Dr,
-          float(scale), op, ep, None if ws is None else _dev(ws, "ws"),
-          0 if ws is None else ws.numel() * ws.element_size())
+    return (qp, cp, _CACHE_FORMATS[fmt], cache.shape[0], cache.shape[1], tp, page_table.shape[1], lp,
+            ip, k, B, Sq, H, Dc, Dr, float(scale), op, ep, None if ws is None else _dev(ws, "ws"),
+            0 if ws is None else ws.numel() * ws.element_size()), O, lse, ws
+
+
+def dsa_latent_attn(Q, cache, page_table, lens, scale: float, fmt: str = "e4m3", idx=None,
+                    Dc: int = 512, O=None, lse=None, ws=None, stream=None):
+    """Attention of the Sq newest tokens of each sequence over the paged latent cache.
+
+    Q [B,Sq,H,Dc+Dr] bf16, cache uint8 [num_pages, page_size, row_bytes], page_table int32
+    [B, max_pages], lens int32 [B] (cached tokens, the Sq new ones among them), idx int32
+    [B,Sq,k] (the selected positions, as dsa_topk gives them) or None for every cached key
+    -> (O bf16 [B,Sq,H,Dc], lse fp32 [B,Sq,H]).
+
+    ws: a device byte buffer of at least latent_attn_workspace_bytes(...) (allocated here if
+    None). What is allocated here is allocated on `stream`.
+    """
+    args, O, lse, ws = _latent_args(Q, cache, page_table, lens, scale, fmt, idx, Dc, O, lse, ws, stream)
+    _call(lib.dsa_latent_attn, "dsa_latent_attn", Q.device, stream, *args)
     return O, lse
+
+
+def _latent_refusal(qp, cp, fmt, num_pages, page_size, tp, max_pages, lp, ip, k, B, Sq, H, Dc, Dr, scale,
+                    op, ep, wp, ws_bytes) -> int:
+    """The status with which the library refuses these arguments of dsa_latent_attn, or DSA_OK."""
+    if min(B, Sq, H, num_pages, page_size, max_pages) < 1:
+        return DSA_ERR_INVALID_ARG
+    if any(p is not None and p % 16 for p in (qp, cp, tp, lp, ip, op, ep)):
+        return DSA_ERR_INVALID_ARG
+    need = latent_attn_workspace_bytes(B, Sq, H, Dc, Dr, k)   # 0: dims or heads that it does not take
+    scale = ctypes.c_float(scale).value
+    if (need == 0 or not 0.0 < scale <= ctypes.c_float(2.0e38).value
+            or max(num_pages, max_pages) * page_size >= 1 << 31 or B * Sq >= (1 << 31) // H):
+        return DSA_ERR_UNSUPPORTED
+    return DSA_OK if wp is not None and wp % 16 == 0 and ws_bytes >= need else DSA_ERR_WORKSPACE
 
 
 def dsa_decode_layer(Q, kv, pos, inv_freq, slots, cache, page_table, lens, scale: float,
@@ -951,14 +972,20 @@ def dsa_decode_layer(Q, kv, pos, inv_freq, slots, cache, page_table, lens, scale
 
     Q [B,Sq,H,Dc+Dr] and kv [B,Sq,Dc+Dr] bf16 before their rotation (neither is changed), pos and
     slots int32 [B,Sq] (the new tokens' positions and cache slots, -1 for padding), inv_freq fp32
-    [Dr/2]; the rest as for dsa_latent_attn, with lens counting the new tokens.
+    [Dr/2]; the rest as for dsa_latent_attn, with lens counting the new tokens. A step that is
+    refused leaves the cache as it was.
     """
     if not isinstance(kv, torch.Tensor) or kv.dim() != 3:
         raise ValueError("kv must be [B, Sq, Dc + Dr]")
     B, Sq, D = kv.shape
     rows = dsa_rope(kv.view(B, Sq, 1, D), pos, inv_freq, off=Dc, layout=layout, mscale=mscale,
                     stream=stream)
-    dsa_cache_write(rows.view(B * Sq, D), slots.view(B * Sq), cache, Dc, fmt=fmt, stream=stream)
     q = dsa_rope(Q, pos, inv_freq, off=Dc, layout=layout, mscale=mscale, stream=stream)
-    return dsa_latent_attn(q, cache, page_table, lens, scale, fmt=fmt, idx=idx, Dc=Dc, ws=ws,
-                           stream=stream)
+    args, O, lse, ws = _latent_args(q, cache, page_table, lens, scale, fmt, idx, Dc, None, None, ws,
+                                    stream)
+    rc = _latent_refusal(*args)
+    if rc != DSA_OK:
+        raise DsaError(rc, "dsa_latent_attn")
+    dsa_cache_write(rows.view(B * Sq, D), slots.view(B * Sq), cache, Dc, fmt=fmt, stream=stream)
+    _call(lib.dsa_latent_attn, "dsa_latent_attn", q.device, stream, *args)
+    return O, lse

@@ -849,3 +849,38 @@ def test_latent_attn_non_finite_rows_behind_a_token(dsa, fmt, Sq, H, lens):
                 else:    # a logit of +inf; one of -inf is a weight of zero
                     up = Q[b, i, :, dim] * value > 0
                     assert bool(O[b, i][up].isnan().all()) and bool(lse[b, i][up].isnan().all()), (b, i)
+
+
+def test_decode_layer_refused_steps_leave_the_cache(dsa):
+    """A step that is refused writes nothing."""
+    B, Sq, H = 2, 1, 16
+    cache, table, _ = make_cache(dsa, [20, 33], 16, "e4m3", 191)
+    inv, _ = dsa.rope_frequencies(DR)
+    Q = torch.zeros(B, Sq, H, D, dtype=torch.bfloat16, device="cuda")
+    good = dict(Q=Q, kv=torch.ones(B, Sq, D, dtype=torch.bfloat16, device="cuda"), pos=i32([[20], [33]]),
+                inv_freq=inv, slots=i32([[3], [7]]), cache=cache.clone(), page_table=table,
+                lens=i32([21, 34]), scale=0.1)
+    wide = torch.zeros(2 * table.numel() + 4, dtype=torch.int32, device="cuda")
+    small = torch.empty(16, dtype=torch.uint8, device="cuda")
+    need = dsa.latent_attn_workspace_bytes(B, Sq, H, DC, DR)
+    odd = torch.empty(need + 32, dtype=torch.uint8, device="cuda")[4:]
+    for bad in (dict(Q=Q[:1].contiguous()), dict(Q=Q.float()), dict(Q=Q[..., :512].contiguous()),
+                dict(Q=torch.zeros(B, Sq, 129, D, dtype=torch.bfloat16, device="cuda")), dict(scale=0.0),
+                dict(scale=math.nan), dict(scale=3e38), dict(lens=i32([21])), dict(lens=i32([21, 34]).long()),
+                dict(lens=i32([0, 0, 21, 34, 0])[1:3]), dict(page_table=table[0]),
+                dict(page_table=table[:1].contiguous()), dict(page_table=table[:, :0].contiguous()),
+                dict(page_table=wide[1:1 + table.numel()].view(table.shape)),
+                dict(page_table=table.cpu()), dict(ws=small), dict(ws=odd), dict(ws=small.cpu()),
+                dict(idx=i32([[[1]]])), dict(idx=i32([[[1]], [[1]]]).long()),
+                dict(idx=i32([[[]], [[]]])), dict(idx=wide[1:3].view(2, 1, 1)), dict(layout="other"),
+                dict(fmt="bf16"), dict(slots=i32([[3]])), dict(pos=i32([[20]])),
+                dict(cache=cache.view(-1, cache.shape[-1]))):
+        kw = {**good, **bad}
+        before = kw["cache"].clone()
+        with pytest.raises((TypeError, ValueError, RuntimeError)):
+            dsa.dsa_decode_layer(**kw)
+        torch.cuda.synchronize()
+        assert torch.equal(kw["cache"], before), bad
+    dsa.dsa_decode_layer(**good)
+    assert not torch.equal(good["cache"], cache)   # the same step, not refused
+    no_error(dsa)

@@ -180,3 +180,25 @@ def test_yarn_frequencies_against_the_ramp(dsa, rot, base, length, fast, slow):
             assert f > w / factor, i          # not fully divided
         if turns <= slow:
             assert f <= w / factor * (1 + 2.0 ** -23), i
+
+
+def test_latent_refusal_agrees_with_the_library(dsa):
+    """What dsa_decode_layer asks before it writes to the cache is what the library then answers. (Its
+    calls below are refused: an accepted set of arguments is not given to the library here.)"""
+    good = dict(qp=A, cp=A, fmt=1, num_pages=8, page_size=64, tp=A, max_pages=4, lp=A, ip=None, k=0, B=2,
+                Sq=1, H=16, Dc=512, Dr=64, scale=0.1, op=A, ep=A, wp=A, ws_bytes=1 << 40)
+    assert dsa._latent_refusal(**good) == dsa.DSA_OK
+    need = dsa.latent_attn_workspace_bytes(2, 1, 16, 512, 64)
+    assert dsa._latent_refusal(**{**good, "ws_bytes": need}) == dsa.DSA_OK
+    assert dsa._latent_refusal(**{**good, "scale": 2.0e38}) == dsa.DSA_OK
+    bads = [{name: A + 4} for name in ("qp", "cp", "tp", "lp", "op", "ep", "wp")]
+    bads += [{name: 0} for name in ("num_pages", "page_size", "max_pages", "B", "Sq", "H")]
+    bads += [dict(ip=A + 4, k=4), dict(Dc=256), dict(Dr=0), dict(H=129), dict(scale=0.0),
+             dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan), dict(scale=2.1e38),
+             dict(scale=1e-60), dict(num_pages=1 << 26), dict(max_pages=1 << 26),
+             dict(B=1 << 20, Sq=1 << 10), dict(wp=None), dict(ws_bytes=need - 1)]
+    for bad in bads:
+        args = {**good, **bad}
+        want = dsa._latent_refusal(**args)
+        assert want != dsa.DSA_OK, bad
+        assert dsa.lib.dsa_latent_attn(*args.values(), None) == want, bad
