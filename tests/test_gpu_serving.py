@@ -884,3 +884,195 @@ def test_decode_layer_refused_steps_leave_the_cache(dsa):
     dsa.dsa_decode_layer(**good)
     assert not torch.equal(good["cache"], cache)   # the same step, not refused
     no_error(dsa)
+
+
+def block_counts(lims, blocks=DC, size=64):
+    """How many of the positions below each limit lie in each block of `size`, the blocks in turn."""
+    d = torch.arange(blocks, device="cuda")
+    full = (lims[..., None] - d * size).clamp(0, size)
+    assert int(lims.max()) <= blocks * size
+    return full.double()
+
+
+def every_key_once(dsa, fmt, lens, Sq, H, page, idx=None, times=2):
+    """Q = 0: every weight is 1, lse is log(keys) up to the logarithm's rounding (2^-22 of it), and
+    with rows that are 1 in the dim of their block of 64 positions O counts the keys of each block:
+    integers, their quotient (2^-22) and one rounding to bf16 (2^-8). A key left out or counted twice
+    changes its block by 2^-6 and lse by 1 / keys."""
+    B = len(lens)
+    cache, table, _ = make_cache(dsa, lens, page, fmt, 151)
+    n = i32(lens)
+    kv = torch.zeros(max(max(lens), 1), D, dtype=torch.bfloat16, device="cuda")
+    p = torch.arange(len(kv), device="cuda")
+    kv[p, (p // 64) % DC] = 1.0
+    for b in range(B):
+        if lens[b] > 0:
+            q = p[:lens[b]]
+            slots = (table[b].long()[q // page] * page + q % page).to(torch.int32)
+            dsa.dsa_cache_write(kv[:lens[b]], slots, cache, DC, fmt=fmt)
+    Q = torch.zeros(B, Sq, H, D, dtype=torch.bfloat16, device="cuda")
+    lims = (n[:, None] - Sq + 1 + torch.arange(Sq, device="cuda")).clamp(min=0)
+    if idx is None:
+        counts = block_counts(lims)
+    else:
+        counts = torch.zeros(B, Sq, DC + 1, dtype=torch.float64, device="cuda")
+        t = idx.long()
+        seen = (t >= 0) & (t < lims[..., None])
+        counts.scatter_add_(2, torch.where(seen, t // 64, DC), torch.ones_like(t, dtype=torch.float64))
+        counts = counts[..., :DC]
+    keys = counts.sum(-1)
+    ref = (counts / keys.clamp(min=1)[..., None])[:, :, None]
+    ref_lse = torch.where(keys > 0, keys.log(), -math.inf)[..., None]
+    first = None
+    for _ in range(times):
+        O = torch.full((B, Sq, H, DC), math.nan, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((B, Sq, H), math.nan, device="cuda")
+        dsa.dsa_latent_attn(Q, cache, table, n, 0.07, fmt=fmt, idx=idx, O=O, lse=lse)
+        no_error(dsa)
+        if first is None:
+            first = O, lse
+        assert torch.equal(O, first[0]) and torch.equal(lse, first[1])
+    for b in range(B):
+        err = (O[b].double() - ref[b]).abs()
+        assert bool((err <= (2.0 ** -8 + 2.0 ** -22) * ref[b]).all()), (b, float(err.max()))
+        off = torch.where(keys[b, :, None] > 0, (lse[b].double() - ref_lse[b]).abs(), 0.0)
+        assert bool((off <= 2.0 ** -22 * ref_lse[b].abs() + 1e-30).all()), (b, float(off.max()))
+        assert bool((lse[b][(keys[b] == 0)] == -math.inf).all())
+
+
+RAGGED = [9000 - 371 * b if b % 6 else (0, 1, 30011, 48)[b // 6 % 4] for b in range(24)]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,Sq,H,page", [
+    (RAGGED, 1, 128, 64), (RAGGED, 2, 100, 48), (RAGGED, 4, 16, 100), ([32768], 1, 16, 64),
+    ([20000, 5], 7, 128, 64), ([31000, 32000, 30500, 29000], 1, 8, 16),
+    ([(7 * b * b + 13 * b) % 401 for b in range(600)], 1, 128, 16),     # a thread splits several tiles
+    ([(11 * b) % 97 for b in range(1300)], 1, 1, 16), ([900, 777], 700, 128, 64),
+    ([1500], 1500, 64, 64)])
+def test_latent_attn_every_key_once(dsa, fmt, lens, Sq, H, page):
+    every_key_once(dsa, fmt, lens, Sq, H, page)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,Sq,H,k", [
+    ([5000, 300, 0, 20000], 1, 128, 2048), ([700] * 600, 1, 16, 100), ([1100], 1100, 8, 130)])
+def test_latent_attn_every_listed_key_once(dsa, fmt, lens, Sq, H, k):
+    g = torch.Generator()
+    g.manual_seed(161)
+    idx = torch.full((len(lens), Sq, k), -1, dtype=torch.int32)
+    for b, n in enumerate(lens):
+        for i in range(Sq):
+            pick = torch.randperm(max(n - Sq + i + 1, 0), generator=g)[:k].sort().values.to(torch.int32)
+            at = torch.randperm(k, generator=g)[:len(pick)].sort().values   # holes anywhere
+            idx[b, i, at] = pick
+    every_key_once(dsa, fmt, lens, Sq, H, 64, idx.cuda())
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Sq,H,page", [(1, 128, 64), (2, 100, 48), (4, 16, 100)])
+def test_latent_attn_many_ragged_each_sequence(dsa, fmt, Sq, H, page):
+    """As test_latent_attn_many_ragged, the norm of the error held for every sequence by itself (a few
+    short sequences have nearly all of the norm of O)."""
+    cache, table, rows = make_cache(dsa, RAGGED, page, fmt, 81)
+    Q = torch.randn(24, Sq, H, D, generator=gen(83), device="cuda").to(torch.bfloat16)
+    O, lse = dsa.dsa_latent_attn(Q, cache, table, i32(RAGGED), 192 ** -0.5, fmt=fmt)
+    no_error(dsa)
+    for b in range(24):
+        one = slice(b, b + 1)
+        attn_check(O[one], lse[one], Q[one], rows[one], RAGGED[one], 192 ** -0.5)
+
+
+@pytest.mark.parametrize("turned", [False, True])
+def test_latent_attn_every_code_and_scale(dsa, turned):
+    """A token that lists one key has its row as the output, bit for bit as dsa_cache_read has it: every
+    finite e4m3 code, at scales from 2^-120 to 2^120 (2^7 is the largest that widens in one step), the
+    key at any place of a list."""
+    code = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).double()   # 0 to 448
+    scales = [-120, -119, -118, -100, -60, -9, -1, 0, 1, 6, 7, 8, 9, 15, 60, 112, 113, 118, 119, 120]
+    rows = []
+    for k in scales:
+        v = code.clamp(max=240.0) if k == 120 else code      # 1.875 * 2^127: above it, an infinity
+        top = v[-1:]
+        groups = [torch.cat([v, -top]), torch.cat([-v, top]), torch.cat([top, v.flip(0)]),
+                  torch.cat([-top, -v.flip(0)])]
+        if turned:
+            groups = groups[2:] + groups[:2]
+        rows.append(torch.cat(groups) * 2.0 ** k)
+    n = len(rows)
+    kv = torch.zeros(n, D)
+    kv[:, :DC] = torch.stack(rows).float()
+    cache = torch.full((2, 16, dsa.cache_row_bytes(DC, DR, "e4m3")), 0xff, dtype=torch.uint8,
+                       device="cuda")
+    slots = i32(range(n))
+    dsa.dsa_cache_write(kv.to(torch.bfloat16).cuda(), slots, cache, DC, fmt="e4m3")
+    held = cache.view(32, -1)[:n, DC:DC + 16].contiguous().view(torch.float32)
+    assert torch.equal(held.cpu().double(), torch.tensor([[2.0 ** k] * 4 for k in scales]).double())
+    want = dsa.dsa_cache_read(cache, slots, DC, DR, fmt="e4m3")
+    assert torch.equal(want.cpu(), kv.to(torch.bfloat16))     # nothing was rounded
+    for first in (0, 7, 29):
+        idx = torch.full((1, n, 60), -1, dtype=torch.int32, device="cuda")
+        for i in range(n):
+            idx[0, i, (first + 11 * i) % 60] = i
+        Q = torch.zeros(1, n, 16, D, dtype=torch.bfloat16, device="cuda")
+        O, lse = dsa.dsa_latent_attn(Q, cache, i32([[0, 1]]), i32([n]), 0.07, fmt="e4m3", idx=idx)
+        no_error(dsa)
+        bad = (O[0] != want[:, None, :DC]).any(-1).any(-1)
+        assert not bool(bad.any()), [scales[i] for i in torch.nonzero(bad)[:, 0].tolist()]
+        assert not lse.any()
+
+
+def test_a_longer_prompt_with_the_selection_of_the_top_k(dsa):
+    """As test_prompt_with_the_selection_of_the_top_k, with more tokens than one batch of tiles."""
+    S, H, k = 900, 16, 256
+    g = gen(171)
+    bf = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    idx, _ = dsa.dsa_topk(dsa.dsa_index_scores(bf(1, S, 64, 128), bf(1, S, 128),
+                                               torch.rand(1, S, 64, generator=g, device="cuda")), k, S=S)
+    for fmt in ("bf16", "e4m3"):
+        cache, table, rows = make_cache(dsa, [S], 64, fmt, 172)
+        Q = bf(1, S, H, D)
+        O, lse = dsa.dsa_latent_attn(Q, cache, table, i32([S]), 192 ** -0.5, fmt=fmt, idx=idx)
+        no_error(dsa)
+        for i in range(0, S, 50):        # the norm of the error held for 50 tokens at a time
+            part = slice(i, i + 50)
+            attn_check(O[:, part], lse[:, part], Q[:, part], rows, [i + 50], 192 ** -0.5, idx[:, part])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_decode_layer_captured(dsa, fmt):
+    """A serving step captured once and replayed for the steps that follow: its positions, slots and
+    lengths change in place."""
+    B, Sq, H, page = 3, 1, 16, 16
+    lens = [30, 47, 0]
+    cache, table, _ = make_cache(dsa, [40, 60, 0], page, fmt, 181)
+    mine = cache.clone()
+    inv, m = dsa.rope_frequencies(DR, scaling="yarn", factor=8.0)
+    g = gen(182)
+    Q = torch.empty(B, Sq, H, D, dtype=torch.bfloat16, device="cuda")
+    kv = torch.empty(B, Sq, D, dtype=torch.bfloat16, device="cuda")
+    pos, slots, n = i32([[0]] * B), i32([[-1]] * B), i32(lens)
+
+    def step(s):
+        Q.copy_(torch.randn(Q.shape, generator=g, device="cuda"))
+        kv.copy_(torch.randn(kv.shape, generator=g, device="cuda"))
+        at = [k + s if k else 0 for k in lens]
+        pos.copy_(i32([[a] for a in at]))
+        slots.copy_(i32([[int(table[b, a // page]) * page + a % page if lens[b] else -1]
+                         for b, a in enumerate(at)]))
+        n.copy_(i32([k + s + 1 if k else 0 for k in lens]))
+
+    step(0)
+    dsa.dsa_decode_layer(Q, kv, pos, inv, slots, cache, table, n, 0.07, fmt=fmt, mscale=m)
+    mine.copy_(cache)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        O, lse = dsa.dsa_decode_layer(Q, kv, pos, inv, slots, mine, table, n, 0.07, fmt=fmt, mscale=m)
+    for s in range(1, 8):
+        step(s)
+        O.fill_(math.nan)
+        graph.replay()
+        O2, lse2 = dsa.dsa_decode_layer(Q, kv, pos, inv, slots, cache, table, n, 0.07, fmt=fmt, mscale=m)
+        assert torch.equal(O, O2) and torch.equal(lse, lse2) and torch.equal(mine, cache)
+    no_error(dsa)
