@@ -723,6 +723,12 @@ def _code(value, table: dict, name: str) -> int:
     return table[value]
 
 
+def _int32(*sizes):
+    """Sizes that the C ABI takes as int: ctypes would cut what does not fit."""
+    if max(sizes) > 0x7fffffff or min(sizes) < -0x80000000:
+        raise ValueError(f"sizes must be below 2^31, got {sizes}")
+
+
 def _arg(t, name: str, dtype, shape, device) -> int:
     """A tensor argument: its type, shape and (CUDA) device checked, its address returned."""
     if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape
@@ -830,6 +836,7 @@ def dsa_rope(x, pos, inv_freq, off: int = 0, layout: str = "interleaved", mscale
     H, D = x.shape[-2:]
     rot = 2 * inv_freq.numel()
     dev = x.device
+    _int32(x.shape[:-2].numel(), H, D, off, rot)
     if out is None:
         out = _empty(x.shape, x.dtype, dev, stream)
     _call(lib.dsa_rope, "dsa_rope", dev, stream, xp, _arg(out, "out", x.dtype, x.shape, dev),
@@ -843,6 +850,7 @@ def dsa_rope(x, pos, inv_freq, off: int = 0, layout: str = "interleaved", mscale
 @functools.lru_cache(maxsize=None)
 def cache_row_bytes(Dc: int, Dr: int, fmt: str = "e4m3") -> int:
     """Bytes of one cache row (0: dims that the cache does not support)."""
+    _int32(Dc, Dr)
     return lib.dsa_cache_row_bytes(_code(fmt, _CACHE_FORMATS, "fmt"), Dc, Dr)
 
 
@@ -867,6 +875,7 @@ def dsa_cache_write(kv, slots, cache, Dc: int, fmt: str = "e4m3", stream=None):
     if kv.dim() != 2 or kv.shape[1] < Dc:
         raise ValueError("kv must be [T, Dc + Dr]")
     T, Dr = kv.shape[0], kv.shape[1] - Dc
+    _int32(T)
     cp, num = _cache_arg(cache, Dc, Dr, fmt, kv.device)
     sp = _arg(slots, "slots", torch.int32, (T,), kv.device)
     _call(lib.dsa_cache_write, "dsa_cache_write", kv.device, stream, kp, sp, T, Dc, Dr,
@@ -880,6 +889,7 @@ def dsa_cache_read(cache, slots, Dc: int, Dr: int, fmt: str = "e4m3", kv=None, s
     if slots.dim() != 1:
         raise ValueError("slots must be [N]")
     N, dev = slots.shape[0], slots.device
+    _int32(N)
     cp, num = _cache_arg(cache, Dc, Dr, fmt, dev)
     if kv is None:
         kv = _empty((N, Dc + Dr), torch.bfloat16, dev, stream)
@@ -914,6 +924,7 @@ def _latent_args(Q, cache, page_table, lens, scale, fmt, idx, Dc, O, lse, ws, st
         if k < 1:   # NULL would mean every cached key
             raise ValueError("idx must list at least one slot per token (-1 for none)")
         ip = _arg(idx, "idx", torch.int32, (B, Sq, k), dev)
+    _int32(B, Sq, H, k, cache.shape[1], page_table.shape[1])
     tp = _arg(page_table, "page_table", torch.int32, (B, page_table.shape[1]), dev)
     lp = _arg(lens, "lens", torch.int32, (B,), dev)
     if O is None:

@@ -1076,3 +1076,22 @@ def test_decode_layer_captured(dsa, fmt):
         O2, lse2 = dsa.dsa_decode_layer(Q, kv, pos, inv, slots, cache, table, n, 0.07, fmt=fmt, mscale=m)
         assert torch.equal(O, O2) and torch.equal(lse, lse2) and torch.equal(mine, cache)
     no_error(dsa)
+
+
+def test_sizes_past_32_bits_are_refused(dsa):
+    """The library counts in 32-bit integers: what does not fit is refused, not cut."""
+    inv, _ = dsa.rope_frequencies(64)
+    x = torch.ones(2, 1, 128, device="cuda")
+    cache = torch.zeros(2, 4, dsa.cache_row_bytes(DC, DR), dtype=torch.uint8, device="cuda")
+    kv = torch.zeros(2, D, dtype=torch.bfloat16, device="cuda")
+    Q = torch.zeros(1, 1, 4, D, dtype=torch.bfloat16, device="cuda")
+    for wrap in (1 << 32, -(1 << 32), 1 << 40):
+        for call in (lambda: dsa.dsa_rope(x, i32([3, 5]), inv, off=wrap + 64),
+                     lambda: dsa.dsa_cache_write(kv, i32([0, 1]), cache, wrap + DC),
+                     lambda: dsa.dsa_cache_read(cache, i32([0, 1]), wrap + DC, DR, kv=kv),
+                     lambda: dsa.dsa_cache_read(cache, i32([0, 1]), DC, wrap + DR, kv=kv),
+                     lambda: dsa.dsa_latent_attn(Q, cache, i32([[0, 1]]), i32([3]), 0.1, Dc=wrap + DC),
+                     lambda: dsa.cache_row_bytes(wrap + DC, DR)):
+            with pytest.raises(ValueError):
+                call()
+    no_error(dsa)

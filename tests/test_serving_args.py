@@ -202,3 +202,12 @@ def test_latent_refusal_agrees_with_the_library(dsa):
         want = dsa._latent_refusal(**args)
         assert want != dsa.DSA_OK, bad
         assert dsa.lib.dsa_latent_attn(*args.values(), None) == want, bad
+
+
+def test_sizes_are_32_bit(dsa):
+    dsa._int32(0, -1, 2 ** 31 - 1, -2 ** 31)
+    for bad in (2 ** 31, -2 ** 31 - 1, 2 ** 32 + 5):
+        with pytest.raises(ValueError):
+            dsa._int32(1, bad)
+        with pytest.raises(ValueError):
+            dsa.cache_row_bytes(512, bad)
