@@ -184,7 +184,8 @@ __device__ __forceinline__ int tile_keys(const Params& p, int len, int mt) {
 }
 
 // a tile without a key has one (empty) chunk, which writes its rows
-__device__ __forceinline__ int chunks_of(int keys) { return keys > 0 ? (keys + kNK - 1) / kNK : 1; }
+// (keys + kNK - 1 may be past 32 bits)
+__device__ __forceinline__ int chunks_of(int keys) { return keys > 0 ? (keys - 1) / kNK + 1 : 1; }
 
 __device__ __forceinline__ int item_chunks(const Params& p, int item) {
   if (p.a.idx) return p.list_chunks;
@@ -558,8 +559,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         e.b = k.b;
         e.item = k.item;
         e.lim0 = k.lim0;
-        const int j = c * kNK + mykey;
-        e.raw = j < (p.a.idx ? p.a.k : k.keys) ? j : -1;
+        const uint32_t j = static_cast<uint32_t>(c) * kNK + mykey;   // past 2^31 in a last chunk
+        e.raw = j < static_cast<uint32_t>(p.a.idx ? p.a.k : k.keys) ? static_cast<int>(j) : -1;
       };
       if (made + 4 < n && k.c + 4 < k.nch) {
         take(lane >> 3);
@@ -1071,7 +1072,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
       tail->lsum[wg][par][hrow] = l;
       l += other;
-      if (p.a.Sq > 1 && !p.a.idx && (c + 1) * kNK > h.lim0) {
+      if (p.a.Sq > 1 && !p.a.idx && h.lim0 - c * kNK < kNK) {
         // Keys that the tile's later tokens see and its earlier ones do not: an infinity or a NaN in
         // one would go through the earlier ones' weight of zero. S has been worked out, and a token
         // that sees the key has it in its logit; in V it is dropped. (Here, where few registers are
@@ -1343,7 +1344,7 @@ int launch_latent_attn(const LatentArgs& a, int fmt, cudaStream_t stream) {
   const long long items = a.idx ? static_cast<long long>(a.B) * a.Sq
                                 : static_cast<long long>(a.B) * p.tiles;
   p.items = static_cast<int>(items);   // at most B * Sq * H < 2^31
-  p.list_chunks = a.idx ? (a.k + kNK - 1) / kNK : 0;
+  p.list_chunks = a.idx ? (a.k - 1) / kNK + 1 : 0;
   p.prow = part_rows(a.Sq, a.H, a.k);
   p.act_warps = p.prow / 32;
   p.scale_log2 = a.scale * 1.4426950408889634f;

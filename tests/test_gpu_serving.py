@@ -1095,3 +1095,36 @@ def test_sizes_past_32_bits_are_refused(dsa):
             with pytest.raises(ValueError):
                 call()
     no_error(dsa)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_latent_attn_as_long_as_it_can_be(dsa, fmt):
+    """2^31 - 2 keys, the most that pages of more than one row can hold: a page table that names two
+    pages in turn, each of one row many times. The logits are all equal, so the weights are 1, and the
+    values small integers: a cluster's sums (of 2^31 / 70 keys at most) are multiples of their
+    smallest term below 2^24 of it, exact in fp32. What is rounded is the join of up to 80 parts (2^-17),
+    the division and O (2^-8), and lse (2^-22 of it)."""
+    page = 662
+    pages = (2 ** 31 - 2) // page
+    n = page * pages
+    assert n == 2 ** 31 - 2
+    cache = torch.zeros(2, page, dsa.cache_row_bytes(DC, DR, fmt), dtype=torch.uint8, device="cuda")
+    kv = torch.zeros(2 * page, D, dtype=torch.bfloat16, device="cuda")
+    kv[:, 0] = 1.0
+    kv[:page, 300], kv[page:, 511] = 4.0, -2.0
+    dsa.dsa_cache_write(kv, torch.arange(2 * page, dtype=torch.int32, device="cuda"), cache, DC, fmt=fmt)
+    table = (torch.arange(pages, device="cuda") % 2).to(torch.int32)[None].contiguous()
+    Q = torch.zeros(1, 2, 2, D, dtype=torch.bfloat16, device="cuda")
+    Q[:, :, 1, 0] = 8.0
+    O, lse = dsa.dsa_latent_attn(Q, cache, table, i32([n]), 1.0, fmt=fmt)
+    no_error(dsa)
+    for i in range(2):
+        keys = n - 1 + i
+        even = (pages - pages // 2) * page - (1 - i)     # the last page is an even one
+        ref = torch.zeros(DC, dtype=torch.float64, device="cuda")
+        ref[0], ref[300], ref[511] = 1.0, 4.0 * even / keys, -2.0 * (keys - even) / keys
+        for h in range(2):
+            err = (O[0, i, h].double() - ref).abs()
+            assert bool((err <= (2.0 ** -8 + 2.0 ** -16) * ref.abs()).all()), (h, i, O[0, i, h][[0, 300, 511]])
+            want = math.log(keys) + 8.0 * h
+            assert abs(float(lse[0, i, h]) - want) <= 2.0 ** -17 + 2.0 ** -22 * want, (h, i, float(lse[0, i, h]), want)
