@@ -515,7 +515,10 @@ int dsa_rope(const void* x, void* y, int dtype, const int32_t* pos, const float*
  *                   even: within half an e4m3 step (2^-4 of the value, 2^-10 * 2^k for the
  *                   smallest ones). A power of two keeps the read back exact in bf16 (a
  *                   magnitude above 1.9375 * 2^127 rounds up and reads back as an infinity).
- *                   A group with an infinity or a NaN reads back as NaN.
+ *                   A group with an infinity or a NaN reads back as NaN. The readers take rows as
+ *                   dsa_cache_write makes them: of a scale that is no power of two, or a NaN byte
+ *                   under a finite scale, dsa_cache_read and dsa_latent_attn may make different
+ *                   values.
  *
  * Supported: Dc a multiple of 128, 128 <= Dc <= 1024; Dr a multiple of 8, 0 <= Dr <= 256.
  * dsa_cache_row_bytes returns 0 for anything else.
@@ -550,7 +553,8 @@ int dsa_cache_read(const void* cache, int64_t num_slots, int fmt, const int32_t*
  *     l_j = scale * Q[b,i,h] . row_j[0 : Dc+Dr]      0 <= j <= len - Sq + i
  *     O[b,i,h] = sum_j softmax(l)_j row_j[0 : Dc],   lse[b,i,h] = log sum_j exp(l_j)
  *
- * over every such j (idx = NULL), or over the listed ones: idx[b,i,:] as dsa_topk gives them
+ * over every such j (idx = NULL), or over the listed ones (in a time that goes by k, however many of
+ * its entries are -1): idx[b,i,:] as dsa_topk gives them
  * (-1 entries and entries above the token's position are ignored, entries must be distinct; an
  * entry below -1 or >= len is skipped and recorded as DSA_STAGE_LATENT |
  * DSA_DEVERR_BAD_INDEX). Position j of sequence b is row j % page_size of page
@@ -572,9 +576,8 @@ int dsa_cache_read(const void* cache, int64_t num_slots, int fmt, const int32_t*
  * Supported: (Dc, Dr) = (512, 64), 1 <= H <= 128, 0 < scale <= 2e38, page_size >= 1,
  * num_pages * page_size < 2^31, max_pages * page_size < 2^31, B * Sq * H < 2^31. Q . row_j counts
  * as an infinity where it is past fp32 (its products with scale may be: O is right all the same,
- * and lse the nearest fp32, an infinity past its range). The weights are
- * rounded to bf16 for their product with the rows, sums are fp32 in a fixed order (the same
- * bits every time).
+ * and lse the nearest fp32, an infinity past its range). The weights are rounded to bf16 for
+ * their product with the rows, sums are fp32 in a fixed order (the same bits every time).
  */
 size_t dsa_latent_attn_workspace_size(int B, int Sq, int H, int Dc, int Dr, int k);
 int dsa_latent_attn(const void* Q, const void* cache, int fmt, int64_t num_pages, int page_size,

@@ -8,9 +8,10 @@
 //
 // Bound: memory. Each input byte is read once and each output byte written once, 32 bytes of
 // bf16 and 16 of e4m3 per lane; bf16 rows are copied 16 bytes a thread. 131072 rows of 576 dims
-// at slots in no order: read back at 5.65 TB/s from e4m3 and 6.6 TB/s from bf16, written at 5.0
-// and 6.1 TB/s (an e4m3 row is 656 bytes, so that every row shares a 32-byte sector with its
-// neighbours).
+// at slots in no order, calls replayed from a graph: read back in 39.6 us from e4m3 (6.0 TB/s) and
+// 43.1 us from bf16 (7.0), written in 44.9 us (5.3) and 46.9 us (6.4); through the Python binding 2 to
+// 3 us more. What holds the e4m3 rows back is not known: they are 656 bytes, so that neighbours
+// share a 32-byte sector, but that is one sector in twenty.
 
 #include <cuda_fp8.h>
 
@@ -235,8 +236,9 @@ int run(CacheParams p, int rows, int fmt, bool write, cudaStream_t stream) {
   p.upr = fmt == DSA_CACHE_BF16 ? p.row_bytes / 16 : p.Dc / 128 + (p.Dr + 127) / 128;
   p.units = static_cast<long long>(rows) * p.upr;
   // Several units per thread once one each would fill the SMs' eight resident blocks that often:
-  // 131072 rows of 576 dims, 1 / 2 / 4 per thread: e4m3 read back 46.4 / 41.9 / 46.3 us, written
-  // 47.7 / 47.7 / 60.0; bf16 read 62.1 / 50.0 / 45.6, written 63.9 / 53.9 / 49.6. At 16384 rows
+  // 131072 rows of 576 dims, 1 / 2 / 4 per thread, calls through the binding: e4m3 read back 46.4 /
+  // 41.9 / 46.3 us, written 47.7 / 47.7 / 60.0; bf16 read 62.1 / 50.0 / 45.6, written 63.9 / 53.9 /
+  // 49.6. At 16384 rows
   // they are level, below that one is the quickest.
   const long long wave = 152ll * 8 * (kThreads / (fmt == DSA_CACHE_BF16 ? 1 : 8));
   if (fmt == DSA_CACHE_BF16)

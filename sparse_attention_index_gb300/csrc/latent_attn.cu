@@ -310,8 +310,8 @@ __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) 
 // Tells the peer that what it sent has been read, by every lane of the warp; `used` is worked out from
 // all that the lane has read. Relaxed: a release at cluster scope waits for what the warp itself
 // has on its way to the peer, and at every place for it, in this warp or in an issuer's, it took 3 to
-// 10% (four sequences of 131072 e4m3 rows 223 to 241 us instead of 220, 32 ragged bf16 ones 75 to 78
-// instead of 72). The order comes from a chain of dependencies: the arrival hangs on a vote over
+// 10% (four sequences of 131072 e4m3 rows 223 to 241 us instead of 220, and 222 this way; 32 ragged
+// bf16 ones 75 to 78 instead of 72). The order comes from a chain of dependencies: the arrival hangs on a vote over
 // values worked out from the reads, the peer's next stores hang on the arrival, and no value comes
 // out of thin air, so no read can return what those stores write. (Reads and stores are of the same
 // size and place.) kNoMaximum is a NaN that no addition or maximum gives: the vote always passes.
@@ -1050,7 +1050,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       // P = exp2((S - m) c2) over the valid keys (exp2(-inf) = 0 elsewhere). The difference comes
       // first: S c2 and m c2 by themselves may be past fp32, and far from zero their own roundings
-      // would move P.
+      // would move P. For its product with the rows, which are bf16, P is rounded to bf16 too: half a
+      // step of 2^-8 at most, of either sign from key to key. Its sum l, and so lse, takes it unrounded.
       const float base = m == -INFINITY ? 0.f : m;
       const float2 cc = make_float2(c2, c2), bb = make_float2(-base, -base);
       float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};

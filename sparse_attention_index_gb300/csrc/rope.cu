@@ -16,9 +16,11 @@
 // of the first half loads and turns both and the other does nothing (all that is read of a
 // rotated part is read before it is written either way, so rotating in place is safe).
 //
-// Measured: 128 heads of 192 dims, 64 of them turned, 16384 tokens, bf16: 236 us, 6.8 TB/s (two or
-// eight vectors per thread: 260 and 257 us). 4097 tokens of 64 fp32 heads of 128 dims, 64 turned in
-// halves: 45 us, 6.0 TB/s. Reading two angles at once gives 2% in the interleaved layout and costs
+// Measured, calls replayed from a graph (through the Python binding 2 us more): 128 heads of 192 dims,
+// 64 of them turned, 16384 tokens, bf16: 235 us, 6.9 TB/s (two or eight vectors per thread: 260 and 257
+// us). 4097 tokens of 64 fp32 heads of 128 dims, 64 turned in halves: 43 us, 6.3 TB/s. 16384 tokens of 32
+// bf16 heads, all 128 dims in halves: 72 us, 3.7 TB/s, held back by the angles' reads from shared
+// memory (eight of 8 bytes for each vector). Reading two angles at once gives 2% in the interleaved layout and costs
 // 5% in halves (16384 tokens of 32 bf16 heads, all 128 dims: 77.2 us instead of 73.5).
 
 #include "dsa_common.cuh"
