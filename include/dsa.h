@@ -67,6 +67,7 @@ typedef enum { DSA_BF16 = 0, DSA_F32 = 1 } dsa_dtype;
 #define DSA_STAGE_LOSS_BWD 0x600
 #define DSA_STAGE_CACHE 0x700
 #define DSA_STAGE_LATENT 0x800
+#define DSA_STAGE_EVICT 0x900
 
 /* Human-readable name of a status. Never NULL. */
 const char* dsa_status_string(int status);
@@ -584,6 +585,58 @@ int dsa_latent_attn(const void* Q, const void* cache, int fmt, int64_t num_pages
                     const int32_t* page_table, int max_pages, const int32_t* lens,
                     const int32_t* idx, int k, int B, int Sq, int H, int Dc, int Dr, float scale,
                     void* O, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Eviction from the cache by accumulated attention weight: dsa_cache_mass adds up what weight each
+ * cached position receives, dsa_cache_keep chooses the positions that stay within a budget, and
+ * dsa_cache_compact moves their rows.
+ */
+
+/*
+ * dsa_cache_keep - the positions of each sequence that stay when it is cut to `budget`: its first
+ * `sink` ones, its `recent` newest ones, and of the others the budget - sink - recent heaviest by
+ * mass (ties go to the lower position, -0 counts as +0, a NaN as heavier than any number). A
+ * sequence of at most `budget` positions keeps all of them.
+ *
+ *   mass   fp32 [B, n]          lens   int32 [B]: the positions that a sequence has
+ *   keep   int32 [B, budget] out: ascending, -1 behind the last
+ *   count  int32 [B] out: min(lens[b], budget), the sequence's new length
+ *
+ * A length below 0 or above n is taken as the nearest of the two and recorded as
+ * DSA_STAGE_EVICT | DSA_DEVERR_BAD_PAGE. Entries of mass at or behind a sequence's length are not
+ * read. Supported: sink >= 0, recent >= 0, sink + recent <= budget, 1 <= budget <= 2^30,
+ * 1 <= n <= 2^30, B <= 2^27.
+ */
+int dsa_cache_keep(const float* mass, int n, const int32_t* lens, int B, int budget, int sink,
+                   int recent, int32_t* keep, int32_t* count, void* stream);
+
+/*
+ * dsa_cache_compact - moves rows of the cache: position j of sequence b becomes what its position
+ * keep[b,j] was (bytes are copied, in either format). keep int32 [B, budget] as dsa_cache_keep gives
+ * it: ascending, -1 behind the last; lens int32 [B], page_table int32 [B, max_pages]: the sequences
+ * before the move.
+ *
+ *   new_table  int32 [B, new_max_pages]: the pages that the kept rows go to, none of them in use by
+ *              any sequence (new_max_pages * page_size >= budget); or NULL: the rows go to the front
+ *              of the sequence's own pages, which no other sequence may share
+ *   mass       fp32 [B, n] or NULL: moved with the rows into new_mass fp32 [B, new_n]
+ *              (new_n >= budget): new_mass[b,j] = mass[b, keep[b,j]], zero behind the last. new_mass
+ *              may be mass itself (new_n = n); any other overlap is refused.
+ *
+ * An entry outside [-1, lens[b]) moves nothing and is recorded as DSA_STAGE_EVICT |
+ * DSA_DEVERR_BAD_INDEX, and so is, in place, one below its own place j. A page outside
+ * [0, num_pages) moves nothing; it and a length below 0 or above max_pages * page_size (taken as the
+ * nearest of the two) are recorded as DSA_STAGE_EVICT | DSA_DEVERR_BAD_PAGE. Every other byte of the
+ * cache stays as it was.
+ *
+ * Supported: Dc and Dr as for the cache, budget <= 2^30, n and new_n <= 2^30, page_size >= 1,
+ * num_pages * page_size, max_pages * page_size and new_max_pages * page_size below 2^31.
+ */
+int dsa_cache_compact(void* cache, int fmt, int64_t num_pages, int page_size,
+                      const int32_t* page_table, int max_pages, const int32_t* lens,
+                      const int32_t* keep, int budget, const int32_t* new_table, int new_max_pages,
+                      int B, int Dc, int Dr, const float* mass, int n, float* new_mass, int new_n,
+                      void* stream);
 
 #ifdef __cplusplus
 }

@@ -17,6 +17,8 @@ Entry points (same names as the C ABI):
 * ``dsa_rope`` - rotary positions on part of each head, and their inverse (the gradient)
 * ``dsa_cache_write`` / ``dsa_cache_read`` - rows of the paged latent cache (bf16 or e4m3)
 * ``dsa_latent_attn`` - attention of the newest tokens over that cache -> (O, lse)
+* ``dsa_cache_keep`` / ``dsa_cache_compact`` - the positions that stay in the cache by their attention
+  weight, and their rows moved
 * ``dsa_decode_layer`` - these together, one serving step
 """
 from __future__ import annotations
@@ -37,7 +39,7 @@ DSA_DEVERR_TIMEOUT, DSA_DEVERR_BAD_INDEX, DSA_DEVERR_MISALIGNED = 0x01, 0x02, 0x
 DSA_STAGE_INDEXER, DSA_STAGE_TOPK, DSA_STAGE_FWD, DSA_STAGE_BWD = 0x100, 0x200, 0x300, 0x400
 DSA_DEVERR_BAD_PAGE = 0x04
 DSA_STAGE_LOSS, DSA_STAGE_LOSS_BWD = 0x500, 0x600
-DSA_STAGE_CACHE, DSA_STAGE_LATENT = 0x700, 0x800
+DSA_STAGE_CACHE, DSA_STAGE_LATENT, DSA_STAGE_EVICT = 0x700, 0x800, 0x900
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_WORKSPACE = 0, 1, 2, 3
 STATUS = {0: "DSA_OK", 1: "DSA_ERR_INVALID_ARG", 2: "DSA_ERR_UNSUPPORTED", 3: "DSA_ERR_WORKSPACE",
           4: "DSA_ERR_CUDA", 5: "DSA_ERR_TIMEOUT", 6: "DSA_ERR_DEVICE"}
@@ -53,7 +55,8 @@ EXPORTS = ("dsa_status_string", "dsa_version", "dsa_get_last_device_error", "dsa
            "dsa_index_topk_workspace_size", "dsa_index_topk", "dsa_index_topk_fp8",
            "dsa_index_topk_stream_workspace_size", "dsa_index_topk_stream",
            "dsa_index_topk_stream_fp8", "dsa_rope", "dsa_cache_row_bytes", "dsa_cache_write",
-           "dsa_cache_read", "dsa_latent_attn_workspace_size", "dsa_latent_attn")
+           "dsa_cache_read", "dsa_latent_attn_workspace_size", "dsa_latent_attn", "dsa_cache_keep",
+           "dsa_cache_compact")
 
 
 class DsaError(RuntimeError):
@@ -116,7 +119,11 @@ def _load() -> ctypes.CDLL:
     lib.dsa_latent_attn_workspace_size.restype = sz
     lib.dsa_latent_attn.argtypes = [vp, vp, ci, i64, ci, vp, ci, vp, vp, ci, ci, ci, ci, ci, ci, cf,
                                     vp, vp, vp, sz, vp]
+    lib.dsa_cache_keep.argtypes = [vp, ci, vp, ci, ci, ci, ci, vp, vp, vp]
+    lib.dsa_cache_compact.argtypes = [vp, ci, i64, ci, vp, ci, vp, vp, ci, vp, ci, ci, ci, ci, vp, ci,
+                                      vp, ci, vp]
     for name in ("dsa_rope", "dsa_cache_write", "dsa_cache_read", "dsa_latent_attn",
+                 "dsa_cache_keep", "dsa_cache_compact",
                  "dsa_get_last_device_error", "dsa_index_scores", "dsa_index_scores_fp8", "dsa_topk",
                  "dsa_indexer_loss", "dsa_indexer_loss_bwd", "dsa_index_topk",
                  "dsa_index_topk_fp8", "dsa_index_topk_stream", "dsa_index_topk_stream_fp8",
@@ -1000,3 +1007,74 @@ def dsa_decode_layer(Q, kv, pos, inv_freq, slots, cache, page_table, lens, scale
     dsa_cache_write(rows.view(B * Sq, D), slots.view(B * Sq), cache, Dc, fmt=fmt, stream=stream)
     _call(lib.dsa_latent_attn, "dsa_latent_attn", q.device, stream, *args)
     return O, lse
+
+
+def dsa_cache_keep(mass, lens, budget: int, sink: int = 0, recent: int = 0, keep=None, count=None,
+                   stream=None):
+    """The positions of each sequence that stay when it is cut to `budget`: the first `sink`, the
+    `recent` newest, and the heaviest of the others by mass (ties: the lower position).
+
+    mass fp32 [B, n], lens int32 [B] -> (keep int32 [B, budget], ascending, -1 behind the last;
+    count int32 [B], the new lengths).
+    """
+    mp = _dev(mass, "mass", torch.float32)
+    if mass.dim() != 2:
+        raise ValueError("mass must be [B, n]")
+    (B, n), dev = mass.shape, mass.device
+    _int32(B, n, budget, sink, recent)
+    if budget < 1:
+        raise ValueError("budget must be at least 1")
+    if keep is None:
+        keep = _empty((B, budget), torch.int32, dev, stream)
+    if count is None:
+        count = _empty((B,), torch.int32, dev, stream)
+    _call(lib.dsa_cache_keep, "dsa_cache_keep", dev, stream, mp, n,
+          _arg(lens, "lens", torch.int32, (B,), dev), B, budget, sink, recent,
+          _arg(keep, "keep", torch.int32, (B, budget), dev),
+          _arg(count, "count", torch.int32, (B,), dev))
+    return keep, count
+
+
+def dsa_cache_compact(cache, page_table, lens, keep, new_table, Dc: int, Dr: int, fmt: str = "e4m3",
+                      mass=None, new_mass=None, stream=None):
+    """Move the kept rows: position j of sequence b becomes what its position keep[b, j] was.
+
+    cache uint8 [num_pages, page_size, row_bytes], page_table int32 [B, max_pages] and lens int32 [B]
+    before the move, keep int32 [B, budget] (as dsa_cache_keep gives it: ascending, -1 behind the
+    last). new_table int32 [B, new_max_pages]: pages that no sequence uses; or None: the front of the
+    sequence's own pages, which no other sequence may share.
+
+    mass fp32 [B, n]: moved too, into new_mass fp32 [B, new_n] with zeros behind the last ([B, budget]
+    where None; new_mass=mass moves it in place). Returns new_mass.
+    """
+    kp = _dev(keep, "keep", torch.int32)
+    if keep.dim() != 2:
+        raise ValueError("keep must be [B, budget]")
+    (B, budget), dev = keep.shape, keep.device
+    cp, _ = _cache_arg(cache, Dc, Dr, fmt, dev)
+    if cache.dim() != 3:
+        raise ValueError("cache must be [num_pages, page_size, row_bytes]")
+    if page_table.dim() != 2 or (new_table is not None and new_table.dim() != 2):
+        raise ValueError("page_table and new_table must be [B, pages]")
+    if mass is None and new_mass is not None:
+        raise ValueError("new_mass is given without mass")
+    new_pages = 0 if new_table is None else new_table.shape[1]
+    _int32(B, budget, Dc, Dr, cache.shape[1], page_table.shape[1], new_pages)
+    tp = _arg(page_table, "page_table", torch.int32, (B, page_table.shape[1]), dev)
+    lp = _arg(lens, "lens", torch.int32, (B,), dev)
+    np_ = None if new_table is None else _arg(new_table, "new_table", torch.int32, (B, new_pages), dev)
+    mp = wp = None
+    n = new_n = 0
+    if mass is not None:
+        if mass.dim() != 2 or (new_mass is not None and new_mass.dim() != 2):
+            raise ValueError("mass and new_mass must be [B, n]")
+        if new_mass is None:
+            new_mass = _empty((B, budget), torch.float32, dev, stream)
+        n, new_n = mass.shape[1], new_mass.shape[1]
+        _int32(n, new_n)
+        mp = _arg(mass, "mass", torch.float32, (B, n), dev)
+        wp = _arg(new_mass, "new_mass", torch.float32, (B, new_n), dev)
+    _call(lib.dsa_cache_compact, "dsa_cache_compact", dev, stream, cp, _CACHE_FORMATS[fmt],
+          cache.shape[0], cache.shape[1], tp, page_table.shape[1], lp, kp, budget, np_, new_pages, B,
+          Dc, Dr, mp, n, wp, new_n)
+    return new_mass

@@ -595,4 +595,72 @@ int dsa_latent_attn(const void* Q, const void* cache, int fmt, int64_t num_pages
   return dsa::launch_latent_attn(a, fmt, as_stream(stream));
 }
 
+int dsa_cache_keep(const float* mass, int n, const int32_t* lens, int B, int budget, int sink,
+                   int recent, int32_t* keep, int32_t* count, void* stream) {
+  if (!mass || !lens || !keep || !count) return DSA_ERR_INVALID_ARG;
+  if (n < 1 || B < 1 || budget < 1 || sink < 0 || recent < 0 || sink > budget ||
+      recent > budget - sink)
+    return DSA_ERR_INVALID_ARG;
+  const void* ptrs[] = {mass, lens, keep, count};
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return DSA_ERR_INVALID_ARG;
+  if (n > (1 << 30) || budget > (1 << 30) || B > (1 << 27)) return DSA_ERR_UNSUPPORTED;
+  return dsa::launch_cache_keep(mass, n, lens, B, budget, sink, recent, keep, count,
+                                as_stream(stream));
+}
+
+int dsa_cache_compact(void* cache, int fmt, int64_t num_pages, int page_size,
+                      const int32_t* page_table, int max_pages, const int32_t* lens,
+                      const int32_t* keep, int budget, const int32_t* new_table, int new_max_pages,
+                      int B, int Dc, int Dr, const float* mass, int n, float* new_mass, int new_n,
+                      void* stream) {
+  if (!cache || !page_table || !lens || !keep) return DSA_ERR_INVALID_ARG;
+  if (B < 1 || Dc < 1 || Dr < 0 || num_pages < 1 || page_size < 1 || max_pages < 1 || budget < 1)
+    return DSA_ERR_INVALID_ARG;
+  if (fmt != DSA_CACHE_BF16 && fmt != DSA_CACHE_E4M3) return DSA_ERR_INVALID_ARG;
+  if ((mass != nullptr) != (new_mass != nullptr)) return DSA_ERR_INVALID_ARG;
+  const void* ptrs[] = {cache, page_table, lens, keep, new_table, mass, new_mass};
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return DSA_ERR_INVALID_ARG;
+  if (new_table && new_max_pages < 1) return DSA_ERR_INVALID_ARG;
+  if (mass) {
+    if (n < 1 || new_n < budget) return DSA_ERR_INVALID_ARG;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(mass), b = reinterpret_cast<uintptr_t>(new_mass);
+    const uintptr_t a_end = a + static_cast<uintptr_t>(B) * n * 4;
+    const uintptr_t b_end = b + static_cast<uintptr_t>(B) * new_n * 4;
+    if (a == b ? n != new_n : a < b_end && b < a_end) return DSA_ERR_INVALID_ARG;
+  }
+  // positions, slots and rows are counted in 32 bits
+  const long long most = 1LL << 31;
+  if (dsa::cache_row_bytes(fmt, Dc, Dr) == 0 || budget > (1 << 30) || num_pages >= most ||
+      num_pages * page_size >= most || static_cast<long long>(max_pages) * page_size >= most ||
+      (mass && (n > (1 << 30) || new_n > (1 << 30))))
+    return DSA_ERR_UNSUPPORTED;
+  if (new_table) {
+    const long long room = static_cast<long long>(new_max_pages) * page_size;
+    if (room >= most) return DSA_ERR_UNSUPPORTED;
+    if (room < budget) return DSA_ERR_INVALID_ARG;
+  } else if (B > 65535) {
+    return DSA_ERR_UNSUPPORTED;   // the grid's range
+  }
+  dsa::CompactArgs a = {};
+  a.cache = static_cast<uint8_t*>(cache);
+  a.page_table = page_table;
+  a.lens = lens;
+  a.keep = keep;
+  a.new_table = new_table;
+  a.mass = mass;
+  a.new_mass = new_mass;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  a.new_max_pages = new_max_pages;
+  a.budget = budget;
+  a.B = B;
+  a.row_bytes = static_cast<int>(dsa::cache_row_bytes(fmt, Dc, Dr));
+  a.n = n;
+  a.new_n = new_n;
+  return dsa::launch_cache_compact(a, as_stream(stream));
+}
+
 }  // extern "C"

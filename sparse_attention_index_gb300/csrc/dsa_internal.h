@@ -177,4 +177,17 @@ struct LatentArgs {
 size_t latent_attn_workspace(int B, int Sq, int H, int k);
 int launch_latent_attn(const LatentArgs& a, int fmt, cudaStream_t stream);
 
+// eviction (evict.cu): which positions stay, and their rows moved
+int launch_cache_keep(const float* mass, int n, const int32_t* lens, int B, int budget, int sink,
+                      int recent, int32_t* keep, int32_t* count, cudaStream_t stream);
+struct CompactArgs {
+  uint8_t* cache;
+  const int32_t *page_table, *lens, *keep, *new_table;   // new_table nullptr: in place
+  const float* mass;                                     // nullptr: no weights
+  float* new_mass;
+  long long num_pages;
+  int page_size, max_pages, new_max_pages, budget, B, row_bytes, n, new_n;
+};
+int launch_cache_compact(const CompactArgs& a, cudaStream_t stream);
+
 }  // namespace dsa

@@ -1,0 +1,455 @@
+// Eviction from the paged latent cache by accumulated attention weight: choosing the positions that
+// stay (dsa_cache_keep) and moving their rows (dsa_cache_compact). The weights themselves come from
+// mass.cu.
+//
+// Choosing. A cluster of CTAs has a sequence, each CTA an even slice of the positions that go by
+// their weight. The weights are mapped to integers that order like them and the budget's last one is
+// found digit by digit (11, 11 and 10 bits): a histogram per CTA in shared memory, added up over the
+// cluster through distributed shared memory. Ties at that value go to the lower positions: one pass
+// over the slice counts, an exclusive sum over warps and CTAs places, one more writes. The weights are
+// read from memory once and kept in shared memory as far as it holds them.
+// Bound: latency. 64 sequences of 8192 weights are 2 MB; the passes and their barriers are what it
+// takes.
+//
+// Moving. Rows are copied 16 bytes a thread; memory is the bound. To other pages, all rows at once. In
+// place, row keep[j] goes to position j <= keep[j] and ascending lists never overwrite a row that is
+// still to be read, as long as rows go in order: so a CTA takes a column slice of all rows of a
+// sequence and walks down, the slices being independent of one another.
+
+#include "dsa_common.cuh"
+#include "dsa_internal.h"
+
+namespace dsa {
+namespace {
+
+constexpr int kErrIdx = DSA_STAGE_EVICT | DSA_DEVERR_BAD_INDEX;
+constexpr int kErrPage = DSA_STAGE_EVICT | DSA_DEVERR_BAD_PAGE;
+
+// ------------------------------------------------------------------ choosing
+
+constexpr int kKeepThreads = 1024;
+constexpr int kKeepWarps = kKeepThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMostHeld = 49152;   // weights that a CTA keeps in shared memory (192 KB)
+
+struct KeepParams {
+  const float* mass;
+  const int32_t* lens;
+  int32_t *keep, *count;
+  int n, budget, sink, recent;
+  int held;   // weights per CTA that shared memory has room for
+  int* err;
+};
+
+struct KeepTail {
+  int hist[3][kBins];      // one per digit, so that a barrier per digit is enough
+  int above[kKeepWarps], equal[kKeepWarps];   // of each warp's part
+  int2 total;              // of the CTA
+  int sums[kKeepWarps];
+  int digit, left, exact;
+};
+
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
+  uint32_t a;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+// An integer that orders like the weight: -0 like +0, a NaN above everything.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  if (x != x) return 0xffffffffu;
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__global__ void __launch_bounds__(kKeepThreads) keep_kernel(const KeepParams p) {
+  extern __shared__ uint32_t keys[];
+  __shared__ KeepTail s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int C = cluster_size(), rank = cluster_rank(), b = blockIdx.x / C;
+  int len = __ldg(p.lens + b);
+  if (len < 0 || len > p.n) {
+    if (tid == 0) report_error(p.err, kErrPage);
+    len = max(0, min(len, p.n));
+  }
+  int32_t* keep = p.keep + static_cast<long long>(b) * p.budget;
+  const float* mass = p.mass + static_cast<long long>(b) * p.n;
+  if (rank == 0 && tid == 0) p.count[b] = min(len, p.budget);
+  if (len <= p.budget) {   // everything stays (the whole cluster leaves)
+    for (int j = rank * kKeepThreads + tid; j < p.budget; j += C * kKeepThreads)
+      keep[j] = j < len ? j : -1;
+    return;
+  }
+  const int m = p.budget - p.sink - p.recent;   // to be chosen by weight
+  for (int j = rank * kKeepThreads + tid; j < p.sink + p.recent; j += C * kKeepThreads) {
+    if (j < p.sink)
+      keep[j] = j;
+    else
+      keep[m + j] = len - (p.sink + p.recent) + j;
+  }
+  if (m == 0) return;
+
+  // this CTA's slice of the positions between the first and the newest ones, m < all
+  const int all = len - p.sink - p.recent;
+  const int per = ((all + C - 1) / C + 31) / 32 * 32;
+  const int at0 = min(all, rank * per), mine = min(all, at0 + per) - at0;
+  mass += p.sink + at0;
+  const bool held = per <= p.held;
+  for (int i = tid; i < 3 * kBins; i += kKeepThreads) (&s.hist[0][0])[i] = 0;
+  __syncthreads();
+#pragma unroll 8
+  for (int i = tid; i < mine; i += kKeepThreads) {
+    const uint32_t k = order_key(__ldg(mass + i));
+    if (held) keys[i] = k;
+    atomicAdd(&s.hist[0][k >> 21], 1);
+  }
+  auto key_at = [&](int i) { return held ? keys[i] : order_key(__ldg(mass + i)); };
+
+  // the m-th heaviest: its digits, and how many of the equal ones are taken
+  uint32_t found = 0;
+  int left = m;
+  bool exact = false;   // every weight with the digits found so far is taken
+  int shift = 21;
+#pragma unroll 1
+  for (int d = 0; d < 3; ++d) {
+    cluster_sync();
+    // bins from the top, two per thread
+    const int bins = d == 2 ? 1024 : 2048, hi = bins - 1 - 2 * tid;
+    int c0 = 0, c1 = 0;
+    if (hi > 0)
+      for (int r = 0; r < C; ++r) {
+        c0 += ld_cluster(&s.hist[d][hi], r);
+        c1 += ld_cluster(&s.hist[d][hi - 1], r);
+      }
+    int incl = c0 + c1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) s.sums[warp] = incl;
+    __syncthreads();
+    int before = incl - (c0 + c1);
+    for (int w = 0; w < warp; ++w) before += s.sums[w];
+    if (before < left && before + c0 >= left) {
+      s.digit = hi;
+      s.left = left - before;
+      s.exact = before + c0 == left;
+    } else if (before + c0 < left && before + c0 + c1 >= left) {
+      s.digit = hi - 1;
+      s.left = left - before - c0;
+      s.exact = before + c0 + c1 == left;
+    }
+    __syncthreads();
+    found = (found << (d == 2 ? 10 : 11)) | static_cast<uint32_t>(s.digit);
+    left = s.left;
+    exact = s.exact != 0;
+    if (d == 2 || exact) break;
+    const int next = d == 0 ? 10 : 0;   // the next digit's lowest bit
+#pragma unroll 4
+    for (int i = tid; i < mine; i += kKeepThreads) {
+      const uint32_t k = key_at(i);
+      if (k >> shift == found) atomicAdd(&s.hist[d + 1][(k >> next) & (d == 0 ? 2047u : 1023u)], 1);
+    }
+    shift = next;
+  }
+  const uint32_t low = found << shift;   // exact: the lightest that stays, or what is below it
+
+  // counts of each warp's part, then what is in front of it
+  const int part = (per / 32 + kKeepWarps - 1) / kKeepWarps * 32;
+  const int w0 = min(mine, warp * part), w1 = min(mine, w0 + part);
+  auto above = [&](uint32_t k) { return exact ? k >= low : k > low; };
+  auto equal = [&](uint32_t k) { return !exact && k == low; };
+  int na = 0, ne = 0;
+  for (int i = w0 + lane; i < w1; i += 32) {
+    const uint32_t k = key_at(i);
+    na += above(k);
+    ne += equal(k);
+  }
+  na = __reduce_add_sync(0xffffffffu, na);
+  ne = __reduce_add_sync(0xffffffffu, ne);
+  if (lane == 0) {
+    s.above[warp] = na;
+    s.equal[warp] = ne;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const int a = __reduce_add_sync(0xffffffffu, s.above[lane]);
+    const int e = __reduce_add_sync(0xffffffffu, s.equal[lane]);
+    if (lane == 0) s.total = make_int2(a, e);
+  }
+  cluster_sync();
+  int fa = 0, fe = 0;
+  for (int r = 0; r < rank; ++r) {
+    fa += ld_cluster(&s.total.x, r);
+    fe += ld_cluster(&s.total.y, r);
+  }
+  for (int w = 0; w < warp; ++w) {
+    fa += s.above[w];
+    fe += s.equal[w];
+  }
+  const uint32_t lower = (1u << lane) - 1;
+  for (int i0 = w0; i0 < w1; i0 += 32) {
+    const bool in = i0 + lane < w1;
+    const uint32_t k = in ? key_at(i0 + lane) : 0u;
+    const uint32_t ma = __ballot_sync(0xffffffffu, in && above(k));
+    const uint32_t me = __ballot_sync(0xffffffffu, in && equal(k));
+    const int ea = fe + __popc(me & lower);   // equal ones in front
+    const bool taken = (ma >> lane & 1u) || ((me >> lane & 1u) && ea < left);
+    if (taken) keep[p.sink + fa + __popc(ma & lower) + min(ea, left)] = p.sink + at0 + i0 + lane;
+    fa += __popc(ma);
+    fe += __popc(me);
+  }
+  cluster_sync();   // no CTA leaves while another may still read its counts
+}
+
+// ------------------------------------------------------------------ moving
+
+constexpr int kMoveThreads = 256, kMoveRows = 16;   // rows of a block
+constexpr int kWalkThreads = 512, kWalkDepth = 4;   // 16-byte pieces per thread and step
+
+struct MoveParams {
+  uint8_t* cache;
+  const int32_t *page_table, *lens, *keep, *new_table;
+  const float* mass;
+  float* new_mass;
+  long long num_pages, rows;   // rows: B * budget
+  int page_size, max_pages, new_max_pages, budget, upr;   // upr: 16-byte units per row
+  int n, new_n;                // columns of mass and new_mass
+  int B, unit_slice;
+  int* err;
+};
+
+__device__ __forceinline__ int seq_len(const MoveParams& p, int b) {
+  const int cap = p.max_pages * p.page_size;
+  const int len = __ldg(p.lens + b);
+  if (len < 0 || len > cap) report_error(p.err, kErrPage);
+  return max(0, min(len, cap));
+}
+
+// the slot of position j, -1 where its page is not one of the cache
+__device__ __forceinline__ long long slot_of(const MoveParams& p, const int32_t* table, int j) {
+  const int pg = j / p.page_size;
+  const int page = __ldg(table + pg);
+  if (page < 0 || page >= p.num_pages) {
+    report_error(p.err, kErrPage);
+    return -1;
+  }
+  return static_cast<long long>(page) * p.page_size + (j - pg * p.page_size);
+}
+
+// a list entry, -1 where it names no row
+__device__ __forceinline__ int entry(const MoveParams& p, long long row, int len) {
+  const int e = __ldg(p.keep + row);
+  if (e < -1 || e >= len) {
+    report_error(p.err, kErrIdx);
+    return -1;
+  }
+  return e;
+}
+
+// to other pages: kMoveRows rows per block
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) {
+  __shared__ long long src[kMoveRows], dst[kMoveRows];
+  const long long row0 = static_cast<long long>(blockIdx.x) * kMoveRows;
+  if (threadIdx.x < kMoveRows) {
+    const long long row = row0 + threadIdx.x;
+    long long from = -1, to = -1;
+    if (row < p.rows) {
+      const int b = static_cast<int>(row / p.budget), j = static_cast<int>(row - static_cast<long long>(b) * p.budget);
+      const int e = entry(p, row, seq_len(p, b));
+      float w = 0.f;
+      if (e >= 0) {
+        from = slot_of(p, p.page_table + static_cast<long long>(b) * p.max_pages, e);
+        to = slot_of(p, p.new_table + static_cast<long long>(b) * p.new_max_pages, j);
+        if (p.mass && e < p.n) w = __ldg(p.mass + static_cast<long long>(b) * p.n + e);
+      }
+      if (p.mass) p.new_mass[static_cast<long long>(b) * p.new_n + j] = w;
+    }
+    src[threadIdx.x] = to < 0 ? -1 : from;
+    dst[threadIdx.x] = to;
+  }
+  __syncthreads();
+  const uint4* in = reinterpret_cast<const uint4*>(p.cache);
+  uint4* out = reinterpret_cast<uint4*>(p.cache);
+  const uint32_t upr = p.upr, units = kMoveRows * upr;
+#pragma unroll 4
+  for (uint32_t u = threadIdx.x; u < units; u += kMoveThreads) {
+    const uint32_t r = u / upr, c = u - r * upr;
+    if (src[r] >= 0) out[dst[r] * upr + c] = __ldcs(in + src[r] * upr + c);
+  }
+  if (p.mass && p.new_n > p.budget) {   // the weights' ends, shared out among the blocks
+    const int tail = p.new_n - p.budget;
+    const long long count = static_cast<long long>(p.B) * tail;
+    const long long each = (count + gridDim.x - 1) / gridDim.x;
+    const long long end = min(count, (blockIdx.x + 1ll) * each);
+    for (long long i = blockIdx.x * each + threadIdx.x; i < end; i += kMoveThreads) {
+      const long long b = i / tail;
+      p.new_mass[b * p.new_n + p.budget + (i - b * tail)] = 0.f;
+    }
+  }
+}
+
+// in place: block (slice, b) walks down the rows of sequence b
+__global__ void __launch_bounds__(kWalkThreads, 2) walk_kernel(const MoveParams p) {
+  const int b = blockIdx.y, per = p.unit_slice;
+  const int u = blockIdx.x * per + threadIdx.x % per;
+  const int step = kWalkThreads / per, chunk = step * kWalkDepth;
+  const int len = seq_len(p, b);
+  const int32_t* table = p.page_table + static_cast<long long>(b) * p.max_pages;
+  uint4* data = reinterpret_cast<uint4*>(p.cache);
+  const int end = min(p.budget, len);   // row j comes from a position j or later
+  uint4 v[2][kWalkDepth];
+  long long to[2][kWalkDepth];
+  auto load = [&](int c, uint4 (&x)[kWalkDepth], long long (&dst)[kWalkDepth]) {
+#pragma unroll
+    for (int k = 0; k < kWalkDepth; ++k) {
+      const int j = c * chunk + k * step + threadIdx.x / per;
+      dst[k] = -1;
+      if (j >= end || u >= p.upr) continue;
+      const int e = entry(p, static_cast<long long>(b) * p.budget + j, len);
+      if (e < 0 || e == j) continue;
+      if (e < j) {   // not an ascending list
+        report_error(p.err, kErrIdx);
+        continue;
+      }
+      const long long from = slot_of(p, table, e), at = slot_of(p, table, j);
+      if (from < 0 || at < 0) continue;
+      x[k] = data[from * p.upr + u];
+      dst[k] = at * p.upr + u;
+    }
+  };
+  auto store = [&](const uint4 (&x)[kWalkDepth], const long long (&dst)[kWalkDepth]) {
+#pragma unroll
+    for (int k = 0; k < kWalkDepth; ++k)
+      if (dst[k] >= 0) data[dst[k]] = x[k];
+  };
+  // What chunk c + 1 reads lies behind all that chunks up to c write, so its loads go first; what
+  // chunk c reads may be what it writes itself, so a barrier parts the two.
+  const int chunks = (end + chunk - 1) / chunk;
+  load(0, v[0], to[0]);
+#pragma unroll 1
+  for (int c = 0; c < chunks; c += 2) {
+    __syncthreads();
+    load(c + 1, v[1], to[1]);
+    store(v[0], to[0]);
+    __syncthreads();
+    load(c + 2, v[0], to[0]);
+    store(v[1], to[1]);
+  }
+}
+
+// The weights of sequence b, walked down the same way (new_mass may be mass), and zeros behind them.
+__global__ void __launch_bounds__(kWalkThreads) walk_mass_kernel(const MoveParams p) {
+  const int b = blockIdx.x;
+  const int len = seq_len(p, b);
+  const float* mass = p.mass + static_cast<long long>(b) * p.n;
+  float* out = p.new_mass + static_cast<long long>(b) * p.new_n;
+  constexpr int kDepth = 8, kChunk = kWalkThreads * kDepth;
+  for (int j0 = 0; j0 < p.new_n; j0 += kChunk) {
+    float x[kDepth];
+#pragma unroll
+    for (int k = 0; k < kDepth; ++k) {
+      const int j = j0 + k * kWalkThreads + threadIdx.x;
+      x[k] = 0.f;
+      if (j < p.budget) {
+        const int e = entry(p, static_cast<long long>(b) * p.budget + j, len);
+        if (e >= j && e < p.n) x[k] = mass[e];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kDepth; ++k) {
+      const int j = j0 + k * kWalkThreads + threadIdx.x;
+      if (j < p.new_n) out[j] = x[k];
+    }
+  }
+}
+
+}  // namespace
+
+int launch_cache_keep(const float* mass, int n, const int32_t* lens, int B, int budget, int sink,
+                      int recent, int32_t* keep, int32_t* count, cudaStream_t stream) {
+  KeepParams p = {mass, lens, keep, count, n, budget, sink, recent, 0, device_error_word()};
+  int C = 8;
+  while (C > 1 && ((n + C - 1) / C < 2048 || static_cast<long long>(B) * C > 304)) C /= 2;
+  const int per = ((n + C - 1) / C + 31) / 32 * 32;
+  p.held = per <= kMostHeld ? per : 0;
+  const size_t smem = static_cast<size_t>(p.held) * 4;
+  if (static_cast<long long>(B) * C > 0x7fffffffLL) return DSA_ERR_UNSUPPORTED;
+  if (cudaFuncSetAttribute(keep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kMostHeld * 4) != cudaSuccess)
+    return DSA_ERR_CUDA;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = C;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(B) * C);
+  cfg.blockDim = dim3(kKeepThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, keep_kernel, p) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+int launch_cache_compact(const CompactArgs& a, cudaStream_t stream) {
+  MoveParams p = {};
+  p.cache = a.cache;
+  p.page_table = a.page_table;
+  p.lens = a.lens;
+  p.keep = a.keep;
+  p.new_table = a.new_table;
+  p.num_pages = a.num_pages;
+  p.rows = static_cast<long long>(a.B) * a.budget;
+  p.page_size = a.page_size;
+  p.max_pages = a.max_pages;
+  p.new_max_pages = a.new_max_pages;
+  p.budget = a.budget;
+  p.upr = a.row_bytes / 16;
+  p.n = a.n;
+  p.new_n = a.new_n;
+  p.B = a.B;
+  p.err = device_error_word();
+  const bool walk_mass = a.mass && (!a.new_table || a.new_mass == a.mass);
+  if (walk_mass) {
+    MoveParams w = p;
+    w.mass = a.mass;
+    w.new_mass = a.new_mass;
+    walk_mass_kernel<<<a.B, kWalkThreads, 0, stream>>>(w);
+    if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
+  } else {
+    p.mass = a.mass;
+    p.new_mass = a.new_mass;
+  }
+  if (a.new_table) {
+    const long long blocks = (p.rows + kMoveRows - 1) / kMoveRows;
+    if (blocks > 0x7fffffffLL) return DSA_ERR_UNSUPPORTED;
+    move_kernel<<<static_cast<unsigned>(blocks), kMoveThreads, 0, stream>>>(p);
+  } else {
+    p.unit_slice = 8;
+    while (p.unit_slice > 2 && static_cast<long long>(a.B) * (p.upr / p.unit_slice) < 304)
+      p.unit_slice /= 2;
+    const dim3 grid((p.upr + p.unit_slice - 1) / p.unit_slice, a.B);
+    walk_kernel<<<grid, kWalkThreads, 0, stream>>>(p);
+  }
+  return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+}  // namespace dsa
