@@ -587,6 +587,41 @@ int dsa_latent_attn(const void* Q, const void* cache, int fmt, int64_t num_pages
                     void* O, float* lse, void* ws, size_t ws_bytes, void* stream);
 
 /*
+ * dsa_latent_attn_shared - dsa_latent_attn for sequences that share long prefixes, each stored once
+ * in the cache: the prefix of group g is prefix_lens[g] positions in the pages prefix_table[g,:], and
+ * the sequences starts[g] <= b < starts[g+1] are its group (G + 1 starts that go up; a sequence in
+ * front of the first or behind the last has no prefix). Token i of sequence b sees every position of
+ * its group's prefix, then its own positions 0 <= j <= lens[b] - Sq + i in the pages page_table[b,:];
+ * lens counts the sequence's own positions, its Sq new ones among them:
+ *
+ *     O[b,i,h] = sum softmax(l) row[0 : Dc],   lse[b,i,h] = log sum exp(l),   l = scale * Q[b,i,h] . row
+ *
+ * over both. The rows of a group's prefix are read for up to 128 (token, head) pairs of the group at
+ * once, whatever sequences they belong to; the two parts are joined in fp32. A token that has no
+ * position of its own (len < Sq - i: padding) sees no prefix either: O = 0 and lse = -inf.
+ *
+ *   prefix_table int32 [G, max_prefix_pages]   prefix_lens int32 [G]   starts int32 [G + 1]
+ *   Q, cache, page_table, lens, O, lse as for dsa_latent_attn
+ *   ws    workspace of dsa_latent_attn_shared_workspace_size() bytes (overwritten): fp32 parts, about
+ *         2 KB for each of two parts per (token, head). Nothing is kept in it between calls.
+ *
+ * Lengths, prefix lengths and pages outside their range are treated and recorded as by
+ * dsa_latent_attn; a start below the one in front of it, below 0 or above B is taken as the nearest
+ * that is not and recorded as DSA_STAGE_LATENT | DSA_DEVERR_BAD_INDEX. Infinities, NaNs, roundings and
+ * the order of sums as for dsa_latent_attn.
+ *
+ * Supported: as for dsa_latent_attn, with 1 <= G <= 64, max_prefix_pages * page_size < 2^31 and
+ * B * Sq * H < 2^30.
+ */
+size_t dsa_latent_attn_shared_workspace_size(int B, int Sq, int H, int G, int Dc, int Dr);
+int dsa_latent_attn_shared(const void* Q, const void* cache, int fmt, int64_t num_pages,
+                           int page_size, const int32_t* prefix_table, int max_prefix_pages,
+                           const int32_t* prefix_lens, const int32_t* starts, int G,
+                           const int32_t* page_table, int max_pages, const int32_t* lens, int B,
+                           int Sq, int H, int Dc, int Dr, float scale, void* O, float* lse, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/*
  * Eviction from the cache by accumulated attention weight: dsa_cache_mass adds up what weight each
  * cached position receives, dsa_cache_keep chooses the positions that stay within a budget, and
  * dsa_cache_compact moves their rows.

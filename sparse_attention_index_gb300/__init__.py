@@ -17,6 +17,7 @@ Entry points (same names as the C ABI):
 * ``dsa_rope`` - rotary positions on part of each head, and their inverse (the gradient)
 * ``dsa_cache_write`` / ``dsa_cache_read`` - rows of the paged latent cache (bf16 or e4m3)
 * ``dsa_latent_attn`` - attention of the newest tokens over that cache -> (O, lse)
+* ``dsa_latent_attn_shared`` - the same for sequences that share long prefixes, stored once
 * ``dsa_cache_keep`` / ``dsa_cache_compact`` - the positions that stay in the cache by their attention
   weight, and their rows moved
 * ``dsa_decode_layer`` - these together, one serving step
@@ -55,7 +56,8 @@ EXPORTS = ("dsa_status_string", "dsa_version", "dsa_get_last_device_error", "dsa
            "dsa_index_topk_workspace_size", "dsa_index_topk", "dsa_index_topk_fp8",
            "dsa_index_topk_stream_workspace_size", "dsa_index_topk_stream",
            "dsa_index_topk_stream_fp8", "dsa_rope", "dsa_cache_row_bytes", "dsa_cache_write",
-           "dsa_cache_read", "dsa_latent_attn_workspace_size", "dsa_latent_attn", "dsa_cache_keep",
+           "dsa_cache_read", "dsa_latent_attn_workspace_size", "dsa_latent_attn",
+           "dsa_latent_attn_shared_workspace_size", "dsa_latent_attn_shared", "dsa_cache_keep",
            "dsa_cache_compact")
 
 
@@ -119,11 +121,15 @@ def _load() -> ctypes.CDLL:
     lib.dsa_latent_attn_workspace_size.restype = sz
     lib.dsa_latent_attn.argtypes = [vp, vp, ci, i64, ci, vp, ci, vp, vp, ci, ci, ci, ci, ci, ci, cf,
                                     vp, vp, vp, sz, vp]
+    lib.dsa_latent_attn_shared_workspace_size.argtypes = [ci, ci, ci, ci, ci, ci]
+    lib.dsa_latent_attn_shared_workspace_size.restype = sz
+    lib.dsa_latent_attn_shared.argtypes = [vp, vp, ci, i64, ci, vp, ci, vp, vp, ci, vp, ci, vp, ci, ci,
+                                           ci, ci, ci, cf, vp, vp, vp, sz, vp]
     lib.dsa_cache_keep.argtypes = [vp, ci, vp, ci, ci, ci, ci, vp, vp, vp]
     lib.dsa_cache_compact.argtypes = [vp, ci, i64, ci, vp, ci, vp, vp, ci, vp, ci, ci, ci, ci, vp, ci,
                                       vp, ci, vp]
     for name in ("dsa_rope", "dsa_cache_write", "dsa_cache_read", "dsa_latent_attn",
-                 "dsa_cache_keep", "dsa_cache_compact",
+                 "dsa_latent_attn_shared", "dsa_cache_keep", "dsa_cache_compact",
                  "dsa_get_last_device_error", "dsa_index_scores", "dsa_index_scores_fp8", "dsa_topk",
                  "dsa_indexer_loss", "dsa_indexer_loss_bwd", "dsa_index_topk",
                  "dsa_index_topk_fp8", "dsa_index_topk_stream", "dsa_index_topk_stream_fp8",
@@ -964,6 +970,59 @@ def dsa_latent_attn(Q, cache, page_table, lens, scale: float, fmt: str = "e4m3",
     """
     args, O, lse, ws = _latent_args(Q, cache, page_table, lens, scale, fmt, idx, Dc, O, lse, ws, stream)
     _call(lib.dsa_latent_attn, "dsa_latent_attn", Q.device, stream, *args)
+    return O, lse
+
+
+@functools.lru_cache(maxsize=1024)
+def latent_attn_shared_workspace_bytes(B, Sq, H, G, Dc, Dr) -> int:
+    return int(lib.dsa_latent_attn_shared_workspace_size(B, Sq, H, G, Dc, Dr))
+
+
+def dsa_latent_attn_shared(Q, cache, prefix_table, prefix_lens, starts, page_table, lens, scale: float,
+                           fmt: str = "e4m3", Dc: int = 512, O=None, lse=None, ws=None, stream=None):
+    """dsa_latent_attn for sequences that share long prefixes, each stored once in the cache.
+
+    prefix_table int32 [G, max_prefix_pages] and prefix_lens int32 [G]: the prefix of each group;
+    starts int32 [G + 1]: the sequences starts[g] <= b < starts[g + 1] are group g (those in front of
+    the first start and behind the last have no prefix). Every token sees its group's whole prefix and
+    then its own cached positions; page_table and lens are the sequences' own, without the prefix. The
+    rest as for dsa_latent_attn -> (O bf16 [B,Sq,H,Dc], lse fp32 [B,Sq,H]).
+
+    ws: a device byte buffer of at least latent_attn_shared_workspace_bytes(...) (allocated here if
+    None). What is allocated here is allocated on `stream`.
+    """
+    qp = _dev(Q, "Q", torch.bfloat16)
+    if Q.dim() != 4 or Q.shape[3] < Dc:
+        raise ValueError("Q must be [B, Sq, H, Dc + Dr]")
+    B, Sq, H, D = Q.shape
+    Dr, dev = D - Dc, Q.device
+    cp, _ = _cache_arg(cache, Dc, Dr, fmt, dev)
+    if cache.dim() != 3:
+        raise ValueError("cache must be [num_pages, page_size, row_bytes]")
+    if page_table.dim() != 2 or prefix_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages] and prefix_table [G, max_prefix_pages]")
+    G, P = prefix_table.shape
+    _int32(B, Sq, H, G, P, cache.shape[1], page_table.shape[1])
+    gp = _arg(prefix_table, "prefix_table", torch.int32, (G, P), dev)
+    pp = _arg(prefix_lens, "prefix_lens", torch.int32, (G,), dev)
+    sp = _arg(starts, "starts", torch.int32, (G + 1,), dev)
+    tp = _arg(page_table, "page_table", torch.int32, (B, page_table.shape[1]), dev)
+    lp = _arg(lens, "lens", torch.int32, (B,), dev)
+    if O is None:
+        O = _empty((B, Sq, H, Dc), torch.bfloat16, dev, stream)
+    if lse is None:
+        lse = _empty((B, Sq, H), torch.float32, dev, stream)
+    op = _arg(O, "O", torch.bfloat16, (B, Sq, H, Dc), dev)
+    ep = _arg(lse, "lse", torch.float32, (B, Sq, H), dev)
+    need = latent_attn_shared_workspace_bytes(B, Sq, H, G, Dc, Dr)
+    if ws is None and need > 0:
+        ws = _empty((need,), torch.uint8, dev, stream)
+    if ws is not None and ws.device != dev:
+        raise ValueError(f"ws is on {ws.device}, the other arguments on {dev}")
+    _call(lib.dsa_latent_attn_shared, "dsa_latent_attn_shared", dev, stream, qp, cp,
+          _CACHE_FORMATS[fmt], cache.shape[0], cache.shape[1], gp, P, pp, sp, G, tp,
+          page_table.shape[1], lp, B, Sq, H, Dc, Dr, float(scale), op, ep,
+          None if ws is None else _dev(ws, "ws"), 0 if ws is None else ws.numel() * ws.element_size())
     return O, lse
 
 

@@ -595,6 +595,61 @@ int dsa_latent_attn(const void* Q, const void* cache, int fmt, int64_t num_pages
   return dsa::launch_latent_attn(a, fmt, as_stream(stream));
 }
 
+size_t dsa_latent_attn_shared_workspace_size(int B, int Sq, int H, int G, int Dc, int Dr) {
+  if (B < 1 || Sq < 1 || H < 1 || H > 128 || Dc != 512 || Dr != 64 || G < 1 ||
+      G > dsa::kLatentGroups || static_cast<long long>(B) * Sq >= (1LL << 30) / H)
+    return 0;
+  return dsa::latent_attn_shared_workspace(B, Sq, H, G);
+}
+
+int dsa_latent_attn_shared(const void* Q, const void* cache, int fmt, int64_t num_pages,
+                           int page_size, const int32_t* prefix_table, int max_prefix_pages,
+                           const int32_t* prefix_lens, const int32_t* starts, int G,
+                           const int32_t* page_table, int max_pages, const int32_t* lens, int B,
+                           int Sq, int H, int Dc, int Dr, float scale, void* O, float* lse, void* ws,
+                           size_t ws_bytes, void* stream) {
+  if (!Q || !cache || !prefix_table || !prefix_lens || !starts || !page_table || !lens || !O || !lse)
+    return DSA_ERR_INVALID_ARG;
+  if (B < 1 || Sq < 1 || H < 1 || G < 1 || Dc < 1 || Dr < 0 || num_pages < 1 || page_size < 1 ||
+      max_pages < 1 || max_prefix_pages < 1)
+    return DSA_ERR_INVALID_ARG;
+  if (fmt != DSA_CACHE_BF16 && fmt != DSA_CACHE_E4M3) return DSA_ERR_INVALID_ARG;
+  const void* ptrs[] = {Q, cache, prefix_table, prefix_lens, starts, page_table, lens, O, lse};
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return DSA_ERR_INVALID_ARG;
+  const size_t need = dsa_latent_attn_shared_workspace_size(B, Sq, H, G, Dc, Dr);
+  if (need == 0) return DSA_ERR_UNSUPPORTED;
+  if (!(scale > 0.f) || scale > 2.0e38f) return DSA_ERR_UNSUPPORTED;   // times log2(e) finite
+  const long long most = 1LL << 31;   // positions and slots are counted in 32 bits
+  if (num_pages >= most || num_pages * page_size >= most ||
+      static_cast<long long>(max_pages) * page_size >= most ||
+      static_cast<long long>(max_prefix_pages) * page_size >= most)
+    return DSA_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < need || !aligned16(ws)) return DSA_ERR_WORKSPACE;
+  dsa::LatentArgs a = {};
+  a.Q = static_cast<const uint16_t*>(Q);
+  a.cache = static_cast<const uint8_t*>(cache);
+  a.page_table = page_table;
+  a.lens = lens;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  a.B = B;
+  a.Sq = Sq;
+  a.H = H;
+  a.scale = scale;
+  a.O = static_cast<uint16_t*>(O);
+  a.lse = lse;
+  a.ws = ws;
+  a.err = dsa::device_error_word();
+  a.prefix_table = prefix_table;
+  a.prefix_lens = prefix_lens;
+  a.starts = starts;
+  a.G = G;
+  a.max_prefix = max_prefix_pages;
+  return dsa::launch_latent_attn_shared(a, fmt, as_stream(stream));
+}
+
 int dsa_cache_keep(const float* mass, int n, const int32_t* lens, int B, int budget, int sink,
                    int recent, int32_t* keep, int32_t* count, void* stream) {
   if (!mass || !lens || !keep || !count) return DSA_ERR_INVALID_ARG;

@@ -173,9 +173,15 @@ struct LatentArgs {
   float* lse;
   void* ws;
   int* err;
+  // shared prefixes
+  const int32_t *prefix_table, *prefix_lens, *starts;
+  int G, max_prefix;
 };
 size_t latent_attn_workspace(int B, int Sq, int H, int k);
 int launch_latent_attn(const LatentArgs& a, int fmt, cudaStream_t stream);
+constexpr int kLatentGroups = 64;   // groups that dsa_latent_attn_shared takes
+size_t latent_attn_shared_workspace(int B, int Sq, int H, int G);
+int launch_latent_attn_shared(const LatentArgs& a, int fmt, cudaStream_t stream);
 
 // eviction (evict.cu): which positions stay, and their rows moved
 int launch_cache_keep(const float* mass, int n, const int32_t* lens, int B, int budget, int sink,

@@ -80,6 +80,8 @@ constexpr int kErrIdx = DSA_STAGE_LATENT | DSA_DEVERR_BAD_INDEX;
 constexpr int kErrPage = DSA_STAGE_LATENT | DSA_DEVERR_BAD_PAGE;
 constexpr int kErrTime = DSA_STAGE_LATENT | DSA_DEVERR_TIMEOUT;
 static_assert(kKeysPerWarp == 8, "the keys of a gather warp are one byte of the chunk's mask");
+constexpr int kMaxGroups = kLatentGroups;   // groups of sequences that share a prefix
+constexpr int kAllSee = -0x7fffffff - 1;   // Header::lim0 of a prefix's tile: every row sees every key
 
 // e4m3: 48 keys x 16 pieces of 16 codes and 48 x 4 of positional dims, four and one per gather
 // thread, and two scales per key, in a ring of raw chunks
@@ -129,6 +131,9 @@ struct Tail {
   int item0, c0;
   long long first, end;
   int each;
+  // shared prefixes: first sequence of each group and the end of the last, first tile of each group's
+  // rows and their number, keys of its prefix
+  int gstart[kMaxGroups + 1], gtile[kMaxGroups + 1], gkeys[kMaxGroups];
 };
 
 static_assert(Layout<false>::kTailOff + sizeof(Tail) <= kSmemMost &&
@@ -150,6 +155,12 @@ struct Params {
   float2* ml;       // [2 * clusters][prow]: running max (of the logits before scale) and sum
   int2* joins;      // [clusters]: the tile that begins in a cluster's range and goes on behind it
                     // (-1: none), and the last cluster that works on it
+  // Shared prefixes: the tiles of the groups' rows over their prefixes come first, then those of the
+  // sequences over their own keys. Each leaves parts, tile i's of cluster c at i + c (which goes up
+  // along the work, so that no two have the same); part, ml: [most tiles + clusters].
+  int most_items;   // tiles that there can be
+  int2* spans;      // [most tiles]: the first and the last cluster of each
+  int* groups;      // the tables of Tail, for the join: gstart, gtile
 };
 
 // ------------------------------------------------------------------ the split
@@ -166,9 +177,30 @@ __device__ __forceinline__ int tile_rows(const Params& p, int mt) {
   return min(128, p.a.Sq * p.a.H - mt * 128);
 }
 
+// the group whose tiles `item` is one of (item < gtile[G])
+__device__ __forceinline__ int group_of(const Params& p, const Tail* tail, int item) {
+  int g = 0;
+  for (int n = p.a.G; n > 1;) {   // the last one that begins at or in front of it
+    const int half = n >> 1;
+    if (tail->gtile[g + half] <= item) g += half;
+    n -= half;
+  }
+  return g;
+}
+
 // first row of tile `item` in Q, O and lse, and the rows it has
-__device__ __forceinline__ long long rows_of(const Params& p, int item, int& rows) {
-  if (p.a.idx) {
+template <bool SHARED>
+__device__ __forceinline__ long long rows_of(const Params& p, const Tail* tail, int item, int& rows) {
+  if (SHARED) {
+    const int prefix_tiles = tail->gtile[p.a.G];
+    if (item < prefix_tiles) {
+      const int g = group_of(p, tail, item), row = (item - tail->gtile[g]) * 128;
+      const int per = p.a.Sq * p.a.H;
+      rows = min(128, (tail->gstart[g + 1] - tail->gstart[g]) * per - row);
+      return static_cast<long long>(tail->gstart[g]) * per + row;
+    }
+    item -= prefix_tiles;
+  } else if (p.a.idx) {
     rows = p.a.H;
     return static_cast<long long>(item) * p.a.H;
   }
@@ -187,8 +219,14 @@ __device__ __forceinline__ int tile_keys(const Params& p, int len, int mt) {
 // (keys + kNK - 1 may be past 32 bits)
 __device__ __forceinline__ int chunks_of(int keys) { return keys > 0 ? (keys - 1) / kNK + 1 : 1; }
 
-__device__ __forceinline__ int item_chunks(const Params& p, int item) {
-  if (p.a.idx) return p.list_chunks;
+template <bool SHARED>
+__device__ __forceinline__ int item_chunks(const Params& p, const Tail* tail, int item) {
+  if (SHARED) {
+    if (item < tail->gtile[p.a.G]) return chunks_of(tail->gkeys[group_of(p, tail, item)]);
+    item -= tail->gtile[p.a.G];
+  } else if (p.a.idx) {
+    return p.list_chunks;
+  }
   const int b = item / p.tiles;
   return chunks_of(tile_keys(p, seq_len(p.a, b, false), item - b * p.tiles));
 }
@@ -200,16 +238,18 @@ __device__ __forceinline__ int item_chunks(const Params& p, int item) {
 // (its Q, an empty pipeline, an output), so a tile weighs that much in front of its chunks. Cluster
 // c has the chunks at weights [each c, each (c + 1)). Short ranges count no such cost: they would be
 // cut into setups alone.
+template <bool SHARED>
 __device__ __forceinline__ void my_chunks(const Params& p, int cluster, Tail* tail) {
+  const int items = SHARED ? tail->gtile[p.a.G] + p.items : p.items;
   long long total, before = 0, s = 0;   // chunks: of all tiles, in front of this thread's, of its own
   int i0 = 0, i1 = 0;                   // this thread's tiles
-  if (p.a.idx) {
+  if (!SHARED && p.a.idx) {
     total = static_cast<long long>(p.items) * p.list_chunks;
   } else {
-    const int q = (p.items + kThreads - 1) / kThreads;
-    i0 = min(p.items, static_cast<int>(threadIdx.x) * q);
-    i1 = min(p.items, i0 + q);
-    for (int i = i0; i < i1; ++i) s += item_chunks(p, i);
+    const int q = (items + kThreads - 1) / kThreads;
+    i0 = min(items, static_cast<int>(threadIdx.x) * q);
+    i1 = min(items, i0 + q);
+    for (int i = i0; i < i1; ++i) s += item_chunks<SHARED>(p, tail, i);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     long long incl = s;
 #pragma unroll
@@ -227,14 +267,14 @@ __device__ __forceinline__ void my_chunks(const Params& p, int cluster, Tail* ta
     before += incl - s;
   }
   const int cost = (total + p.clusters - 1) / p.clusters >= 4 * kTileCost ? kTileCost : 0;
-  const long long weight = total + static_cast<long long>(cost) * p.items;
+  const long long weight = total + static_cast<long long>(cost) * items;
   const long long each =
       max((weight + p.clusters - 1) / p.clusters, static_cast<long long>(kMinChunks));
   const long long w0 = each * cluster, w1 = min(w0 + each, weight);
   if (threadIdx.x == 0) tail->each = static_cast<int>(each);
   if (w0 >= weight) return;   // first and end stay 0
   if (w1 == weight && threadIdx.x == 0) tail->end = total;
-  if (p.a.idx) {
+  if (!SHARED && p.a.idx) {
     if (threadIdx.x != 0) return;
     const int per = cost + p.list_chunks;
     // chunks in front of weight w
@@ -250,7 +290,7 @@ __device__ __forceinline__ void my_chunks(const Params& p, int cluster, Tail* ta
   }
   long long at = before + static_cast<long long>(cost) * i0;   // weight in front of tile i
   for (int i = i0; i < i1; ++i) {
-    const int m = i1 - i0 == 1 ? static_cast<int>(s) : item_chunks(p, i);
+    const int m = i1 - i0 == 1 ? static_cast<int>(s) : item_chunks<SHARED>(p, tail, i);
     const long long end = at + cost + m;
     if (w0 >= at && w0 < end) {
       const int c = max(0, static_cast<int>(w0 - at) - cost);
@@ -262,6 +302,35 @@ __device__ __forceinline__ void my_chunks(const Params& p, int cluster, Tail* ta
     at = end;
     before += m;
   }
+}
+
+// The groups of sequences that share a prefix, into the tail: starts that go down or out of [0, B] are
+// taken as the nearest that do not, a group without rows or keys has no tiles. Every thread of the
+// block calls it.
+__device__ __forceinline__ void my_groups(const Params& p, bool report, Tail* tail) {
+  const int t = threadIdx.x, G = p.a.G;
+  if (t <= G) tail->gstart[t] = __ldg(p.a.starts + t);
+  if (t < G) {
+    const int cap = p.a.max_prefix * p.a.page_size, keys = __ldg(p.a.prefix_lens + t);
+    if (report && (keys < 0 || keys > cap)) report_error(p.a.err, kErrPage);
+    tail->gkeys[t] = max(0, min(keys, cap));
+  }
+  __syncthreads();
+  if (t == 0) {
+    int at = 0, tiles = 0;
+    bool bad = false;
+    for (int g = 0; g <= G; ++g) {
+      const int want = tail->gstart[g], got = max(at, min(want, p.a.B));
+      bad = bad || want != got;
+      if (g > 0) {
+        if (tail->gkeys[g - 1] > 0) tiles += ((got - at) * p.a.Sq * p.a.H + 127) / 128;
+      }
+      tail->gstart[g] = at = got;
+      tail->gtile[g] = tiles;
+    }
+    if (report && bad) report_error(p.a.err, kErrIdx);
+  }
+  __syncthreads();
 }
 
 // ------------------------------------------------------------------ small helpers
@@ -435,8 +504,21 @@ struct Cursor {
   int item, c, nch, len, keys, b, lim0;
 };
 
-__device__ __forceinline__ void enter_item(const Params& p, int item, Cursor& k) {
+template <bool SHARED>
+__device__ __forceinline__ void enter_item(const Params& p, const Tail* tail, int item, Cursor& k) {
   k.item = item;
+  if (SHARED) {
+    const int prefix_tiles = tail->gtile[p.a.G];
+    if (item < prefix_tiles) {
+      const int g = group_of(p, tail, item);
+      k.b = ~g;
+      k.keys = k.len = tail->gkeys[g];
+      k.nch = chunks_of(k.keys);
+      k.lim0 = kAllSee;
+      return;
+    }
+    item -= prefix_tiles;
+  }
   k.b = item / (p.a.idx ? p.a.Sq : p.tiles);
   const int at = item - k.b * (p.a.idx ? p.a.Sq : p.tiles);   // the token, or the tile
   k.len = seq_len(p.a, k.b, true);
@@ -451,7 +533,7 @@ __device__ __forceinline__ void enter_item(const Params& p, int item, Cursor& k)
   }
 }
 
-template <bool FP8>
+template <bool FP8, bool SHARED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     latent_attn_kernel(const Params p) {
   using L = Layout<FP8>;
@@ -503,7 +585,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // thread 0 has made this CTA's barriers; the peer's are ready once cluster_wait returns
   cluster_arrive();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  my_chunks(p, cluster, tail);
+  if (SHARED) {
+    my_groups(p, blockIdx.x == 0, tail);
+    if (blockIdx.x == 0 && threadIdx.x <= p.a.G) {
+      p.groups[threadIdx.x] = tail->gstart[threadIdx.x];
+      p.groups[kMaxGroups + 1 + threadIdx.x] = tail->gtile[threadIdx.x];
+    }
+  }
+  my_chunks<SHARED>(p, cluster, tail);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -512,7 +601,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (n == 0) {
     // nothing here (both CTAs agree)
-    if (threadIdx.x == 0 && rank == 0) p.joins[cluster] = make_int2(-1, 0);
+    if (!SHARED && threadIdx.x == 0 && rank == 0) p.joins[cluster] = make_int2(-1, 0);
     cluster_wait();
   } else if (warp >= kGatherWarp0) {
     // ================================================================ gather
@@ -520,8 +609,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int mykey = gw * kKeysPerWarp + (lane & 7);
     const long long row_bytes = FP8 ? kDc + 16 + 2 * kDr : 2 * kD;
     Cursor k;
-    enter_item(p, item0, k);
+    enter_item<SHARED>(p, tail, item0, k);
     k.c = c0;
+    const bool scribe = gw == 0 && lane == 0 && rank == 0;
+    if (SHARED && scribe && c0 == 0) p.spans[item0].x = cluster;
     int made = 0;   // chunks handed out
     // Three steps for the keys of four chunks, lane 8 i + j the warp's key j of the i-th of them:
     // the chunk and its list entry, the page of its position, its slot.
@@ -537,7 +628,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // the next tile's Q, to be read by the softmax warps some chunks later, on its way to L2
     auto prefetch_q = [&](int item) {
       int rows;
-      const long long r0 = rows_of(p, item, rows);
+      const long long r0 = rows_of<SHARED>(p, tail, item, rows);
       for (int i = gw * 32 + lane; i < rows * 5; i += kGatherThreads) {
         const int row = i / 5, piece = i - row * 5;
         const uint16_t* at = p.a.Q + (r0 + row) * kD +
@@ -560,7 +651,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         e.item = k.item;
         e.lim0 = k.lim0;
         const uint32_t j = static_cast<uint32_t>(c) * kNK + mykey;   // past 2^31 in a last chunk
-        e.raw = j < static_cast<uint32_t>(p.a.idx ? p.a.k : k.keys) ? static_cast<int>(j) : -1;
+        e.raw = j < static_cast<uint32_t>(!SHARED && p.a.idx ? p.a.k : k.keys) ? static_cast<int>(j) : -1;
       };
       if (made + 4 < n && k.c + 4 < k.nch) {
         take(lane >> 3);
@@ -573,19 +664,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (++made == n) {
             // a tile that begins here and goes on in later clusters
             const int left = k.nch - 1 - k.c;
-            if (gw == 0 && lane == 0 && rank == 0)
+            if (SHARED && scribe && left == 0) p.spans[k.item].y = cluster;
+            if (!SHARED && scribe)
               p.joins[cluster] =
                   left > 0 && k.c < n
                       ? make_int2(k.item, cluster + (left + tail->each - 1) / tail->each)
                       : make_int2(-1, 0);
           } else if (++k.c == k.nch) {
-            enter_item(p, k.item + 1, k);
+            if (SHARED && scribe) {
+              p.spans[k.item].y = cluster;
+              p.spans[k.item + 1].x = cluster;
+            }
+            enter_item<SHARED>(p, tail, k.item + 1, k);
             k.c = 0;
             prefetch_q(k.item);
           }
         }
       }
-      if (p.a.idx && e.raw >= 0)
+      if (!SHARED && p.a.idx && e.raw >= 0)
         e.raw = __ldg(p.a.idx + static_cast<long long>(e.item) * p.a.k + e.raw);
       return e;
     };
@@ -596,7 +692,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else if (e.raw >= 0 && e.raw < e.keys) {
         const int pg = p.page_shift >= 0 ? e.raw >> p.page_shift : e.raw / p.a.page_size;
         q.off = e.raw - pg * p.a.page_size;
-        q.page = __ldg(p.a.page_table + static_cast<long long>(e.b) * p.a.max_pages + pg);
+        q.page = __ldg((SHARED && e.b < 0
+                            ? p.a.prefix_table + static_cast<long long>(~e.b) * p.a.max_prefix
+                            : p.a.page_table + static_cast<long long>(e.b) * p.a.max_pages) + pg);
       }
       return q;
     };
@@ -876,7 +974,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // this CTA's dims of the row of Q, packed bf16 pairs, into the thread's TMEM lane
     auto load_q = [&](int item) {
       int rows;
-      const long long r0 = rows_of(p, item, rows);
+      const long long r0 = rows_of<SHARED>(p, tail, item, rows);
       const bool in = hrow < rows;
       const uint4* src = reinterpret_cast<const uint4*>(p.a.Q + (in ? r0 + hrow : 0) * kD);
       const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -943,11 +1041,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         cur = item;
         m = -INFINITY;
         l = 0.f;
-        r0 = rows_of(p, item, rows);
+        r0 = rows_of<SHARED>(p, tail, item, rows);
         // keys that this row sees: the tile's first token sees lim0, each later one one more
-        if (!p.a.idx) lim = h.lim0 + (static_cast<int>(r0 % H) + hrow) / H;
+        if (SHARED || !p.a.idx) lim = h.lim0 + (static_cast<int>(r0 % H) + hrow) / H;
       }
-      if (!p.a.idx) {
+      if (SHARED ? h.lim0 != kAllSee : !p.a.idx) {
         const int left = lim - c * kNK;   // keys of the chunk that the row sees
         if (left < kNK) vm = left <= 0 ? 0ull : vm & ((1ull << left) - 1);
       }
@@ -1073,7 +1171,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
       tail->lsum[wg][par][hrow] = l;
       l += other;
-      if (p.a.Sq > 1 && !p.a.idx && h.lim0 - c * kNK < kNK) {
+      if (p.a.Sq > 1 && (SHARED ? h.lim0 != kAllSee : !p.a.idx) && h.lim0 - c * kNK < kNK) {
         // Keys that the tile's later tokens see and its earlier ones do not: an infinity or a NaN in
         // one would go through the earlier ones' weight of zero. S has been worked out, and a token
         // that sees the key has it in its logit; in V it is dropped. (Here, where few registers are
@@ -1103,7 +1201,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         break;
       tc_fence_after();
       const long long row = r0 + hrow;
-      if (flags & 4) {
+      if (!SHARED && (flags & 4)) {
         const float inv = l == 0.f ? 0.f : 1.f / l;   // NaN stays NaN
         uint4* out = reinterpret_cast<uint4*>(p.a.O + row * kDc + rank * kHalf);
 #pragma unroll 1
@@ -1128,11 +1226,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           p.a.lse[row] = lse_of(p, m, l);
       } else {
         // part 0 of this cluster: a tile begun before its range; part 1: one that goes on behind
-        const int part = 2 * cluster + (item == item0 && c0 > 0 ? 0 : 1);
+        const int part = SHARED ? item + cluster : 2 * cluster + (item == item0 && c0 > 0 ? 0 : 1);
         float4* out = p.part + static_cast<long long>(part) * (kDc / 4) * p.prow +
                       static_cast<long long>(rank * (kHalf / 4)) * p.prow + hrow;
+        // (a warp's rows go out together, and of a tile of few rows the first warps alone)
 #pragma unroll 1
-        for (int d0 = 0; d0 < kHalf; d0 += 32) {
+        for (int d0 = SHARED && quarter * 32 >= rows ? kHalf : 0; d0 < kHalf; d0 += 32) {
           uint32_t ov[32];
           tmem_ld_x32(tmem + lane_off + kColO + d0, ov);
           tmem_ld_wait();
@@ -1184,7 +1283,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) latent_join_kernel(const Para
   // nothing to join, or not written: a cluster whose waits ran out (recorded) leaves what was there
   if (tile.x < 0 || tile.x >= p.items || tile.y <= first || tile.y >= p.clusters) return;
   int rows;
-  long long r0 = rows_of(p, tile.x, rows);
+  long long r0 = rows_of<false>(p, nullptr, tile.x, rows);
   rows -= blockIdx.y * 32;   // left from this block's first on
   r0 += blockIdx.y * 32;
   if (rows <= 0) return;
@@ -1257,6 +1356,115 @@ __global__ void __launch_bounds__(32 * kJoinWarps) latent_join_kernel(const Para
       pack4(v, sum[out_row] == 0.f ? 0.f : 1.f / sum[out_row]);
 }
 
+// The join of shared prefixes: block (x, y, z) rows [32 y, 32 y + 32) of a sequence's own tile x, one
+// per lane. A row's parts are those of its own tile and those of the tile of its group's rows that it
+// is in; the warps share the dims or the parts, as above.
+template <bool SHARE>
+__global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const Params p) {
+  __shared__ __align__(16) uint8_t buffer[2 * kMaxClusters * 32 * sizeof(float2)];
+  float2(*ml)[32] = reinterpret_cast<float2(*)[32]>(buffer);
+  // the warps' sums, in the same place later
+  float4(*acc)[kJoinD4][33] = reinterpret_cast<float4(*)[kJoinD4][33]>(buffer);
+  static_assert(sizeof(float4[kJoinWarps][kJoinD4][33]) <= sizeof(buffer), "they fit");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = p.a.G;
+  const int b = blockIdx.x / p.tiles, mt = blockIdx.x - b * p.tiles;
+  const int at = blockIdx.y * 32 + lane;   // row of the tile
+  if (static_cast<int>(blockIdx.y) * 32 >= tile_rows(p, mt)) return;
+  const bool in = at < tile_rows(p, mt);
+  const int per = p.a.Sq * p.a.H, row = mt * 128 + at;
+  // a token that has no place in its sequence (padding) has no key
+  const bool there = in && seq_len(p.a, b, false) - p.a.Sq + row / p.a.H >= 0;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int* gstart = p.groups;
+  const int* gtile = p.groups + kMaxGroups + 1;
+  int g = 0;
+  while (g < G && b >= __ldcg(gstart + g + 1)) ++g;
+  const int prefix_tiles = __ldcg(gtile + G);
+  // parts first[k] + i, i < n[k], at row where[k] of each: k = 0 the prefix's, k = 1 the own keys'
+  int first[2] = {0, 0}, n[2] = {0, 0}, where[2] = {0, at};
+  auto find = [&](int k, int item) {
+    if (item < 0 || item >= p.most_items) return;
+    const int2 s = __ldcg(p.spans + item);
+    // not written: a cluster whose waits ran out (recorded)
+    if (s.x < 0 || s.y < s.x || s.y >= p.clusters) return;
+    first[k] = item + s.x;
+    n[k] = s.y - s.x + 1;
+  };
+  if (there) {
+    find(1, prefix_tiles + blockIdx.x);
+    if (g < G && b >= __ldcg(gstart + g) && __ldcg(gtile + g + 1) > __ldcg(gtile + g)) {
+      const int off = (b - __ldcg(gstart + g)) * per + row;
+      where[0] = off & 127;
+      find(0, __ldcg(gtile + g) + (off >> 7));
+    }
+  }
+  const int parts = n[0] + n[1];
+  const int most = __reduce_max_sync(0xffffffffu, parts);
+  auto part_of = [&](int i) {
+    return static_cast<long long>(i < n[0] ? first[0] + i : first[1] + i - n[0]);
+  };
+  for (int i = warp; i < most; i += kJoinWarps)
+    if (i < parts) ml[i][lane] = __ldcg(p.ml + part_of(i) * p.prow + where[i >= n[0]]);
+  __syncthreads();
+  float top = -INFINITY, l = 0.f;
+  for (int i = 0; i < parts; ++i) top = fmaxf(top, ml[i][lane].x);
+  // a part without a key has m = -inf, l = 0 and O = 0; one with a NaN keeps it in l
+  auto weight = [&](float2 q) {
+    return q.x == -INFINITY ? (q.y == 0.f ? 0.f : 1.f) : exp2f((q.x - top) * p.scale_log2);
+  };
+  const int d4 = SHARE ? blockIdx.z * kJoinD4 : (blockIdx.z * kJoinWarps + warp) * kJoinD4;
+  float4 o[kJoinD4];
+#pragma unroll
+  for (int d = 0; d < kJoinD4; ++d) o[d] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = SHARE ? warp : 0; i < parts; i += SHARE ? kJoinWarps : 1) {
+    const float4* src = p.part + (part_of(i) * (kDc / 4) + d4) * p.prow + where[i >= n[0]];
+    float4 x[kJoinD4];
+#pragma unroll
+    for (int d = 0; d < kJoinD4; ++d) x[d] = __ldcg(src + d * p.prow);
+    const float w = weight(ml[i][lane]);
+#pragma unroll
+    for (int d = 0; d < kJoinD4; ++d) {
+      o[d].x += w * x[d].x;
+      o[d].y += w * x[d].y;
+      o[d].z += w * x[d].z;
+      o[d].w += w * x[d].w;
+    }
+  }
+  for (int i = 0; i < parts; ++i) l += weight(ml[i][lane]) * ml[i][lane].y;
+  const long long out_row = static_cast<long long>(b) * per + row;
+  if (blockIdx.z == 0 && warp == 0 && in) p.a.lse[out_row] = lse_of(p, top, l);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  auto pack4 = [](float4 v, float inv) {
+    return make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+  };
+  if (!SHARE) {
+    if (!in) return;
+    uint4* out = reinterpret_cast<uint4*>(p.a.O + out_row * kDc + d4 * 4);
+#pragma unroll
+    for (int d = 0; d < kJoinD4; d += 2) {
+      const uint2 a = pack4(o[d], inv), b = pack4(o[d + 1], inv);
+      out[d / 2] = make_uint4(a.x, a.y, b.x, b.y);
+    }
+    return;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int d = 0; d < kJoinD4; ++d) acc[warp][d][lane] = o[d];
+  __syncthreads();
+  if (warp >= kJoinD4 || !in) return;   // warp d: four dims of the lane's row
+  float4 v = acc[0][warp][lane];
+#pragma unroll
+  for (int w = 1; w < kJoinWarps; ++w) {
+    const float4 x = acc[w][warp][lane];
+    v.x += x.x;
+    v.y += x.y;
+    v.z += x.z;
+    v.w += x.w;
+  }
+  *reinterpret_cast<uint2*>(p.a.O + out_row * kDc + (d4 + warp) * 4) = pack4(v, inv);
+}
+
 int part_rows(int Sq, int H, int k) {
   const long long rows = k > 0 ? H : static_cast<long long>(Sq) * H;
   return static_cast<int>(rows < 128 ? (rows + 31) / 32 * 32 : 128);
@@ -1264,7 +1472,7 @@ int part_rows(int Sq, int H, int k) {
 
 // Clusters of the kernel that fit on the current device at once; the first call on a device also
 // raises the kernel's shared-memory limit there.
-template <bool FP8>
+template <bool FP8, bool SHARED>
 int resident_clusters(size_t smem) {
   constexpr int kMaxDevices = 64;
   static int known[kMaxDevices] = {};
@@ -1274,7 +1482,7 @@ int resident_clusters(size_t smem) {
   std::lock_guard<std::mutex> guard(lock);
   if (known[dev] == 0) {
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    if (cudaFuncSetAttribute(latent_attn_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(latent_attn_kernel<FP8, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem)) != cudaSuccess)
       return 0;
     cudaLaunchAttribute attr = {};
@@ -1288,7 +1496,7 @@ int resident_clusters(size_t smem) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int c = 0;
-    if (cudaOccupancyMaxActiveClusters(&c, latent_attn_kernel<FP8>, &cfg) != cudaSuccess || c < 1)
+    if (cudaOccupancyMaxActiveClusters(&c, latent_attn_kernel<FP8, SHARED>, &cfg) != cudaSuccess || c < 1)
       return 0;
     known[dev] = c < kMaxClusters ? c : kMaxClusters;
   }
@@ -1297,8 +1505,9 @@ int resident_clusters(size_t smem) {
 
 template <bool FP8>
 int launch(Params p, cudaStream_t stream) {
+  constexpr bool SHARED = false;
   const size_t smem = Layout<FP8>::kTailOff + sizeof(Tail);
-  p.clusters = resident_clusters<FP8>(smem);
+  p.clusters = resident_clusters<FP8, SHARED>(smem);
   if (p.clusters < 1) return DSA_ERR_CUDA;
   // no more clusters than the longest possible sequences have work for
   const long long cap = static_cast<long long>(p.a.max_pages) * p.a.page_size;
@@ -1307,7 +1516,7 @@ int launch(Params p, cudaStream_t stream) {
   if (wanted < p.clusters) p.clusters = static_cast<int>(wanted);
   p.ml = reinterpret_cast<float2*>(p.part + 2ll * p.clusters * (kDc / 4) * p.prow);
   p.joins = reinterpret_cast<int2*>(p.ml + 2ll * p.clusters * p.prow);
-  latent_attn_kernel<FP8><<<2 * p.clusters, kThreads, smem, stream>>>(p);
+  latent_attn_kernel<FP8, SHARED><<<2 * p.clusters, kThreads, smem, stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
   if (p.clusters == 1) return DSA_OK;   // nothing is split
   // its blocks may be set up while the last clusters finish; they wait for the parts
@@ -1324,6 +1533,46 @@ int launch(Params p, cudaStream_t stream) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, share ? latent_join_kernel<true> : latent_join_kernel<false>,
+                            p) == cudaSuccess
+             ? DSA_OK
+             : DSA_ERR_CUDA;
+}
+
+// tiles of the groups' rows that there can be: each group's rows are rounded up
+long long most_prefix_tiles(int B, int Sq, int H, int G) {
+  return static_cast<long long>(B) * Sq * H / 128 + (G < B ? G : B);
+}
+
+template <bool FP8>
+int launch_shared(Params p, cudaStream_t stream) {
+  const size_t smem = Layout<FP8>::kTailOff + sizeof(Tail);
+  p.clusters = resident_clusters<FP8, true>(smem);
+  if (p.clusters < 1) return DSA_ERR_CUDA;
+  // no more clusters than the longest possible sequences and prefixes have work for
+  const long long own = (static_cast<long long>(p.a.max_pages) * p.a.page_size + kNK - 1) / kNK;
+  const long long pre = (static_cast<long long>(p.a.max_prefix) * p.a.page_size + kNK - 1) / kNK;
+  const long long wanted =
+      (p.items * own + (p.most_items - p.items) * pre + kMinChunks - 1) / kMinChunks;
+  if (wanted < p.clusters) p.clusters = static_cast<int>(wanted);
+  const long long parts = static_cast<long long>(p.most_items) + kMaxClusters;
+  p.ml = reinterpret_cast<float2*>(p.part + parts * (kDc / 4) * p.prow);
+  p.spans = reinterpret_cast<int2*>(p.ml + parts * p.prow);
+  p.groups = reinterpret_cast<int*>(p.spans + p.most_items);
+  latent_attn_kernel<FP8, true><<<2 * p.clusters, kThreads, smem, stream>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
+  // its blocks may be set up while the last clusters finish; they wait for the parts
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  const int rows = part_rows(p.a.Sq, p.a.H, 0);   // of the largest own tile
+  const bool share = static_cast<long long>(p.items) * rows <= 152 * 6;
+  cfg.gridDim = dim3(p.items, rows / 32, kDc / (4 * kJoinD4) / (share ? 1 : kJoinWarps));
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, share ? shared_join_kernel<true> : shared_join_kernel<false>,
                             p) == cudaSuccess
              ? DSA_OK
              : DSA_ERR_CUDA;
@@ -1354,6 +1603,34 @@ int launch_latent_attn(const LatentArgs& a, int fmt, cudaStream_t stream) {
     if (a.page_size == 1 << i) p.page_shift = i;
   p.part = static_cast<float4*>(a.ws);
   return fmt == DSA_CACHE_E4M3 ? launch<true>(p, stream) : launch<false>(p, stream);
+}
+
+size_t latent_attn_shared_workspace(int B, int Sq, int H, int G) {
+  const long long rows = static_cast<long long>(B) * Sq * H;
+  const long long tiles = (static_cast<long long>(Sq) * H + 127) / 128;
+  const size_t items = static_cast<size_t>(most_prefix_tiles(B, Sq, H, G) + B * tiles);
+  const size_t prow = rows < 128 ? (rows + 31) / 32 * 32 : 128;
+  return (items + kMaxClusters) * prow * (kDc * sizeof(float) + sizeof(float2)) +
+         items * sizeof(int2) + 2 * (kMaxGroups + 1) * sizeof(int);
+}
+
+int launch_latent_attn_shared(const LatentArgs& a, int fmt, cudaStream_t stream) {
+  Params p = {};
+  p.a = a;
+  p.tiles = static_cast<int>((static_cast<long long>(a.Sq) * a.H + 127) / 128);
+  const long long items = static_cast<long long>(a.B) * p.tiles;
+  const long long most = items + most_prefix_tiles(a.B, a.Sq, a.H, a.G);
+  p.items = static_cast<int>(items);   // at most B * Sq * H
+  p.most_items = static_cast<int>(most);
+  const long long rows = static_cast<long long>(a.B) * a.Sq * a.H;
+  p.prow = rows < 128 ? static_cast<int>((rows + 31) / 32 * 32) : 128;
+  p.act_warps = p.prow / 32;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (a.page_size == 1 << i) p.page_shift = i;
+  p.part = static_cast<float4*>(a.ws);
+  return fmt == DSA_CACHE_E4M3 ? launch_shared<true>(p, stream) : launch_shared<false>(p, stream);
 }
 
 }  // namespace dsa
