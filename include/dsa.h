@@ -628,6 +628,36 @@ int dsa_latent_attn_shared(const void* Q, const void* cache, int fmt, int64_t nu
  */
 
 /*
+ * dsa_cache_mass - the attention weight that each cached position receives from the Sq newest tokens
+ * of its sequence, summed over tokens and heads and added to that of earlier steps. With len = lens[b]
+ * as for dsa_latent_attn (or the sequences' own positions, for dsa_latent_attn_shared) and lse the one
+ * that the attention gave for the same Q:
+ *
+ *     mass[b,j] = decay * prev[b,j] + sum_{i,h} exp(scale * Q[b,i,h] . row_j - lse[b,i,h]),   j < len
+ *
+ * over the tokens i that see j (j <= len - Sq + i), or, with lists idx[b,i,:] as dsa_latent_attn takes
+ * them, over those whose list names it. mass[b,j] = 0 for j >= len. prev NULL: no earlier weight.
+ *
+ *   Q, cache, page_table, lens, idx, k as for dsa_latent_attn     lse  fp32 [B, Sq, H]
+ *   prev  fp32 [B, n] or NULL     mass fp32 [B, n] out; may be prev itself, any other overlap is refused
+ *   ws    workspace of dsa_cache_mass_workspace_size() bytes (0 without lists), overwritten
+ *
+ * A token whose lse is -inf adds nothing (it has no key); a NaN in lse, in Q or in a row reaches the
+ * positions that it bears on. A logit counts as an infinity where it is past fp32. Lengths, list entries
+ * and pages outside their range are treated as by dsa_latent_attn and recorded with DSA_STAGE_EVICT;
+ * positions n and behind are left out, and a length above n is recorded as DSA_DEVERR_BAD_PAGE. The
+ * arithmetic is fp32 (products of bf16 exact, sums in a fixed order: the same bits every time).
+ *
+ * Supported: as for dsa_latent_attn, with a finite decay, n <= 2^30 and B * Sq * k < 2^31.
+ */
+size_t dsa_cache_mass_workspace_size(int B, int Sq, int H, int Dc, int Dr, int k);
+int dsa_cache_mass(const void* Q, const void* cache, int fmt, int64_t num_pages, int page_size,
+                   const int32_t* page_table, int max_pages, const int32_t* lens,
+                   const int32_t* idx, int k, const float* lse, int B, int Sq, int H, int Dc, int Dr,
+                   float scale, const float* prev, float decay, float* mass, int n, void* ws,
+                   size_t ws_bytes, void* stream);
+
+/*
  * dsa_cache_keep - the positions of each sequence that stay when it is cut to `budget`: its first
  * `sink` ones, its `recent` newest ones, and of the others the budget - sink - recent heaviest by
  * mass (ties go to the lower position, -0 counts as +0, a NaN as heavier than any number). A

@@ -18,6 +18,7 @@ Entry points (same names as the C ABI):
 * ``dsa_cache_write`` / ``dsa_cache_read`` - rows of the paged latent cache (bf16 or e4m3)
 * ``dsa_latent_attn`` - attention of the newest tokens over that cache -> (O, lse)
 * ``dsa_latent_attn_shared`` - the same for sequences that share long prefixes, stored once
+* ``dsa_cache_mass`` - the attention weight that each cached position receives
 * ``dsa_cache_keep`` / ``dsa_cache_compact`` - the positions that stay in the cache by their attention
   weight, and their rows moved
 * ``dsa_decode_layer`` - these together, one serving step
@@ -57,8 +58,8 @@ EXPORTS = ("dsa_status_string", "dsa_version", "dsa_get_last_device_error", "dsa
            "dsa_index_topk_stream_workspace_size", "dsa_index_topk_stream",
            "dsa_index_topk_stream_fp8", "dsa_rope", "dsa_cache_row_bytes", "dsa_cache_write",
            "dsa_cache_read", "dsa_latent_attn_workspace_size", "dsa_latent_attn",
-           "dsa_latent_attn_shared_workspace_size", "dsa_latent_attn_shared", "dsa_cache_keep",
-           "dsa_cache_compact")
+           "dsa_latent_attn_shared_workspace_size", "dsa_latent_attn_shared",
+           "dsa_cache_mass_workspace_size", "dsa_cache_mass", "dsa_cache_keep", "dsa_cache_compact")
 
 
 class DsaError(RuntimeError):
@@ -125,11 +126,15 @@ def _load() -> ctypes.CDLL:
     lib.dsa_latent_attn_shared_workspace_size.restype = sz
     lib.dsa_latent_attn_shared.argtypes = [vp, vp, ci, i64, ci, vp, ci, vp, vp, ci, vp, ci, vp, ci, ci,
                                            ci, ci, ci, cf, vp, vp, vp, sz, vp]
+    lib.dsa_cache_mass_workspace_size.argtypes = [ci, ci, ci, ci, ci, ci]
+    lib.dsa_cache_mass_workspace_size.restype = sz
+    lib.dsa_cache_mass.argtypes = [vp, vp, ci, i64, ci, vp, ci, vp, vp, ci, vp, ci, ci, ci, ci, ci, cf,
+                                   vp, cf, vp, ci, vp, sz, vp]
     lib.dsa_cache_keep.argtypes = [vp, ci, vp, ci, ci, ci, ci, vp, vp, vp]
     lib.dsa_cache_compact.argtypes = [vp, ci, i64, ci, vp, ci, vp, vp, ci, vp, ci, ci, ci, ci, vp, ci,
                                       vp, ci, vp]
     for name in ("dsa_rope", "dsa_cache_write", "dsa_cache_read", "dsa_latent_attn",
-                 "dsa_latent_attn_shared", "dsa_cache_keep", "dsa_cache_compact",
+                 "dsa_latent_attn_shared", "dsa_cache_mass", "dsa_cache_keep", "dsa_cache_compact",
                  "dsa_get_last_device_error", "dsa_index_scores", "dsa_index_scores_fp8", "dsa_topk",
                  "dsa_indexer_loss", "dsa_indexer_loss_bwd", "dsa_index_topk",
                  "dsa_index_topk_fp8", "dsa_index_topk_stream", "dsa_index_topk_stream_fp8",
@@ -1066,6 +1071,63 @@ def dsa_decode_layer(Q, kv, pos, inv_freq, slots, cache, page_table, lens, scale
     dsa_cache_write(rows.view(B * Sq, D), slots.view(B * Sq), cache, Dc, fmt=fmt, stream=stream)
     _call(lib.dsa_latent_attn, "dsa_latent_attn", q.device, stream, *args)
     return O, lse
+
+
+@functools.lru_cache(maxsize=1024)
+def cache_mass_workspace_bytes(B, Sq, H, Dc, Dr, k=0) -> int:
+    return int(lib.dsa_cache_mass_workspace_size(B, Sq, H, Dc, Dr, k))
+
+
+def dsa_cache_mass(Q, cache, page_table, lens, lse, scale: float, n: int, fmt: str = "e4m3", idx=None,
+                   prev=None, decay: float = 1.0, Dc: int = 512, mass=None, ws=None, stream=None):
+    """The attention weight that each cached position receives from the Sq newest tokens of its
+    sequence, summed over tokens and heads, on top of decay * prev -> mass fp32 [B, n].
+
+    Q, cache, page_table, lens, scale, fmt, idx as for dsa_latent_attn, and lse fp32 [B,Sq,H] from it
+    (or from dsa_latent_attn_shared; page_table and lens are then the sequences' own). n: positions
+    that mass has room for. prev fp32 [B, n] or None; mass=prev adds in place. Positions at or behind a
+    sequence's length get zero.
+
+    ws (lists only): a device byte buffer of at least cache_mass_workspace_bytes(...) (allocated here if
+    None). What is allocated here is allocated on `stream`.
+    """
+    qp = _dev(Q, "Q", torch.bfloat16)
+    if Q.dim() != 4 or Q.shape[3] < Dc:
+        raise ValueError("Q must be [B, Sq, H, Dc + Dr]")
+    B, Sq, H, D = Q.shape
+    Dr, dev = D - Dc, Q.device
+    cp, _ = _cache_arg(cache, Dc, Dr, fmt, dev)
+    if cache.dim() != 3:
+        raise ValueError("cache must be [num_pages, page_size, row_bytes]")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    k = 0
+    ip = None
+    if idx is not None:
+        k = idx.shape[-1]
+        if k < 1:   # NULL would mean every cached key
+            raise ValueError("idx must list at least one slot per token (-1 for none)")
+        ip = _arg(idx, "idx", torch.int32, (B, Sq, k), dev)
+    _int32(B, Sq, H, k, n, cache.shape[1], page_table.shape[1])
+    if n < 1:
+        raise ValueError("n must be at least 1")
+    tp = _arg(page_table, "page_table", torch.int32, (B, page_table.shape[1]), dev)
+    lp = _arg(lens, "lens", torch.int32, (B,), dev)
+    ep = _arg(lse, "lse", torch.float32, (B, Sq, H), dev)
+    pp = None if prev is None else _arg(prev, "prev", torch.float32, (B, n), dev)
+    if mass is None:
+        mass = _empty((B, n), torch.float32, dev, stream)
+    mp = _arg(mass, "mass", torch.float32, (B, n), dev)
+    need = cache_mass_workspace_bytes(B, Sq, H, Dc, Dr, k) if k else 0
+    if ws is None and need > 0:
+        ws = _empty((need,), torch.uint8, dev, stream)
+    if ws is not None and ws.device != dev:
+        raise ValueError(f"ws is on {ws.device}, the other arguments on {dev}")
+    _call(lib.dsa_cache_mass, "dsa_cache_mass", dev, stream, qp, cp, _CACHE_FORMATS[fmt],
+          cache.shape[0], cache.shape[1], tp, page_table.shape[1], lp, ip, k, ep, B, Sq, H, Dc, Dr,
+          float(scale), pp, float(decay), mp, n, None if ws is None else _dev(ws, "ws"),
+          0 if ws is None else ws.numel() * ws.element_size())
+    return mass
 
 
 def dsa_cache_keep(mass, lens, budget: int, sink: int = 0, recent: int = 0, keep=None, count=None,

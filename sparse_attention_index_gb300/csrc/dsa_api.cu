@@ -2,6 +2,7 @@
 // See include/dsa.h for the contract of every entry point.
 
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include <mutex>
@@ -648,6 +649,67 @@ int dsa_latent_attn_shared(const void* Q, const void* cache, int fmt, int64_t nu
   a.G = G;
   a.max_prefix = max_prefix_pages;
   return dsa::launch_latent_attn_shared(a, fmt, as_stream(stream));
+}
+
+size_t dsa_cache_mass_workspace_size(int B, int Sq, int H, int Dc, int Dr, int k) {
+  if (B < 1 || Sq < 1 || H < 1 || H > 128 || Dc != 512 || Dr != 64 || k < 1 ||
+      static_cast<long long>(B) * Sq >= (1LL << 31) / k)
+    return 0;
+  return dsa::cache_mass_workspace(B, Sq, k);
+}
+
+int dsa_cache_mass(const void* Q, const void* cache, int fmt, int64_t num_pages, int page_size,
+                   const int32_t* page_table, int max_pages, const int32_t* lens,
+                   const int32_t* idx, int k, const float* lse, int B, int Sq, int H, int Dc, int Dr,
+                   float scale, const float* prev, float decay, float* mass, int n, void* ws,
+                   size_t ws_bytes, void* stream) {
+  if (!Q || !cache || !page_table || !lens || !lse || !mass) return DSA_ERR_INVALID_ARG;
+  if (B < 1 || Sq < 1 || H < 1 || Dc < 1 || Dr < 0 || num_pages < 1 || page_size < 1 ||
+      max_pages < 1 || n < 1)
+    return DSA_ERR_INVALID_ARG;
+  if (k < 0 || (k > 0) != (idx != nullptr)) return DSA_ERR_INVALID_ARG;
+  if (fmt != DSA_CACHE_BF16 && fmt != DSA_CACHE_E4M3) return DSA_ERR_INVALID_ARG;
+  const void* ptrs[] = {Q, cache, page_table, lens, idx, lse, prev, mass};
+  for (const void* ptr : ptrs)
+    if (!aligned16(ptr)) return DSA_ERR_INVALID_ARG;
+  if (prev && prev != mass) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(prev), y = reinterpret_cast<uintptr_t>(mass);
+    if ((x < y ? y - x : x - y) < static_cast<uintptr_t>(B) * n * 4) return DSA_ERR_INVALID_ARG;
+  }
+  if (Dc != 512 || Dr != 64 || H > 128) return DSA_ERR_UNSUPPORTED;
+  if (!(scale > 0.f) || scale > 2.0e38f || !isfinite(decay)) return DSA_ERR_UNSUPPORTED;
+  const long long most = 1LL << 31;   // positions, slots and query rows are counted in 32 bits
+  if (num_pages >= most || num_pages * page_size >= most ||
+      static_cast<long long>(max_pages) * page_size >= most ||
+      static_cast<long long>(B) * Sq >= most / H || n > (1 << 30))
+    return DSA_ERR_UNSUPPORTED;
+  if (k > 0) {
+    const size_t need = dsa_cache_mass_workspace_size(B, Sq, H, Dc, Dr, k);
+    if (need == 0) return DSA_ERR_UNSUPPORTED;
+    if (!ws || ws_bytes < need || !aligned16(ws)) return DSA_ERR_WORKSPACE;
+  }
+  dsa::MassArgs a = {};
+  a.Q = static_cast<const uint16_t*>(Q);
+  a.cache = static_cast<const uint8_t*>(cache);
+  a.page_table = page_table;
+  a.lens = lens;
+  a.idx = idx;
+  a.lse = lse;
+  a.prev = prev;
+  a.num_pages = num_pages;
+  a.page_size = page_size;
+  a.max_pages = max_pages;
+  a.k = k;
+  a.B = B;
+  a.Sq = Sq;
+  a.H = H;
+  a.n = n;
+  a.scale = scale;
+  a.decay = decay;
+  a.mass = mass;
+  a.ws = ws;
+  a.err = dsa::device_error_word();
+  return dsa::launch_cache_mass(a, fmt, as_stream(stream));
 }
 
 int dsa_cache_keep(const float* mass, int n, const int32_t* lens, int B, int budget, int sink,

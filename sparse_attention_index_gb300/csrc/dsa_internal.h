@@ -183,6 +183,22 @@ constexpr int kLatentGroups = 64;   // groups that dsa_latent_attn_shared takes
 size_t latent_attn_shared_workspace(int B, int Sq, int H, int G);
 int launch_latent_attn_shared(const LatentArgs& a, int fmt, cudaStream_t stream);
 
+// the weight that cached positions receive (mass.cu)
+struct MassArgs {
+  const uint16_t* Q;
+  const uint8_t* cache;
+  const int32_t *page_table, *lens, *idx;
+  const float *lse, *prev;
+  long long num_pages;
+  int page_size, max_pages, k, B, Sq, H, n;
+  float scale, decay;
+  float* mass;
+  void* ws;
+  int* err;
+};
+size_t cache_mass_workspace(int B, int Sq, int k);
+int launch_cache_mass(const MassArgs& a, int fmt, cudaStream_t stream);
+
 // eviction (evict.cu): which positions stay, and their rows moved
 int launch_cache_keep(const float* mass, int n, const int32_t* lens, int B, int budget, int sink,
                       int recent, int32_t* keep, int32_t* count, cudaStream_t stream);

@@ -2,10 +2,21 @@
 
 Which positions stay and where their rows go are whole numbers and copied bytes: they are equal to the
 definition's, with no tolerance.
+
+Weights: el bounds the error of a logit l (576 exact products added in fp32, each addition off by at most
+2^-23 of the sum of magnitudes). exp(l - lse) takes that error, those of the subtraction and of the change
+of base (2^-24 |l - lse| each, 2^-22 with the second's own constant) and the exponential's (2^-22, and
+2^-22 for the others' product). A sum of c such weights, all positive, in fp32, with decay * prev in front
+of it, is off by at most (c + 3) 2^-24 of the whole (c + 3 roundings, each of at most half a step of a
+partial sum).
 """
+import math
+
 import numpy as np
 import pytest
 import torch
+
+from test_gpu_serving import D, gen, i32, make_cache, no_error
 
 pytestmark = pytest.mark.gpu
 
@@ -17,20 +28,6 @@ def dsa():
     import sparse_attention_index_gb300 as m
     m.dsa_get_last_device_error()
     return m
-
-
-def no_error(dsa):
-    assert dsa.dsa_get_last_device_error() == 0
-
-
-def gen(seed):
-    g = torch.Generator(device="cuda")
-    g.manual_seed(seed)
-    return g
-
-
-def i32(x):
-    return torch.tensor(x, dtype=torch.int32, device="cuda")
 
 
 # -------------------------------------------------------------------------------- what stays
@@ -246,4 +243,278 @@ def test_python_refusals(dsa):
     with pytest.raises(ValueError):
         dsa.dsa_cache_compact(cache, table, lens, i32([0, 1]), new_table, DC, DR)
     assert torch.equal(cache, before)
+    no_error(dsa)
+
+
+# ------------------------------------------------------------------------------- the weights
+
+
+def mass_inputs(dsa, lens, Sq, H, page, fmt, seed, k=0):
+    """A cache, queries, lists and the attention's lse (the definition's, rounded to fp32)."""
+    cache, table, rows = make_cache(dsa, lens, page, fmt, seed)
+    g, B = gen(seed + 1), len(lens)
+    Q = torch.randn(B, Sq, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    scale = 192 ** -0.5
+    idx = None
+    if k:
+        idx = torch.full((B, Sq, k), -1, dtype=torch.int32, device="cuda")
+        for b, n in enumerate(lens):
+            for i in range(Sq):
+                at = torch.randperm(max(n, 1), generator=g, device="cuda")[:min(k, max(n, 0))].sort().values
+                idx[b, i, :len(at)] = at.to(torch.int32)          # entries behind the token among them
+    lse = torch.full((B, Sq, H), -math.inf, device="cuda")
+    for b in range(B):
+        for i in range(Sq):
+            at = seen(lens[b], Sq, i, None if idx is None else idx[b, i])
+            if len(at):
+                l = scale * (Q[b, i].double() @ rows[b][at].T)
+                lse[b, i] = torch.logsumexp(l, -1).float()
+    return Q, cache, table, i32(lens), lse, scale, idx, rows
+
+
+def seen(n, Sq, i, listed):
+    """The positions that token i of a sequence of n sees."""
+    limit = max(n, 0) - Sq + i + 1
+    if listed is None:
+        return torch.arange(max(limit, 0), device="cuda")
+    t = listed.long()
+    return t[(t >= 0) & (t < limit)]
+
+
+def mass_check(got, Q, rows, lens, lse, scale, idx=None, prev=None, decay=1.0):
+    B, Sq, H, _ = Q.shape
+    n = got.shape[1]
+    for b in range(B):
+        m = min(max(int(lens[b]), 0), n)
+        ref = torch.zeros(n, dtype=torch.float64, device="cuda")
+        tol = torch.zeros_like(ref)
+        if prev is not None:
+            ref[:m] = decay * prev[b, :m].double()
+        base = ref.clone()
+        for i in range(Sq):
+            at = seen(int(lens[b]), Sq, i, None if idx is None else idx[b, i])
+            at = at[at < n]
+            if len(at) == 0:
+                continue
+            q, kv = Q[b, i].double(), rows[b][at]
+            x = scale * (q @ kv.T) - lse[b, i].double()[:, None]
+            x[lse[b, i] == -math.inf] = -math.inf
+            w = torch.exp(x)
+            el = D * 2.0 ** -23 * scale * (q.abs() @ kv.abs().T)
+            r = torch.where(w > 0, torch.expm1(el + x.abs() * 2.0 ** -22 + 2.0 ** -21), torch.zeros_like(w))
+            ref.index_add_(0, at, w.sum(0))
+            tol.index_add_(0, at, (w * r).sum(0))
+        tol += (Sq * H + 3) * 2.0 ** -24 * (ref - base + base.abs())
+        err = (got[b].double() - ref).abs()
+        assert bool((err <= tol).all()), (b, float((err - tol).max()), int((err - tol).argmax()))
+        assert not got[b, m:].any()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,Sq,H,page", [
+    ([1], 1, 1, 16), ([489], 1, 16, 64), ([127, 128, 129], 1, 128, 7), ([0, 1, 97, 0], 1, 20, 16),
+    ([3, 130], 4, 16, 16), ([2, 700], 3, 128, 100), ([7], 7, 5, 64), ([96, 1000, 1, 31, 2049], 2, 64, 32),
+    ([20000], 1, 128, 64), ([300, 40], 33, 128, 16), ([1500], 32, 128, 64), ([200], 70, 3, 16),
+    ([4000, 257], 9, 57, 1)])
+def test_mass(dsa, fmt, lens, Sq, H, page):
+    Q, cache, table, ln, lse, scale, _, rows = mass_inputs(dsa, lens, Sq, H, page, fmt, 11)
+    n = max(lens) + 5
+    prev = torch.rand(len(lens), n, generator=gen(12), device="cuda")
+    got = dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, n, fmt=fmt)
+    mass_check(got, Q, rows, lens, lse, scale)
+    both = dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, n, fmt=fmt, prev=prev, decay=0.875)
+    mass_check(both, Q, rows, lens, lse, scale, None, prev, 0.875)
+    again = prev.clone()
+    assert dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, n, fmt=fmt, prev=again, decay=0.875, mass=again) is again
+    assert torch.equal(again, both)                                       # the same bits
+    no_error(dsa)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,Sq,H,page,k", [
+    ([1], 1, 1, 16, 1), ([489], 1, 16, 64, 100), ([50, 0, 3], 2, 20, 16, 64), ([700, 2000], 3, 128, 100, 500),
+    ([5000, 4097, 9000], 1, 128, 64, 2048), ([300], 9, 8, 16, 129), ([20000, 1], 2, 33, 16, 300)])
+def test_mass_of_lists(dsa, fmt, lens, Sq, H, page, k):
+    Q, cache, table, ln, lse, scale, idx, rows = mass_inputs(dsa, lens, Sq, H, page, fmt, 21, k)
+    n = max(lens) + 1
+    prev = torch.rand(len(lens), n, generator=gen(22), device="cuda")
+    got = dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, n, fmt=fmt, idx=idx)
+    mass_check(got, Q, rows, lens, lse, scale, idx)
+    got = dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, n, fmt=fmt, idx=idx, prev=prev, decay=-0.5, mass=prev.clone())
+    mass_check(got, Q, rows, lens, lse, scale, idx, prev, -0.5)
+    twice = dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, n, fmt=fmt, idx=idx, prev=prev, decay=-0.5)
+    assert torch.equal(got, twice)
+    no_error(dsa)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Sq,H", [(1, 128), (1, 16), (4, 100)])
+def test_mass_many_ragged(dsa, fmt, Sq, H):
+    lens = [5000 - 371 * b if b % 6 else (0, 1, 20011, 128)[b // 6 % 4] for b in range(13)] * 3
+    lens = [max(n, 0) for n in lens]
+    Q, cache, table, ln, lse, scale, _, rows = mass_inputs(dsa, lens, Sq, H, 64, fmt, 31)
+    got = dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, max(lens), fmt=fmt)
+    mass_check(got, Q, rows, lens, lse, scale)
+    no_error(dsa)
+
+
+def test_mass_of_attention_sums_to_the_tokens(dsa):
+    """With the lse that the attention gives, the weights of a token and head sum to one."""
+    lens, Sq, H = [700, 33, 2, 1500], 2, 48
+    Q, cache, table, ln, _, scale, idx, _ = mass_inputs(dsa, lens, Sq, H, 16, "e4m3", 41, 200)
+    for lists in (None, idx):
+        lse = dsa.dsa_latent_attn(Q, cache, table, ln, scale, idx=lists)[1]
+        got = dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, max(lens), idx=lists)
+        # each weight within 2^-12 (the bounds of both logits and of lse), tokens without a key add none
+        tokens = torch.tensor([[float(bool((lse[b, i] > -math.inf).all())) for i in range(Sq)] for b in range(4)])
+        assert (got.double().sum(-1).cpu() - H * tokens.sum(-1)).abs().max() <= 2.0 ** -12 * H * Sq
+    no_error(dsa)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H", [16, 128])
+def test_mass_values_that_are_not_finite(dsa, fmt, H):
+    """A NaN row is NaN in its own place alone; a token's lse of NaN in all that it sees, of -inf in none;
+    an infinite row has the weight of its logit: 0 or what exp gives."""
+    lens, Sq = [200, 150], 2
+    Q, cache, table, ln, lse, scale, _, rows = mass_inputs(dsa, lens, Sq, H, 16, fmt, 51)
+    clean = dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, 200, fmt=fmt)
+    for b, j in ((0, 40), (0, 199), (1, 149)):        # 199: seen by the last token alone
+        slot = int(table[b, j // 16]) * 16 + j % 16
+        dsa.dsa_cache_write(torch.full((1, D), math.nan, dtype=torch.bfloat16, device="cuda"), i32([slot]),
+                            cache, DC, fmt=fmt)
+    got = dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, 200, fmt=fmt)
+    hit = torch.zeros_like(got, dtype=torch.bool)
+    hit[0, 40] = hit[0, 199] = hit[1, 149] = True
+    assert torch.equal(torch.isnan(got), hit) and torch.equal(got[~hit], clean[~hit])
+    # the rows again, and the first token's lse
+    bad = lse.clone()
+    bad[1, 0, H // 2] = math.nan
+    bad[0, 0] = -math.inf
+    cache2, table2, rows2 = make_cache(dsa, lens, 16, fmt, 51)
+    got = dsa.dsa_cache_mass(Q, cache2, table2, ln, bad, scale, 200, fmt=fmt)
+    hit = torch.zeros_like(got, dtype=torch.bool)
+    hit[1, :149] = True
+    assert torch.equal(torch.isnan(got), hit)
+    mass_check(got[:1], Q[:1], rows2[:1], lens[:1], bad[:1], scale)
+    # positional dims of plus and minus infinity: logits of infinite size
+    row = torch.zeros(1, D, dtype=torch.bfloat16, device="cuda")
+    row[0, DC] = math.inf
+    slot = int(table2[0, 0]) * 16
+    dsa.dsa_cache_write(row, i32([slot]), cache2, DC, fmt=fmt)
+    Q[0, :, :, DC] = -Q[0, :, :, DC].abs() - 1
+    got = dsa.dsa_cache_mass(Q, cache2, table2, ln, lse, scale, 200, fmt=fmt)
+    assert float(got[0, 0]) == 0.0
+    Q[0, :, 0, DC] = 1.0
+    got = dsa.dsa_cache_mass(Q, cache2, table2, ln, lse, scale, 200, fmt=fmt)
+    assert float(got[0, 0]) == math.inf
+    no_error(dsa)
+
+
+def test_mass_bad_entries_pages_and_lengths(dsa):
+    lens, Sq, H = [100, 90], 1, 16
+    Q, cache, table, ln, lse, scale, idx, rows = mass_inputs(dsa, lens, Sq, H, 16, "e4m3", 61, 20)
+    idx[0, 0, 3], idx[1, 0, 0] = 100, -2
+    got = dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, 100, idx=idx)
+    assert dsa.dsa_get_last_device_error() == dsa.DSA_STAGE_EVICT | dsa.DSA_DEVERR_BAD_INDEX
+    mass_check(got, Q, rows, lens, lse, scale, idx)
+    # a page that is none: its keys are not there
+    broken = table.clone()
+    broken[0, 2] = cache.shape[0]
+    whole = dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, 100)
+    no_error(dsa)
+    got = dsa.dsa_cache_mass(Q, cache, broken, ln, lse, scale, 100)
+    assert dsa.dsa_get_last_device_error() == dsa.DSA_STAGE_EVICT | dsa.DSA_DEVERR_BAD_PAGE
+    want = whole.clone()
+    want[0, 32:48] = 0
+    assert torch.equal(got, want)
+    # room for fewer positions than there are
+    got = dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, 37)
+    assert dsa.dsa_get_last_device_error() == dsa.DSA_STAGE_EVICT | dsa.DSA_DEVERR_BAD_PAGE
+    assert torch.equal(got, whole[:, :37])
+    got = dsa.dsa_cache_mass(Q, cache, table, i32([-3, 90]), lse, scale, 100)
+    assert dsa.dsa_get_last_device_error() == dsa.DSA_STAGE_EVICT | dsa.DSA_DEVERR_BAD_PAGE
+    assert not got[0].any() and torch.equal(got[1], whole[1])
+
+
+def test_mass_of_an_entry_twice(dsa):
+    """An entry listed twice counts twice, the same bits every time."""
+    Q, cache, table, ln, lse, scale, idx, rows = mass_inputs(dsa, [300], 2, 16, 16, "bf16", 71, 40)
+    idx[0, 0, 5] = idx[0, 0, 4]
+    got = dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, 300, fmt="bf16", idx=idx)
+    mass_check(got, Q, rows, [300], lse, scale, idx)
+    for _ in range(3):
+        assert torch.equal(got, dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, 300, fmt="bf16", idx=idx))
+    no_error(dsa)
+
+
+# ---------------------------------------------------------------------------------- together
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("place", ["new", "same"])
+def test_steps_with_eviction(dsa, fmt, place):
+    """Attention, its weights, the positions that stay, their rows moved; then the next step's attention
+    over what is left is that over the kept rows."""
+    lens, Sq, H, page, budget = [300, 40, 777, 128], 1, 32, 16, 100
+    Q, cache, table, ln, _, scale, _, rows = mass_inputs(dsa, lens, Sq, H, page, fmt, 81)
+    n = 800
+    mass = torch.zeros(4, n, device="cuda")
+    for _ in range(2):
+        O, lse = dsa.dsa_latent_attn(Q, cache, table, ln, scale, fmt=fmt)
+        dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, n, fmt=fmt, prev=mass, decay=0.5, mass=mass)
+    keep, count = dsa.dsa_cache_keep(mass, ln, budget, sink=2, recent=10)
+    want, _ = keep_ref(mass.cpu().numpy(), lens, budget, 2, 10)
+    assert np.array_equal(keep.cpu().numpy(), want)
+    new_table = table
+    if place == "new":
+        spare = torch.zeros(4 * 7, page, cache.shape[-1], dtype=torch.uint8, device="cuda")
+        new_table = (cache.shape[0] + torch.randperm(28, device="cuda").to(torch.int32)).view(4, 7).contiguous()
+        cache = torch.cat([cache, spare])
+    dsa.dsa_cache_compact(cache, table, ln, keep, new_table if place == "new" else None, DC, DR, fmt=fmt, mass=mass,
+                          new_mass=mass)
+    from test_gpu_serving import attn_check
+    O, lse = dsa.dsa_latent_attn(Q, cache, new_table, count, scale, fmt=fmt)
+    kept = [rows[b][keep[b][keep[b] >= 0].long()] for b in range(4)]
+    attn_check(O, lse, Q, kept, [len(r) for r in kept], scale)
+    got = dsa.dsa_cache_mass(Q, cache, new_table, count, lse, scale, n, fmt=fmt, prev=mass)
+    mass_check(got, Q, kept, [len(r) for r in kept], lse, scale, None, mass)
+    no_error(dsa)
+
+
+def test_captured_step(dsa):
+    """A whole step captured into a graph and replayed with other lengths."""
+    lens, H, page, budget = [300, 200, 60], 16, 16, 64
+    Q, cache, table, ln, _, scale, _, _ = mass_inputs(dsa, lens, 1, H, page, "e4m3", 91)
+    start = cache.clone()
+
+    def step():
+        O, lse = dsa.dsa_latent_attn(Q, cache, table, ln, scale)
+        mass = dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, 300)
+        keep, count = dsa.dsa_cache_keep(mass, ln, budget, recent=4)
+        new_mass = dsa.dsa_cache_compact(cache, table, ln, keep, None, DC, DR, mass=mass)
+        return O, lse, mass, keep, count, new_mass
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for other in (lens, [100, 64, 1]):
+        ln.copy_(i32(other))
+        cache.copy_(start)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in outs] + [cache.clone()]
+        cache.copy_(start)
+        for a, b in zip(got, list(step()) + [cache]):
+            assert torch.equal(a, b)
+    # on another stream than the current one
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    mass = dsa.dsa_cache_mass(Q, start, table, ln, got[1], scale, 300, stream=s)
+    keep, count = dsa.dsa_cache_keep(mass, ln, budget, recent=4, stream=s)
+    new_mass = dsa.dsa_cache_compact(start, table, ln, keep, None, DC, DR, mass=mass, stream=s)
+    s.synchronize()
+    for a, b in zip((mass, keep, count, new_mass, start), got[2:]):
+        assert torch.equal(a, b)
     no_error(dsa)
