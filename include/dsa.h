@@ -640,7 +640,8 @@ int dsa_latent_attn_shared(const void* Q, const void* cache, int fmt, int64_t nu
  *
  *   Q, cache, page_table, lens, idx, k as for dsa_latent_attn     lse  fp32 [B, Sq, H]
  *   prev  fp32 [B, n] or NULL     mass fp32 [B, n] out; may be prev itself, any other overlap is refused
- *   ws    workspace of dsa_cache_mass_workspace_size() bytes (0 without lists), overwritten
+ *   ws    workspace of dsa_cache_mass_workspace_size() bytes (0: none needed), overwritten: the lists'
+ *         weights, or the parts of sums that are split over the GPU
  *
  * A token whose lse is -inf adds nothing (it has no key); a NaN in lse, in Q or in a row reaches the
  * positions that it bears on. A logit counts as an infinity where it is past fp32. Lengths, list entries
@@ -648,7 +649,8 @@ int dsa_latent_attn_shared(const void* Q, const void* cache, int fmt, int64_t nu
  * positions n and behind are left out, and a length above n is recorded as DSA_DEVERR_BAD_PAGE. The
  * arithmetic is fp32 (products of bf16 exact, sums in a fixed order: the same bits every time).
  *
- * Supported: as for dsa_latent_attn, with a finite decay, n <= 2^30 and B * Sq * k < 2^31.
+ * Supported: as for dsa_latent_attn, with a finite decay, n <= 2^30 and, with lists, B * Sq * k and
+ * B * (n / 8192 + 1) below 2^31.
  */
 size_t dsa_cache_mass_workspace_size(int B, int Sq, int H, int Dc, int Dr, int k);
 int dsa_cache_mass(const void* Q, const void* cache, int fmt, int64_t num_pages, int page_size,

@@ -1088,7 +1088,7 @@ def dsa_cache_mass(Q, cache, page_table, lens, lse, scale: float, n: int, fmt: s
     that mass has room for. prev fp32 [B, n] or None; mass=prev adds in place. Positions at or behind a
     sequence's length get zero.
 
-    ws (lists only): a device byte buffer of at least cache_mass_workspace_bytes(...) (allocated here if
+    ws: a device byte buffer of at least cache_mass_workspace_bytes(...) (allocated here if
     None). What is allocated here is allocated on `stream`.
     """
     qp = _dev(Q, "Q", torch.bfloat16)
@@ -1118,7 +1118,7 @@ def dsa_cache_mass(Q, cache, page_table, lens, lse, scale: float, n: int, fmt: s
     if mass is None:
         mass = _empty((B, n), torch.float32, dev, stream)
     mp = _arg(mass, "mass", torch.float32, (B, n), dev)
-    need = cache_mass_workspace_bytes(B, Sq, H, Dc, Dr, k) if k else 0
+    need = cache_mass_workspace_bytes(B, Sq, H, Dc, Dr, k)
     if ws is None and need > 0:
         ws = _empty((need,), torch.uint8, dev, stream)
     if ws is not None and ws.device != dev:

@@ -652,10 +652,10 @@ int dsa_latent_attn_shared(const void* Q, const void* cache, int fmt, int64_t nu
 }
 
 size_t dsa_cache_mass_workspace_size(int B, int Sq, int H, int Dc, int Dr, int k) {
-  if (B < 1 || Sq < 1 || H < 1 || H > 128 || Dc != 512 || Dr != 64 || k < 1 ||
-      static_cast<long long>(B) * Sq >= (1LL << 31) / k)
+  if (B < 1 || Sq < 1 || H < 1 || H > 128 || Dc != 512 || Dr != 64 || k < 0 ||
+      (k > 0 && static_cast<long long>(B) * Sq >= (1LL << 31) / k))
     return 0;
-  return dsa::cache_mass_workspace(B, Sq, k);
+  return dsa::cache_mass_workspace(B, Sq, H, k);
 }
 
 int dsa_cache_mass(const void* Q, const void* cache, int fmt, int64_t num_pages, int page_size,
@@ -683,11 +683,12 @@ int dsa_cache_mass(const void* Q, const void* cache, int fmt, int64_t num_pages,
       static_cast<long long>(max_pages) * page_size >= most ||
       static_cast<long long>(B) * Sq >= most / H || n > (1 << 30))
     return DSA_ERR_UNSUPPORTED;
-  if (k > 0) {
-    const size_t need = dsa_cache_mass_workspace_size(B, Sq, H, Dc, Dr, k);
-    if (need == 0) return DSA_ERR_UNSUPPORTED;
-    if (!ws || ws_bytes < need || !aligned16(ws)) return DSA_ERR_WORKSPACE;
-  }
+  // blocks of the lists' sums and entries
+  if (k > 0 && (static_cast<long long>(B) * Sq >= most / k ||
+                static_cast<long long>(B) * (n / 8192 + 1) >= most))
+    return DSA_ERR_UNSUPPORTED;
+  const size_t need = dsa_cache_mass_workspace_size(B, Sq, H, Dc, Dr, k);
+  if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws))) return DSA_ERR_WORKSPACE;
   dsa::MassArgs a = {};
   a.Q = static_cast<const uint16_t*>(Q);
   a.cache = static_cast<const uint8_t*>(cache);

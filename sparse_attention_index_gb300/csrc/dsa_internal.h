@@ -196,7 +196,7 @@ struct MassArgs {
   void* ws;
   int* err;
 };
-size_t cache_mass_workspace(int B, int Sq, int k);
+size_t cache_mass_workspace(int B, int Sq, int H, int k);
 int launch_cache_mass(const MassArgs& a, int fmt, cudaStream_t stream);
 
 // eviction (evict.cu): which positions stay, and their rows moved

@@ -49,6 +49,7 @@
 
 #include "dsa_common.cuh"
 #include "dsa_internal.h"
+#include "latent_row.cuh"
 
 namespace dsa {
 namespace {
@@ -90,8 +91,6 @@ constexpr uint32_t kRawRope = kCodeReps * kGatherThreads * 16;
 constexpr uint32_t kRawScale = kRawRope + kGatherThreads * 16;
 constexpr uint32_t kRaw = kRawScale + kNK * 8;
 constexpr int kAhead = 2;
-// 2^7 as bf16: the largest scale that widens in one step
-constexpr uint32_t kScaleMost = 134u << 7;
 static_assert(kNK * (kHalfR / 8) == kGatherThreads, "one piece of positional dims per thread");
 
 template <bool FP8>
@@ -455,23 +454,10 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32
                : "memory");
 }
 
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a),
-                                   *reinterpret_cast<const __nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-// Four e4m3 bytes to bf16. The 7 magnitude bits, moved to the top of the bf16 mantissa and the
-// bottom of its exponent, are the value times 2^-120 (biases 127 and 7; the subnormals of one are
-// subnormals of the other), so one exact multiply by 2^(120 + k), twice in `up`, widens and scales.
-// The bytes come out as (0, 2) and (1, 3), which needs no byte permutation: of every four latent
-// dims the middle two are swapped in the tile, in Q's columns (load_q) and in O's, and O is written
-// the right way round. (With the dims in order: selected e4m3 keys 138.6 us, long 240; 133 and 225
-// this way, the rest by the loads and stores around it.)
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t up, uint32_t& even, uint32_t& odd) {
-  even = mul_bf16x2(((w << 4) & 0x07f007f0u) | ((w << 8) & 0x80008000u), up);
-  odd = mul_bf16x2(((w >> 4) & 0x07f007f0u) | (w & 0x80008000u), up);
-}
+// widen4 gives the bytes as (0, 2) and (1, 3): of every four latent dims the middle two are swapped in
+// the tile, in Q's columns (load_q) and in O's, and O is written the right way round. (With the dims in
+// order: selected e4m3 keys 138.6 us, long 240; 133 and 225 this way, the rest by the loads and stores
+// around it.)
 
 // two bf16 with infinities and NaNs replaced by zero
 __device__ __forceinline__ uint32_t finite2(uint32_t w) {
@@ -860,7 +846,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < kCodeReps; ++j) {
             // 2^(120 + k) twice, or 2^127 and the rest below
-            const uint32_t up = (min(e[j], kScaleMost) + (120u << 7)) * 0x10001u;
+            const uint32_t up = widen_factor(e[j]);
             wide = wide || e[j] > kScaleMost;
             uint4 w0, w1;
             widen4(code[j].x, up, w0.x, w0.y);
@@ -880,7 +866,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               const uint32_t ej = (j & 2 ? (j & 1 ? scales.w : scales.z)
                                          : (j & 1 ? scales.y : scales.x)) >> 16;
               if (ej <= kScaleMost) continue;
-              const uint32_t more = ej > 0x7f80u ? 0x7fff7fffu : (ej - (7u << 7)) * 0x10001u;
+              const uint32_t more = widen_rest(ej);
               uint4* const piece = reinterpret_cast<uint4*>(at + j * 256 + (put ^ (i * 16)));
               uint4 w = *piece;
               w.x = mul_bf16x2(w.x, more);

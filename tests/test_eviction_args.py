@@ -54,6 +54,8 @@ def test_cache_mass_refusals(dsa):
     for bad in (dict(ws=None), dict(ws=MIS), dict(nbytes=need - 1)):
         assert call(idx=P, k=4, **bad) == 3
     assert size(2, 1, 16, 512, 64, 0) == 0 and size(2, 1, 129, 512, 64, 4) == 0
+    need = size(2, 9, 16, 512, 64, 0)      # sums of more than 128 pairs may be split
+    assert need > 0 and call(Sq=9, nbytes=need - 1) == 3 and call(Sq=9, ws=None) == 3
 
 
 def test_cache_keep_refusals(dsa):
