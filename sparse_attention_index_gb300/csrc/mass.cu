@@ -4,24 +4,33 @@
 //   mass[j] = decay prev[j] + sum over tokens i and heads h that see j of exp(scale q_ih . row_j - lse_ih)
 //
 // with lse from the attention itself, so that one more product of queries and rows is all it takes. The
-// keys are the 128 lanes of a tile and the (token, head) pairs its columns, so that a key's sum over
+// keys are the lanes of a tile and the (token, head) pairs its columns, so that a key's sum over
 // tokens and heads stays within one thread:
 //
-//   S [128 keys x 128 pairs] = K [128 x 576] . Q^T,   sum_c exp(scale S_c - lse_c)
+//   S [256 keys x 128 pairs] = K [256 x 576] . Q^T,   sum_c exp(scale S_c - lse_c)
 //
-// Both operands go through shared memory in atoms of 64 dims (16 KB). Up to 128 pairs a sequence (a
-// token with a list always is): Q stays, the rows stream through a ring of five atoms, and memory is
-// the bound. More pairs: a tile's rows stay and the pairs stream past them, 128 at a time; the tensor
-// cores are the bound. The work, tiles or (tile, 128 pairs), is cut into one even range per CTA whatever
+// A tile is the pair instruction's (cta_group::2): each CTA of a cluster of two has 128 of the keys and
+// half of the pairs' rows in its shared memory, so that a query's row is fetched once for 256 keys and
+// takes half the room. Both operands go through shared memory in atoms of 64 dims. Up to 128 pairs a
+// sequence (a token with a list always is): Q stays, the rows stream through a ring, and memory is the
+// bound. More pairs: a tile's rows stay and the pairs stream past them, 128 at a time; the tensor cores
+// are the bound. The work, tiles or (tile, 128 pairs), is cut into one even range per cluster whatever
 // the lengths. A tile whose pairs lie in several ranges leaves a part in each, which
 // join_kernel adds up in order. Lengths are read on the device only.
 //
+// The tensor cores cut off, not round, what an addition moves behind the last bit, always towards zero.
+// Over all 576 dims that would move a weight by 1.5e-6 of itself; so the first five atoms and the
+// last four have an accumulator each (7e-7), added up in the epilogue.
+//
 // Warp-specialised CTA, 704 threads:
 //   warps 0-3   epilogue, one key per thread
-//   warp 4      single-thread UMMA issuer; owns TMEM: two buffers of 128 columns
+//   warp 4      in the first CTA the single-thread UMMA issuer; owns TMEM: two buffers of two
+//               accumulators of 128 columns
 //   warp 5      Q by TMA
-//   warps 6-21  rows, a quarter of a key's atom per thread: bf16 by cp.async, e4m3 by way of
-//               registers (a tile ahead), widened to bf16, exactly
+//   warps 6-21  rows, a quarter of a key's atom per thread: cp.async, bf16 into the operand's place, e4m3
+//               into a ring of raw atoms, then widened to bf16, exactly
+
+#include <mutex>
 
 #include "dsa_common.cuh"
 #include "dsa_internal.h"
@@ -31,46 +40,61 @@ namespace dsa {
 namespace {
 
 constexpr int kDc = 512, kDr = 64, kD = kDc + kDr;
-constexpr int kTile = 128;               // keys of a tile, and pairs at a time
+constexpr int kKeys = 128, kTile = 2 * kKeys;   // keys of a CTA and of a tile
+constexpr int kPairs = 128;              // pairs at a time
 constexpr int kAtoms = kD / 64;
-constexpr uint32_t kAtom = kTile * 128;
-constexpr int kRing = 5;                 // atoms of the operand that streams; the other has all nine
-constexpr int kSlots = kRing + kAtoms;
+constexpr int kFirstAtoms = 5;           // atoms of the first accumulator
+constexpr uint32_t kKeyAtom = kKeys * 128, kQueryAtom = kPairs / 2 * 128;
+constexpr uint32_t kRawAtom = kKeys * 64;   // of codes; one of positional dims is two
+constexpr int kRawSteps = 10;            // raw atoms of a tile: eight of codes, two of positional dims
 constexpr int kIssueWarp = 4, kQueryWarp = 5, kGatherWarp0 = 6, kGatherWarps = 16;
 constexpr int kGatherThreads = 32 * kGatherWarps;
 constexpr int kThreads = 32 * (kGatherWarp0 + kGatherWarps);
-constexpr int kMaxCtas = 256;
+constexpr int kMaxClusters = 128;
 constexpr int kErrIdx = DSA_STAGE_EVICT | DSA_DEVERR_BAD_INDEX;
 constexpr int kErrPage = DSA_STAGE_EVICT | DSA_DEVERR_BAD_PAGE;
 constexpr int kErrTime = DSA_STAGE_EVICT | DSA_DEVERR_TIMEOUT;
-static_assert(kGatherThreads == 4 * kTile, "a quarter of a key's atom per thread");
+static_assert(kGatherThreads == 4 * kKeys, "a quarter of a key's atom per thread");
+
+// 216 KB in 27 pieces of 8 KB: atoms of rows, atoms of Q, raw atoms
+template <bool FP8, bool MULTI>
+struct Layout {
+  static constexpr int kKeySlots = MULTI || !FP8 ? kAtoms : 5;
+  static constexpr int kQuerySlots = MULTI && FP8 ? 5 : kAtoms;
+  static constexpr int kRawSlots = FP8 ? (MULTI ? 4 : 8) : 0;
+  static constexpr uint32_t kQueryOff = kKeySlots * kKeyAtom;
+  static constexpr uint32_t kRawOff = kQueryOff + kQuerySlots * kQueryAtom;
+  static constexpr uint32_t kTailOff = kRawOff + kRawSlots * kRawAtom;
+};
 
 struct Tail {
-  float nlse[2][kTile];      // -lse of the pairs
-  int lim[2][kTile];         // positions below it are seen by the pair; a pair that adds nothing: none
+  float nlse[2][kPairs];     // -lse of the pairs
+  int lim[2][kPairs];        // positions below it are seen by the pair; a pair that adds nothing: none
   int group_lim[2][4];       // the least of 32 pairs
   uint32_t valid[4][kGatherWarps];   // the tile's keys that are there: four bits a key
-  uint64_t k_full[kAtoms], k_empty[kAtoms], q_full[kAtoms], q_empty[kAtoms];   // of ring or residents
+  uint64_t k_full[kAtoms], k_empty[kAtoms], q_full[kAtoms], q_empty[kAtoms];
   uint64_t d_full[2], d_empty[2], valid_full[4], staged, drain;
   uint32_t tmem_base;
   int abort_flag;
   long long sums[kThreads / 32];
-  // this CTA's range: its first item and the first unit of it here, and how many units
+  // this cluster's range: its first item and the first unit of it here, and how many units
   int item0;
   long long first, count;
 };
-constexpr size_t kSmem = kSlots * kAtom + sizeof(Tail);
-static_assert(kSmem <= 232448, "shared memory of a block");
+static_assert(Layout<true, true>::kTailOff + sizeof(Tail) <= 232448 &&
+                  Layout<true, false>::kTailOff + sizeof(Tail) <= 232448 &&
+                  Layout<false, true>::kTailOff + sizeof(Tail) <= 232448,
+              "shared memory of a block");
 
 struct Params {
   MassArgs a;
   int items;        // sequences, or tokens with a list each
   int nts;          // columns of 128 pairs
-  int box;          // pairs loaded at a time (a multiple of 16)
+  int box;          // pairs at a time (a multiple of 16), half of them in each CTA
   int page_shift;   // log2 of the page size, -1 where it is no power of two
   float* w;         // lists: the weight of each entry [B, Sq, k]
-  float* part;      // [2 * ctas][128]
-  int4* joins;      // [ctas]: (sequence, tile, last CTA that has a part of it) or (-1, ...)
+  float* part;      // [2 * clusters][256]
+  int4* joins;      // [clusters]: (sequence, tile, last cluster that has a part of it) or (-1, ...)
 };
 
 __device__ __forceinline__ int seq_len(const MassArgs& a, int b, bool report) {
@@ -82,10 +106,10 @@ __device__ __forceinline__ int seq_len(const MassArgs& a, int b, bool report) {
 
 __device__ __forceinline__ int item_tiles(const Params& p, int item) {
   const int keys = p.a.idx ? p.a.k : min(p.a.n, seq_len(p.a, item, false));
-  return (keys + kTile - 1) / kTile;   // (n and k are at most 2^30)
+  return keys > 0 ? (keys - 1) / kTile + 1 : 0;
 }
 
-// this CTA's range of units, into the tail; every thread of the block calls it, before a barrier
+// this cluster's range of units, into the tail; every thread of the block calls it, before a barrier
 template <bool MULTI>
 __device__ __forceinline__ void my_units(const Params& p, Tail* tail) {
   const long long per_tile = MULTI ? p.nts : 1;
@@ -114,8 +138,9 @@ __device__ __forceinline__ void my_units(const Params& p, Tail* tail) {
     }
     before += incl - s;
   }
-  const long long each = (total + gridDim.x - 1) / gridDim.x;
-  const long long u0 = min(total, each * blockIdx.x), u1 = min(total, u0 + each);
+  const int clusters = gridDim.x >> 1, cluster = blockIdx.x >> 1;
+  const long long each = (total + clusters - 1) / clusters;
+  const long long u0 = min(total, each * cluster), u1 = min(total, u0 + each);
   if (u0 == u1) return;   // count stays 0
   if (p.a.idx) {
     if (threadIdx.x != 0) return;
@@ -136,7 +161,7 @@ __device__ __forceinline__ void my_units(const Params& p, Tail* tail) {
   }
 }
 
-// where a warp stands in its CTA's range
+// where a warp stands in its cluster's range
 template <bool MULTI>
 struct Cursor {
   int item, tile, nt, tiles;
@@ -193,6 +218,68 @@ __device__ __forceinline__ float ex2f(float x) {
   return y;
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// the address of a barrier of the first CTA, from either
+__device__ __forceinline__ uint32_t first_cta(const uint64_t* bar) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(bar)));
+  return r;
+}
+// Arrives at a barrier of the first CTA, without a scope of its own: a release at cluster scope waits
+// for all that the warp has on its way, copies too, and took 88 us instead of XX (32 ragged e4m3
+// sequences). What has to be in order here is in the writer's own SM, where the tensor cores read it:
+// its shared memory, which fence.proxy.async has made theirs in front of this, or TMEM, read in front of
+// tcgen05.wait::ld. Nothing that another thread reads by plain loads hangs on these barriers.
+__device__ __forceinline__ void arrive_first_cta(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// tma_load_2d that counts on a barrier of the first CTA, from either
+__device__ __forceinline__ void tma2_load_2d(void* dst, const void* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+
+// The pair instruction: A is 128 rows of each CTA, B half of the columns of each, at the same places.
+__device__ __forceinline__ void umma2_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrive once on `bar` of both CTAs when every earlier tcgen05.mma of this thread has completed.
+__device__ __forceinline__ void umma2_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 // the slot counter of a ring, and the parity to wait for
 template <int N>
 struct Ring {
@@ -209,50 +296,57 @@ struct Ring {
 // ------------------------------------------------------------------ the kernel
 
 template <bool FP8, bool MULTI>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mass_kernel(const Params p, const __grid_constant__ CUtensorMap qmap) {
-  constexpr int kKeySlots = MULTI ? kAtoms : kRing, kQuerySlots = MULTI ? kRing : kAtoms;
+  using L = Layout<FP8, MULTI>;
+  constexpr int kKeySlots = L::kKeySlots, kQuerySlots = L::kQuerySlots;
+  constexpr int kNone = -0x7fffffff - 1;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* const qsmem = smem + kKeySlots * kAtom;
-  Tail* tail = reinterpret_cast<Tail*>(smem + kSlots * kAtom);
+  uint8_t* const qsmem = smem + L::kQueryOff;
+  Tail* tail = reinterpret_cast<Tail*>(smem + L::kTailOff);
   volatile int* abort_flag = &tail->abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int cluster = blockIdx.x >> 1;
   const MassArgs& a = p.a;
   int* err = a.err;
+  // the same in both CTAs of a cluster (one layout), so both leave
   if ((smem_u32(smem) & 1023u) != 0) {
     if (threadIdx.x == 0) report_error(err, DSA_STAGE_EVICT | DSA_DEVERR_MISALIGNED);
     return;
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kAtoms; ++i) {
-      mbar_init(&tail->k_full[i], kGatherThreads);
+      mbar_init(&tail->k_full[i], 2 * kGatherWarps);   // of the first CTA: both CTAs' rows
       mbar_init(&tail->k_empty[i], 1);
-      mbar_init(&tail->q_full[i], 1);
+      mbar_init(&tail->q_full[i], 1);                  // of the first CTA: both CTAs' halves
       mbar_init(&tail->q_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tail->d_full[i], 1);
-      mbar_init(&tail->d_empty[i], kTile);
+      mbar_init(&tail->d_empty[i], 8);                 // of the first CTA: both CTAs' epilogue warps
     }
     for (int i = 0; i < 4; ++i) mbar_init(&tail->valid_full[i], kGatherWarps);
-    mbar_init(&tail->staged, kTile);
+    mbar_init(&tail->staged, kPairs);
     mbar_init(&tail->drain, 1);
     tail->abort_flag = 0;
     tail->count = 0;
     fence_mbar_init();
   }
   if (warp == kIssueWarp) {
-    tmem_alloc(&tail->tmem_base, 256);
-    tmem_relinquish();
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                     smem_u32(&tail->tmem_base))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __syncthreads();
   my_units<MULTI>(p, tail);
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();   // and both CTAs' barriers and TMEM are there
   tc_fence_after();
   const uint32_t tmem = tail->tmem_base;
-  const long long n = tail->count;
+  const long long n = tail->count;   // the same in both CTAs
 
   if (warp < 4) {
     // ================================================================ epilogue
@@ -266,11 +360,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = z0 + lane; j < z1; j += 32) a.mass[static_cast<long long>(b) * a.n + j] = 0.f;
       }
     }
-    const int key = threadIdx.x;   // TMEM lane
+    const int me = threadIdx.x;   // TMEM lane
+    const int key = rank * kKeys + me;   // of the tile
     const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
     const int pairs = a.idx ? a.H : a.Sq * a.H;   // of an item
     const float2 scale2 = make_float2(a.scale, a.scale);
     const float2 log2e = make_float2(1.4426950408889634f, 1.4426950408889634f);
+    const uint32_t d_empty[2] = {first_cta(&tail->d_empty[0]), first_cta(&tail->d_empty[1])};
     if (n > 0) {
       Cursor<MULTI> c(p, tail);
       int cur_item = -1, len = 0;
@@ -292,9 +388,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // buffer was last read two stages ago, before every thread's arrival at the last one.)
         if (MULTI || fresh_item) {
           const int w = stages & 1;
-          const int pr = c.nt * kTile + key;
+          const int pr = c.nt * kPairs + me;
           float v = 0.f;
-          int lim = -0x7fffffff - 1;
+          int lim = kNone;
           if (pr < pairs) {
             const long long row = static_cast<long long>(c.item) * pairs + pr;
             const float lse = __ldg(a.lse + row);
@@ -302,8 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             v = -lse;
             if (lse != -INFINITY) lim = len - a.Sq + token + 1;
           }
-          tail->nlse[w][key] = v;
-          tail->lim[w][key] = lim;
+          tail->nlse[w][me] = v;
+          tail->lim[w][me] = lim;
           lim = __reduce_min_sync(0xffffffffu, lim);
           if (lane == 0) tail->group_lim[w][warp] = lim;
           __syncwarp();
@@ -319,84 +415,89 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!__all_sync(0xffffffffu, mbar_wait(&tail->valid_full[vb], (tiles_done >> 2) & 1,
                                                  abort_flag, err, kErrTime)))
             break;
-          there = (tail->valid[vb][key >> 3] >> (4 * (key & 7)) & 1u) != 0;
+          there = (tail->valid[vb][me >> 3] >> (4 * (me & 7)) & 1u) != 0;
           ++tiles_done;
         }
         if (!__all_sync(0xffffffffu, mbar_wait(&tail->d_full[buf], par, abort_flag, err, kErrTime)))
           break;
         tc_fence_after();
-        const int j0 = c.tile * kTile;
+        const long long j = static_cast<long long>(c.tile) * kTile + key;
         // lists: a key that its token does not see is not there
-        const int last = a.idx ? -0x7fffffff - 1 : min(j0 + kTile, len);
+        const int last =
+            a.idx ? kNone
+                  : static_cast<int>(min(static_cast<long long>(c.tile + 1) * kTile, static_cast<long long>(len)));
         float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         float some = 0.f;
+        const uint32_t d = tmem + lane_off + buf * 2 * kPairs;
 #pragma unroll 1
-        for (int g = 0; g < 4; ++g) {
-          if (c.nt * kTile + g * 32 >= pairs) break;
-          uint32_t s[32];
-          tmem_ld_x32(tmem + lane_off + buf * kTile + g * 32, s);
+        for (int g = 0; g < kPairs / 16; ++g) {
+          if (c.nt * kPairs + g * 16 >= pairs) break;
+          uint32_t s0[16], s1[16];
+          tmem_ld_16(d + g * 16, s0);
+          tmem_ld_16(d + kPairs + g * 16, s1);
           tmem_ld_wait();
-          const float4* nl = reinterpret_cast<const float4*>(&tail->nlse[sb][g * 32]);
-          const int least = tail->group_lim[sb][g];
-          if (least != -0x7fffffff - 1 && least >= last) {
+          float2 s[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            s[q] = add2(make_float2(__uint_as_float(s0[2 * q]), __uint_as_float(s0[2 * q + 1])),
+                        make_float2(__uint_as_float(s1[2 * q]), __uint_as_float(s1[2 * q + 1])));
+          const float4* nl = reinterpret_cast<const float4*>(&tail->nlse[sb][g * 16]);
+          const int least = tail->group_lim[sb][g >> 1];
+          if (least != kNone && least >= last) {
             // every pair of the group sees every key of the tile
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
+            for (int q = 0; q < 4; ++q) {
               const float4 v = nl[q];
               // the difference first, in one rounding: far from zero those of the products with
               // log2(e) would move the weight
-              float2 x = fma2(make_float2(__uint_as_float(s[4 * q]), __uint_as_float(s[4 * q + 1])),
-                              scale2, make_float2(v.x, v.y));
-              float2 y = fma2(make_float2(__uint_as_float(s[4 * q + 2]), __uint_as_float(s[4 * q + 3])),
-                              scale2, make_float2(v.z, v.w));
+              float2 x = fma2(s[2 * q], scale2, make_float2(v.x, v.y));
+              float2 y = fma2(s[2 * q + 1], scale2, make_float2(v.z, v.w));
               x = mul2(x, log2e);
               y = mul2(y, log2e);
               acc[0] = add2(acc[0], make_float2(ex2f(x.x), ex2f(x.y)));
               acc[1] = add2(acc[1], make_float2(ex2f(y.x), ex2f(y.y)));
             }
           } else {
-            const int j = a.idx ? -0x7fffffff - 1 : j0 + key;
 #pragma unroll
-            for (int q = 0; q < 32; ++q) {
-              const int lim = tail->lim[sb][g * 32 + q];
-              const float x = fmaf(__uint_as_float(s[q]), a.scale, tail->nlse[sb][g * 32 + q]);
-              // (with lists j is below every limit but that of a pair that adds nothing)
-              if (lim != -0x7fffffff - 1 && j < lim) some += ex2f(x * log2e.x);
+            for (int q = 0; q < 16; ++q) {
+              const int lim = tail->lim[sb][g * 16 + q];
+              const float x = fmaf(q & 1 ? s[q / 2].y : s[q / 2].x, a.scale, tail->nlse[sb][g * 16 + q]);
+              if (lim != kNone && (a.idx || j < lim)) some += ex2f(x * log2e.x);
             }
           }
         }
         tc_fence_before();
-        mbar_arrive(&tail->d_empty[buf]);
+        __syncwarp();
+        if (lane == 0) arrive_first_cta(d_empty[buf]);
         sum += ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) + some;
         if (!MULTI || c.nt == p.nts - 1 || u == n - 1) {
           if (!there) sum = 0.f;
           if (a.idx) {
-            if (j0 + key < a.k) p.w[static_cast<long long>(c.item) * a.k + j0 + key] = sum;
+            if (j < a.k) p.w[static_cast<long long>(c.item) * a.k + j] = sum;
           } else if (whole && (!MULTI || c.nt == p.nts - 1)) {
-            if (j0 + key < min(len, a.n)) {
-              const long long at = static_cast<long long>(c.item) * a.n + j0 + key;
+            if (j < min(len, a.n)) {
+              const long long at = static_cast<long long>(c.item) * a.n + j;
               a.mass[at] = a.prev ? fmaf(a.decay, a.prev[at], sum) : sum;
             }
           } else {
             // part 0: a tile begun in front of the range; part 1: one that goes on behind it
-            p.part[(2ll * blockIdx.x + (whole ? 1 : 0)) * kTile + key] = sum;
+            p.part[(2ll * cluster + (whole ? 1 : 0)) * kTile + key] = sum;
           }
         }
         if (MULTI && u == n - 1 && key == 0) {
           const int left = p.nts - 1 - c.nt;
           const int each = static_cast<int>(min(n, 0x40000000ll));   // this range is not the last one
-          p.joins[blockIdx.x] = whole && left > 0
-                                    ? make_int4(c.item, c.tile, blockIdx.x + (left + each - 1) / each, 0)
-                                    : make_int4(-1, 0, 0, 0);
+          p.joins[cluster] = whole && left > 0 ? make_int4(c.item, c.tile, cluster + (left + each - 1) / each, 0)
+                                               : make_int4(-1, 0, 0, 0);
         }
         c.next(p);
       }
     } else if (MULTI && key == 0) {
-      p.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
+      p.joins[cluster] = make_int4(-1, 0, 0, 0);
     }
   } else if (warp == kIssueWarp) {
     // ================================================================ UMMA issuer
-    if (lane == 0 && n > 0) {
+    if (lane == 0 && n > 0 && rank == 0) {
       const uint32_t idesc = umma_idesc_bf16(kTile, p.box);
       const uint64_t k0 = umma_sdesc(smem_u32(smem), 1024, kLayoutSw128);
       const uint64_t q0 = umma_sdesc(smem_u32(qsmem), 1024, kLayoutSw128);
@@ -419,25 +520,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok && (MULTI || first))
             ok = mbar_wait(&tail->q_full[qr.slot], qr.round, abort_flag, err, kErrTime);
           if (!ok) break;
-          fence_proxy_async_smem();   // the rows were written by the generic proxy
           tc_fence_after();
-          const uint64_t kd = umma_desc_adv(k0, kr.slot * kAtom), qd = umma_desc_adv(q0, qr.slot * kAtom);
+          const uint64_t kd = umma_desc_adv(k0, kr.slot * kKeyAtom);
+          const uint64_t qd = umma_desc_adv(q0, qr.slot * kQueryAtom);
+          const uint32_t dst = tmem + (2 * buf + (d >= kFirstAtoms ? 1 : 0)) * kPairs;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_bf16(tmem + buf * kTile, umma_desc_adv(kd, kk * 32), umma_desc_adv(qd, kk * 32), idesc,
-                      d > 0 || kk > 0 ? 1u : 0u);
-          if (!MULTI || last) umma_commit(&tail->k_empty[kr.slot]);
-          if (MULTI || last) umma_commit(&tail->q_empty[qr.slot]);
+            umma2_bf16(dst, umma_desc_adv(kd, kk * 32), umma_desc_adv(qd, kk * 32), idesc,
+                       (d == 0 || d == kFirstAtoms) && kk == 0 ? 0u : 1u);
+          if (!MULTI || last) umma2_commit(&tail->k_empty[kr.slot]);
+          if (MULTI || last) umma2_commit(&tail->q_empty[qr.slot]);
           kr.next();
           qr.next();
-          // what stays is read again: its phase is over only with the last use
-          if (MULTI && !last && kr.slot == 0) kr.round ^= 1u;
-          if (!MULTI && !last && qr.slot == 0) qr.round ^= 1u;
         }
-        if (ok) umma_commit(&tail->d_full[buf]);
+        // what stays is read again: its phase is over only with the last use
+        if (!last) {
+          if (MULTI)
+            kr.round ^= 1u;
+          else
+            qr.round ^= 1u;
+        }
+        if (ok) umma2_commit(&tail->d_full[buf]);
         c.next(p);
       }
-      umma_commit(&tail->drain);
+      umma2_commit(&tail->drain);
       const unsigned long long t0 = globaltimer_ns();
       while (!mbar_try_wait(smem_u32(&tail->drain), 0)) {
         if (globaltimer_ns() - t0 > kWaitLimitNs) {
@@ -451,34 +557,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0 && n > 0) {
       tma_prefetch_desc(&qmap);
       const int pairs = a.idx ? a.H : a.Sq * a.H;
+      const uint32_t full0 = first_cta(&tail->q_full[0]);
       Cursor<MULTI> c(p, tail);
       Ring<kQuerySlots> qr;
       bool ok = true;
-      long long loads = 0;
 #pragma unroll 1
       for (long long u = 0; ok && u < n; ++u) {
         if (MULTI || u == 0 || c.tile == 0) {
-          const int row = c.item * pairs + c.nt * kTile;
+          const int row = c.item * pairs + c.nt * kPairs + rank * (p.box / 2);
 #pragma unroll 1
           for (int d = 0; d < kAtoms; ++d) {
             ok = mbar_wait(&tail->q_empty[qr.slot], qr.round ^ 1u, abort_flag, err, kErrTime);
             if (!ok) break;
-            mbar_arrive_expect_tx(&tail->q_full[qr.slot], p.box * 128);
-            tma_load_2d(qsmem + qr.slot * kAtom, &qmap, &tail->q_full[qr.slot], d * 64, row);
+            // (the second CTA's half may come in front of this: its bytes are only taken off)
+            if (rank == 0) mbar_arrive_expect_tx(&tail->q_full[qr.slot], p.box * 128);
+            tma2_load_2d(qsmem + qr.slot * kQueryAtom, &qmap, full0 + qr.slot * 8, d * 64, row);
             qr.next();
-            ++loads;
           }
         }
         c.next(p);
       }
       if (*abort_flag) {
-        // what is on its way lands before the block ends: the last load of each slot
+        // what is on its way lands before the block ends: some time for it, since the barrier's phase
+        // may hang on the other CTA
         const unsigned long long t0 = globaltimer_ns();
-        for (int i = 0; i < kQuerySlots && i < loads; ++i) {
-          const uint32_t round = i < qr.slot ? qr.round : qr.round ^ 1u;
-          while (!mbar_try_wait(smem_u32(&tail->q_full[i]), round) &&
-                 globaltimer_ns() - t0 < kWaitLimitNs) {
-          }
+        while (globaltimer_ns() - t0 < 1000000ull) {
         }
       }
     }
@@ -504,9 +607,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       f.b = a.idx ? ahead.item / a.Sq : ahead.item;
       f.len = seq_len(a, f.b, false);
       f.limit = a.idx ? f.len - a.Sq + ahead.item % a.Sq + 1 : min(f.len, a.n);
-      f.raw = ahead.tile * kTile + key;
-      if (a.idx)
-        f.raw = f.raw < a.k ? __ldg(a.idx + static_cast<long long>(ahead.item) * a.k + f.raw) : -1;
+      const uint32_t j = static_cast<uint32_t>(ahead.tile) * kTile + rank * kKeys + key;
+      if (a.idx)   // (k may be within a tile of 2^31)
+        f.raw = j < static_cast<uint32_t>(a.k)
+                    ? __ldg(a.idx + static_cast<long long>(ahead.item) * a.k + j)
+                    : -1;
+      else
+        f.raw = static_cast<int>(j);   // n is at most 2^30
       return f;
     };
     struct Paged {
@@ -544,8 +651,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&tail->valid_full[tiles & 3]);
       }
     };
+    // A warp's part of an atom is written: one arrival for it. (One per thread, 512 an atom, is level:
+    // what took the time were the loads.)
+    const uint32_t full0 = first_cta(&tail->k_full[0]);
+    auto tell_full = [&](int slot) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive_first_cta(full0 + slot * 8);
+    };
     const uint32_t at = key * 128;
-    if (!FP8) {
+    if constexpr (!FP8) {
+      // copies of up to kLag atoms behind the newest are on their way
+      constexpr int kLag = 6;   // fewer than the ring's atoms: a slot comes free after its atom is told of
+      static_assert(kLag < kKeySlots, "a slot comes free");
+      Ring<kKeySlots> landed;
+      int flying = 0;
       const uint8_t* row = row_of(page_of(look()));
       bool ok = true;
 #pragma unroll 1
@@ -560,57 +680,93 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait_empty();
           if (!ok) break;
           if (d == 0) tell_valid(tiles, row != nullptr);
-          const uint32_t dst = base + kr.slot * kAtom + at;
+          const uint32_t dst = base + kr.slot * kKeyAtom + at;
           cp_async_16(dst + ((sub ^ (key & 7)) << 4), src + d * 128 + sub * 16, bytes);
           cp_async_16(dst + (((sub + 4) ^ (key & 7)) << 4), src + d * 128 + 64 + sub * 16, bytes);
-          cp_async_mbar_arrive(&tail->k_full[kr.slot]);
+          cp_async_commit();
           kr.next();
+          if (flying < kLag) {
+            ++flying;
+          } else {
+            cp_async_wait<kLag>();
+            tell_full(landed.slot);
+            landed.next();
+          }
           if (d == 3) q = page_of(f);
         }
         row = row_of(q);
+        // the last ones; a tile that stays is waited for as a whole before its slots come free again
+        if (MULTI || !more()) {
+          cp_async_wait<0>();
+          for (; ok && flying > 0; --flying) {
+            tell_full(landed.slot);
+            landed.next();
+          }
+        }
       }
       cp_async_wait<0>();
     } else {
-      // A tile's codes, scales and positional dims are loaded into registers a tile ahead.
-      uint4 code[8], rope[2], scale, next_scale;
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      auto load_code = [&](const uint8_t* row, int d) {
-        code[d] = row ? __ldg(reinterpret_cast<const uint4*>(row + d * 64 + sub * 16)) : zero;
+      // Raw ring: a thread copies in what it widens itself, step by step: eight pieces of 16 codes, two of
+      // positional dims, kAhead steps ahead. The scales come by way of a register, a tile ahead.
+      constexpr int kAhead = L::kRawSlots;
+      const uint32_t raw0 = base + L::kRawOff + t * 16;
+      auto fetch = [&](const uint8_t* row, int step, int slot) {
+        const int from = step < 8 ? step * 64 : kDc + 16 + (step - 8) * 64;
+        cp_async_16(raw0 + slot * kRawAtom, (row ? row : a.cache) + from + sub * 16, row ? 16u : 0u);
       };
-      auto load_rope = [&](const uint8_t* row) {
-        rope[0] = row ? __ldg(reinterpret_cast<const uint4*>(row + kDc + 16 + sub * 16)) : zero;
-        rope[1] = row ? __ldg(reinterpret_cast<const uint4*>(row + kDc + 16 + 64 + sub * 16)) : zero;
+      auto scales_of = [&](const uint8_t* row) {
+        return row ? __ldg(reinterpret_cast<const uint4*>(row + kDc)) : make_uint4(0, 0, 0, 0);
       };
-      auto load_scale = [&](const uint8_t* row) {
-        next_scale = row ? __ldg(reinterpret_cast<const uint4*>(row + kDc)) : zero;
-      };
-      const uint8_t* row = row_of(page_of(look()));   // of the tile in registers
-      load_scale(row);
-#pragma unroll
-      for (int d = 0; d < 8; ++d) load_code(row, d);
-      load_rope(row);
-      bool there = row != nullptr;
+      const uint8_t* row = row_of(page_of(look()));   // of the tile that is fetched
+      bool there = row != nullptr;                    // of the tile that is widened
+      long long togo = left;                          // units of it and of those behind it
+      uint4 scale = scales_of(row);
+      // the next two tiles
       advance();
-      row = row_of(page_of(look()));                  // of the one to be loaded
-      long long togo = n + (MULTI ? Cursor<MULTI>(p, tail).nt : 0);   // units of the tiles left
+      const uint8_t* next = row_of(page_of(look()));
+      if (more()) advance();
+      Found f = look();
+      Paged q = {-1, -1};
+      int fstep = 0;    // the next step to be fetched
+      for (int i = 0; i < kAhead; ++i) {   // (no more than a tile's steps)
+        fetch(row, fstep, i);
+        cp_async_commit();
+        ++fstep;
+      }
+      static_assert(kAhead < kRawSteps, "the first fetches are of one tile");
+      int slot = 0;
       bool ok = true;
 #pragma unroll 1
       for (int tiles = 0; ok && togo > 0; ++tiles, togo -= MULTI ? p.nts : 1) {
-        if (more()) advance();
-        const Found f = look();   // two tiles ahead
-        Paged q = {-1, -1};
-        scale = next_scale;
-        load_scale(row);
-#pragma unroll
+        uint4 next_scale = scale;
+        const bool there_now = there;
+        // one step: its piece out of the ring, and the piece kAhead steps on into the same place
+        auto step = [&]() {
+          cp_async_wait<kAhead - 1>();
+          uint4 x;
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                       : "r"(raw0 + slot * kRawAtom)
+                       : "memory");
+          return x;
+        };
+        auto refill = [&]() {
+          if (fstep == kRawSteps) {   // on to the next tile
+            fstep = 0;
+            row = next;
+            there = row != nullptr;
+            next_scale = scales_of(row);
+          }
+          fetch(row, fstep, slot);
+          cp_async_commit();
+          ++fstep;
+          slot = slot + 1 == kAhead ? 0 : slot + 1;
+        };
+#pragma unroll 1
         for (int d = 0; d < 8; ++d) {
-          ok = wait_empty();
-          if (!ok) break;
-          if (d == 0) tell_valid(tiles, there);
-          uint8_t* dst = smem + kr.slot * kAtom + at;
+          const uint4 x = step();
           const uint32_t e = (d < 2 ? scale.x : d < 4 ? scale.y : d < 6 ? scale.z : scale.w) >> 16;
           const uint32_t up = widen_factor(e);
-          const uint4 x = code[d];
-          load_code(row, d);
           uint4 w0, w1;
           // (bytes 0 2 1 3, so that they come out in order)
           widen4(__byte_perm(x.x, 0, 0x3120), up, w0.x, w0.y);
@@ -624,42 +780,53 @@ __global__ void __launch_bounds__(kThreads, 1)
             w1 = make_uint4(mul_bf16x2(w1.x, rest), mul_bf16x2(w1.y, rest), mul_bf16x2(w1.z, rest),
                             mul_bf16x2(w1.w, rest));
           }
+          refill();
+          ok = wait_empty();
+          if (!ok) break;
+          if (d == 0) tell_valid(tiles, there_now);
+          uint8_t* dst = smem + kr.slot * kKeyAtom + at;
           *reinterpret_cast<uint4*>(dst + (((2 * sub) ^ (key & 7)) << 4)) = w0;
           *reinterpret_cast<uint4*>(dst + (((2 * sub + 1) ^ (key & 7)) << 4)) = w1;
-          fence_proxy_async_smem();
-          mbar_arrive(&tail->k_full[kr.slot]);
+          tell_full(kr.slot);
           kr.next();
-          if (d == 3) q = page_of(f);
+          // the tile two ahead, between the fetches: its page, then its row
+          if (d == 4) q = page_of(f);
         }
         if (!ok) break;
+        const uint4 r0 = step();
+        refill();
+        const uint4 r1 = step();
+        refill();
         ok = wait_empty();
         if (!ok) break;
-        uint8_t* dst = smem + kr.slot * kAtom + at;
-        *reinterpret_cast<uint4*>(dst + ((sub ^ (key & 7)) << 4)) = rope[0];
-        *reinterpret_cast<uint4*>(dst + (((sub + 4) ^ (key & 7)) << 4)) = rope[1];
-        load_rope(row);
-        fence_proxy_async_smem();
-        mbar_arrive(&tail->k_full[kr.slot]);
+        uint8_t* dst = smem + kr.slot * kKeyAtom + at;
+        *reinterpret_cast<uint4*>(dst + ((sub ^ (key & 7)) << 4)) = r0;
+        *reinterpret_cast<uint4*>(dst + (((sub + 4) ^ (key & 7)) << 4)) = r1;
+        tell_full(kr.slot);
         kr.next();
-        there = row != nullptr;
-        row = row_of(q);
+        scale = next_scale;
+        next = row_of(q);
+        if (more()) advance();
+        f = look();
       }
+      cp_async_wait<0>();
     }
   }
 
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();   // no CTA leaves while the other may still write to it
   tc_fence_after();
-  if (warp == kIssueWarp) tmem_dealloc(tmem, 256);
+  if (warp == kIssueWarp)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-// A tile that begins in CTA c's range and goes on behind it: its parts, one after the other.
-__global__ void __launch_bounds__(kTile) join_kernel(const Params p, int ctas) {
+// A tile that begins in cluster c's range and goes on behind it: its parts, one after the other.
+__global__ void __launch_bounds__(kTile) join_kernel(const Params p, int clusters) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const MassArgs& a = p.a;
   const int4 t = __ldcg(p.joins + blockIdx.x);
-  // nothing to join, or not written: a CTA whose waits ran out (recorded) leaves what was there
-  if (t.x < 0 || t.x >= a.B || t.y < 0 || t.z <= static_cast<int>(blockIdx.x) || t.z >= ctas) return;
+  // nothing to join, or not written: a cluster whose waits ran out (recorded) leaves what was there
+  if (t.x < 0 || t.x >= a.B || t.y < 0 || t.z <= static_cast<int>(blockIdx.x) || t.z >= clusters) return;
   const int len = min(seq_len(a, t.x, false), a.n);
   if (t.y >= (len + kTile - 1) / kTile) return;
   const int j = t.y * kTile + threadIdx.x;
@@ -721,60 +888,87 @@ bool query_map(CUtensorMap* map, const void* Q, long long rows, int box) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Clusters of the kernel that fit on the current device at once; the first call on a device also
+// raises the kernel's shared-memory limit there.
+template <bool FP8, bool MULTI>
+int resident_clusters(size_t smem) {
+  constexpr int kMaxDevices = 64;
+  static int known[kMaxDevices] = {};
+  static std::mutex lock;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  std::lock_guard<std::mutex> guard(lock);
+  if (known[dev] == 0) {
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (cudaFuncSetAttribute(mass_kernel<FP8, MULTI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem)) != cudaSuccess)
+      return 0;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sms / 2 * 2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int c = 0;
+    if (cudaOccupancyMaxActiveClusters(&c, mass_kernel<FP8, MULTI>, &cfg) != cudaSuccess || c < 1) return 0;
+    known[dev] = c < kMaxClusters ? c : kMaxClusters;
+  }
+  return known[dev];
+}
+
 template <bool FP8, bool MULTI>
 int launch(Params p, cudaStream_t stream) {
   const MassArgs& a = p.a;
   const int pairs = a.idx ? a.H : a.Sq * a.H;
   p.items = a.idx ? a.B * a.Sq : a.B;
-  p.nts = (pairs + kTile - 1) / kTile;
-  p.box = pairs < kTile ? (pairs + 15) / 16 * 16 : kTile;
+  p.nts = (pairs - 1) / kPairs + 1;
+  p.box = pairs < kPairs ? (pairs + 15) / 16 * 16 : kPairs;
   CUtensorMap map;
-  if (!query_map(&map, a.Q, static_cast<long long>(a.B) * a.Sq * a.H, p.box)) return DSA_ERR_CUDA;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return DSA_ERR_CUDA;
-  if (cudaFuncSetAttribute(mass_kernel<FP8, MULTI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(kSmem)) != cudaSuccess)
-    return DSA_ERR_CUDA;
-  // no more CTAs than the longest possible sequences have work for
+  if (!query_map(&map, a.Q, static_cast<long long>(a.B) * a.Sq * a.H, p.box / 2)) return DSA_ERR_CUDA;
+  const size_t smem = Layout<FP8, MULTI>::kTailOff + sizeof(Tail);
+  int clusters = resident_clusters<FP8, MULTI>(smem);
+  if (clusters < 1) return DSA_ERR_CUDA;
+  // no more clusters than the longest possible sequences have work for
   const long long cap = static_cast<long long>(a.max_pages) * a.page_size;
   const long long keys = a.idx ? a.k : cap < a.n ? cap : a.n;
   const long long most = p.items * ((keys + kTile - 1) / kTile) * (MULTI ? p.nts : 1);
-  int ctas = sms < kMaxCtas ? sms : kMaxCtas;
-  if (most < ctas) ctas = static_cast<int>(most);
+  if (most < clusters) clusters = static_cast<int>(most);
   if (MULTI) {
     p.part = static_cast<float*>(a.ws);
-    p.joins = reinterpret_cast<int4*>(p.part + 2 * kMaxCtas * kTile);
+    p.joins = reinterpret_cast<int4*>(p.part + 2 * kMaxClusters * kTile);
   }
   p.w = static_cast<float*>(a.ws);
-  mass_kernel<FP8, MULTI><<<ctas, kThreads, kSmem, stream>>>(p, map);
+  mass_kernel<FP8, MULTI><<<2 * clusters, kThreads, smem, stream>>>(p, map);
   if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
   if (a.idx) {
     const long long blocks = static_cast<long long>(a.B) * ((a.n + kSlice - 1) / kSlice);
     add_lists_kernel<<<static_cast<unsigned>(blocks), kAddThreads, 0, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
   }
-  if (!MULTI || ctas == 1) return DSA_OK;   // nothing is split
-  // its blocks may be set up while the last CTAs finish; they wait for the parts
+  if (!MULTI || clusters == 1) return DSA_OK;   // nothing is split
+  // its blocks may be set up while the last clusters finish; they wait for the parts
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas - 1);
+  cfg.gridDim = dim3(clusters - 1);
   cfg.blockDim = dim3(kTile);
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel, p, ctas) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, join_kernel, p, clusters) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
 }  // namespace
 
 size_t cache_mass_workspace(int B, int Sq, int H, int k) {
   if (k > 0) return static_cast<size_t>(B) * Sq * k * sizeof(float);
-  if (static_cast<long long>(Sq) * H <= kTile) return 0;
-  return 2 * kMaxCtas * kTile * sizeof(float) + kMaxCtas * sizeof(int4);
+  if (static_cast<long long>(Sq) * H <= kPairs) return 0;
+  return 2 * kMaxClusters * kTile * sizeof(float) + kMaxClusters * sizeof(int4);
 }
 
 int launch_cache_mass(const MassArgs& a, int fmt, cudaStream_t stream) {
@@ -783,7 +977,7 @@ int launch_cache_mass(const MassArgs& a, int fmt, cudaStream_t stream) {
   p.page_shift = -1;
   for (int i = 0; i < 31; ++i)
     if (a.page_size == 1 << i) p.page_shift = i;
-  const bool multi = !a.idx && static_cast<long long>(a.Sq) * a.H > kTile;
+  const bool multi = !a.idx && static_cast<long long>(a.Sq) * a.H > kPairs;
   if (fmt == DSA_CACHE_E4M3)
     return multi ? launch<true, true>(p, stream) : launch<true, false>(p, stream);
   return multi ? launch<false, true>(p, stream) : launch<false, false>(p, stream);
