@@ -23,6 +23,16 @@ __device__ __forceinline__ void widen4(uint32_t w, uint32_t up, uint32_t& even, 
   odd = mul_bf16x2(((w >> 4) & 0x07f007f0u) | (w & 0x80008000u), up);
 }
 
+// The same with the bytes in order, two at a time: each byte under its own sign, which prmt spreads out,
+// moved up by four bits.
+__device__ __forceinline__ void widen4_in_order(uint32_t w, uint32_t up, uint32_t& lo, uint32_t& hi) {
+  uint32_t a, b;
+  asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(a) : "r"(w));
+  asm("prmt.b32 %0, %1, 0, 0xb3a2;" : "=r"(b) : "r"(w));
+  lo = mul_bf16x2((a << 4) & 0x87f087f0u, up);
+  hi = mul_bf16x2((b << 4) & 0x87f087f0u, up);
+}
+
 // `up` of a scale given as bf16 bits (at most kScaleMost)
 __device__ __forceinline__ uint32_t widen_factor(uint32_t scale) {
   return (min(scale, kScaleMost) + (120u << 7)) * 0x10001u;

@@ -22,13 +22,14 @@
 // Over all 576 dims that would move a weight by 1.5e-6 of itself; so the first five atoms and the
 // last four have an accumulator each (7e-7), added up in the epilogue.
 //
-// Warp-specialised CTA, 704 threads:
-//   warps 0-3   epilogue, one key per thread
-//   warp 4      in the first CTA the single-thread UMMA issuer; owns TMEM: two buffers of two
-//               accumulators of 128 columns
-//   warp 5      Q by TMA
-//   warps 6-21  rows, a quarter of a key's atom per thread: cp.async, bf16 into the operand's place, e4m3
-//               into a ring of raw atoms, then widened to bf16, exactly
+// Warp-specialised CTA, 896 threads:
+//   warps 0-7    epilogue, one key per thread: warps 0-3 the first 64 pairs, 4-7 the others
+//   warp 8       in the first CTA the single-thread UMMA issuer; owns TMEM: two buffers of two
+//                accumulators of 128 columns
+//   warp 9       Q by TMA
+//   warp 10      the pairs' lse and limits, a unit ahead
+//   warps 12-27  rows, a quarter of a key's atom per thread: cp.async, bf16 into the operand's place, e4m3
+//                into a ring of raw atoms, then widened to bf16, exactly
 
 #include <mutex>
 
@@ -43,11 +44,13 @@ constexpr int kDc = 512, kDr = 64, kD = kDc + kDr;
 constexpr int kKeys = 128, kTile = 2 * kKeys;   // keys of a CTA and of a tile
 constexpr int kPairs = 128;              // pairs at a time
 constexpr int kAtoms = kD / 64;
+constexpr int kGroup = 3, kGroups = kAtoms / kGroup;   // atoms that are handed over together
 constexpr int kFirstAtoms = 5;           // atoms of the first accumulator
 constexpr uint32_t kKeyAtom = kKeys * 128, kQueryAtom = kPairs / 2 * 128;
 constexpr uint32_t kRawAtom = kKeys * 64;   // of codes; one of positional dims is two
 constexpr int kRawSteps = 10;            // raw atoms of a tile: eight of codes, two of positional dims
-constexpr int kIssueWarp = 4, kQueryWarp = 5, kGatherWarp0 = 6, kGatherWarps = 16;
+constexpr int kEpilogueWarps = 8;
+constexpr int kIssueWarp = 8, kQueryWarp = 9, kStageWarp = 10, kGatherWarp0 = 12, kGatherWarps = 16;
 constexpr int kGatherThreads = 32 * kGatherWarps;
 constexpr int kThreads = 32 * (kGatherWarp0 + kGatherWarps);
 constexpr int kMaxClusters = 128;
@@ -56,14 +59,14 @@ constexpr int kErrPage = DSA_STAGE_EVICT | DSA_DEVERR_BAD_PAGE;
 constexpr int kErrTime = DSA_STAGE_EVICT | DSA_DEVERR_TIMEOUT;
 static_assert(kGatherThreads == 4 * kKeys, "a quarter of a key's atom per thread");
 
-// 216 KB in 27 pieces of 8 KB: atoms of rows, atoms of Q, raw atoms
+// 224 KB in 28 pieces of 8 KB: groups of atoms of rows, groups of atoms of Q, raw atoms
 template <bool FP8, bool MULTI>
 struct Layout {
-  static constexpr int kKeySlots = MULTI || !FP8 ? kAtoms : 5;
-  static constexpr int kQuerySlots = MULTI && FP8 ? 5 : kAtoms;
-  static constexpr int kRawSlots = FP8 ? (MULTI ? 4 : 8) : 0;
-  static constexpr uint32_t kQueryOff = kKeySlots * kKeyAtom;
-  static constexpr uint32_t kRawOff = kQueryOff + kQuerySlots * kQueryAtom;
+  static constexpr int kKeySlots = MULTI || !FP8 ? kGroups : 2;
+  static constexpr int kQuerySlots = MULTI && FP8 ? 2 : kGroups;
+  static constexpr int kRawSlots = FP8 ? (MULTI ? 4 : 7) : 0;
+  static constexpr uint32_t kQueryOff = kKeySlots * kGroup * kKeyAtom;
+  static constexpr uint32_t kRawOff = kQueryOff + kQuerySlots * kGroup * kQueryAtom;
   static constexpr uint32_t kTailOff = kRawOff + kRawSlots * kRawAtom;
 };
 
@@ -71,12 +74,13 @@ struct Tail {
   float nlse[2][kPairs];     // -lse of the pairs
   int lim[2][kPairs];        // positions below it are seen by the pair; a pair that adds nothing: none
   int group_lim[2][4];       // the least of 32 pairs
-  uint32_t valid[4][kGatherWarps];   // the tile's keys that are there: four bits a key
-  uint64_t k_full[kAtoms], k_empty[kAtoms], q_full[kAtoms], q_empty[kAtoms];
-  uint64_t d_full[2], d_empty[2], valid_full[4], staged, drain;
+  uint32_t valid[3][kGatherWarps];   // the tile's keys that are there: four bits a key
+  float other[kKeys];        // the sums of the second 64 pairs
+  uint64_t k_full[kGroups], k_empty[kGroups], q_full[kGroups], q_empty[kGroups];
+  uint64_t d_full[2], d_empty[2], valid_full[3], staged_full[2], staged_empty[2], other_full, other_empty;
+  uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
-  long long sums[kThreads / 32];
   // this cluster's range: its first item and the first unit of it here, and how many units
   int item0;
   long long first, count;
@@ -113,6 +117,7 @@ __device__ __forceinline__ int item_tiles(const Params& p, int item) {
 template <bool MULTI>
 __device__ __forceinline__ void my_units(const Params& p, Tail* tail) {
   const long long per_tile = MULTI ? p.nts : 1;
+  long long* sums = reinterpret_cast<long long*>(tail->nlse);   // not in use yet
   long long total, before = 0, s = 0;
   int i0 = 0, i1 = 0;   // this thread's items
   if (p.a.idx) {
@@ -129,12 +134,12 @@ __device__ __forceinline__ void my_units(const Params& p, Tail* tail) {
       const long long v = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += v;
     }
-    if (lane == 31) tail->sums[warp] = incl;
+    if (lane == 31) sums[warp] = incl;
     __syncthreads();
     total = 0;
     for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += tail->sums[w];
-      total += tail->sums[w];
+      if (w < warp) before += sums[w];
+      total += sums[w];
     }
     before += incl - s;
   }
@@ -316,7 +321,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     return;
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kAtoms; ++i) {
+    for (int i = 0; i < kGroups; ++i) {
       mbar_init(&tail->k_full[i], 2 * kGatherWarps);   // of the first CTA: both CTAs' rows
       mbar_init(&tail->k_empty[i], 1);
       mbar_init(&tail->q_full[i], 1);                  // of the first CTA: both CTAs' halves
@@ -324,10 +329,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tail->d_full[i], 1);
-      mbar_init(&tail->d_empty[i], 8);                 // of the first CTA: both CTAs' epilogue warps
+      mbar_init(&tail->d_empty[i], 2 * kEpilogueWarps);   // of the first CTA: both CTAs' epilogue warps
+      mbar_init(&tail->staged_full[i], 1);
+      mbar_init(&tail->staged_empty[i], kEpilogueWarps);
     }
-    for (int i = 0; i < 4; ++i) mbar_init(&tail->valid_full[i], kGatherWarps);
-    mbar_init(&tail->staged, kPairs);
+    for (int i = 0; i < 3; ++i) mbar_init(&tail->valid_full[i], kGatherWarps);
+    mbar_init(&tail->other_full, 4);
+    mbar_init(&tail->other_empty, 4);
     mbar_init(&tail->drain, 1);
     tail->abort_flag = 0;
     tail->count = 0;
@@ -348,11 +356,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tail->tmem_base;
   const long long n = tail->count;   // the same in both CTAs
 
-  if (warp < 4) {
+  const int pairs = a.idx ? a.H : a.Sq * a.H;   // of an item
+  if (warp < kEpilogueWarps) {
     // ================================================================ epilogue
     if (!a.idx) {
       // zeros behind the sequences' ends, shared out among the CTAs
-      for (int b = warp; b < a.B; b += 4) {
+      for (int b = warp; b < a.B; b += kEpilogueWarps) {
         const int len = seq_len(a, b, blockIdx.x == 0 && lane == 0), end = min(len, a.n);
         const long long room = a.n - end;
         const int z0 = end + static_cast<int>(room * blockIdx.x / gridDim.x);
@@ -360,89 +369,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int j = z0 + lane; j < z1; j += 32) a.mass[static_cast<long long>(b) * a.n + j] = 0.f;
       }
     }
-    const int me = threadIdx.x;   // TMEM lane
+    const int me = threadIdx.x & 127;    // TMEM lane
+    const int half = warp >> 2;          // pairs 64 half, ...
     const int key = rank * kKeys + me;   // of the tile
-    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
-    const int pairs = a.idx ? a.H : a.Sq * a.H;   // of an item
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const float2 scale2 = make_float2(a.scale, a.scale);
     const float2 log2e = make_float2(1.4426950408889634f, 1.4426950408889634f);
-    const uint32_t d_empty[2] = {first_cta(&tail->d_empty[0]), first_cta(&tail->d_empty[1])};
+    const uint32_t d_empty0 = first_cta(&tail->d_empty[0]);
     if (n > 0) {
       Cursor<MULTI> c(p, tail);
       int cur_item = -1, len = 0;
       float sum = 0.f;
       bool whole = false;        // the tile's first pairs were here
-      int tiles_done = 0;        // tiles whose flags have been taken
-      int stages = 0;            // times that pairs' lse and limits have been written
+      Ring<3> vr;                // tiles whose flags have been taken
+      Ring<2> sr;                // sets of lse and limits
+      uint32_t done = 0;         // tiles that are done
       bool there = false;
 #pragma unroll 1
       for (long long u = 0; u < n; ++u) {
         const int buf = static_cast<int>(u) & 1;
         const uint32_t par = static_cast<uint32_t>(u >> 1) & 1u;
-        const bool fresh_item = c.item != cur_item;
-        if (fresh_item) {
+        if (c.item != cur_item) {
           cur_item = c.item;
           len = seq_len(a, a.idx ? c.item / a.Sq : c.item, false);
         }
-        // The pairs' lse and limits: with several columns per tile they change with each unit. (The
-        // buffer was last read two stages ago, before every thread's arrival at the last one.)
-        if (MULTI || fresh_item) {
-          const int w = stages & 1;
-          const int pr = c.nt * kPairs + me;
-          float v = 0.f;
-          int lim = kNone;
-          if (pr < pairs) {
-            const long long row = static_cast<long long>(c.item) * pairs + pr;
-            const float lse = __ldg(a.lse + row);
-            const int token = a.idx ? c.item % a.Sq : pr / a.H;
-            v = -lse;
-            if (lse != -INFINITY) lim = len - a.Sq + token + 1;
-          }
-          tail->nlse[w][me] = v;
-          tail->lim[w][me] = lim;
-          lim = __reduce_min_sync(0xffffffffu, lim);
-          if (lane == 0) tail->group_lim[w][warp] = lim;
-          __syncwarp();
-          mbar_arrive(&tail->staged);
-          if (!__all_sync(0xffffffffu, mbar_wait(&tail->staged, w, abort_flag, err, kErrTime))) break;
-          ++stages;
-        }
-        const int sb = (stages & 1) ^ 1;
+        bool ok = true;
         if (u == 0 || c.nt == 0) {
           sum = 0.f;
           whole = c.nt == 0;
-          const int vb = tiles_done & 3;
-          if (!__all_sync(0xffffffffu, mbar_wait(&tail->valid_full[vb], (tiles_done >> 2) & 1,
-                                                 abort_flag, err, kErrTime)))
-            break;
-          there = (tail->valid[vb][me >> 3] >> (4 * (me & 7)) & 1u) != 0;
-          ++tiles_done;
+          ok = mbar_wait(&tail->valid_full[vr.slot], vr.round, abort_flag, err, kErrTime);
         }
-        if (!__all_sync(0xffffffffu, mbar_wait(&tail->d_full[buf], par, abort_flag, err, kErrTime)))
-          break;
+        ok = ok && mbar_wait(&tail->staged_full[sr.slot], sr.round, abort_flag, err, kErrTime);
+        ok = ok && mbar_wait(&tail->d_full[buf], par, abort_flag, err, kErrTime);
+        if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        const long long j = static_cast<long long>(c.tile) * kTile + key;
+        if (u == 0 || c.nt == 0) {
+          there = (tail->valid[vr.slot][me >> 3] >> (4 * (me & 7)) & 1u) != 0;
+          vr.next();
+        }
+        const int j0 = c.tile * kTile;   // (below 2^31: n and k are)
         // lists: a key that its token does not see is not there
-        const int last =
-            a.idx ? kNone
-                  : static_cast<int>(min(static_cast<long long>(c.tile + 1) * kTile, static_cast<long long>(len)));
+        const int last = a.idx ? kNone : min(j0 + (kTile - 1), len - 1) + 1;
         float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        float some = 0.f;
         const uint32_t d = tmem + lane_off + buf * 2 * kPairs;
+        const int groups = min(4 * half + 4, (pairs - c.nt * kPairs + 15) / 16);
+        uint32_t s0[16], s1[16];
+        if (4 * half < groups) {
+          tmem_ld_16(d + half * 64, s0);
+          tmem_ld_16(d + kPairs + half * 64, s1);
+        }
 #pragma unroll 1
-        for (int g = 0; g < kPairs / 16; ++g) {
-          if (c.nt * kPairs + g * 16 >= pairs) break;
-          uint32_t s0[16], s1[16];
-          tmem_ld_16(d + g * 16, s0);
-          tmem_ld_16(d + kPairs + g * 16, s1);
+        for (int g = 4 * half; g < groups; ++g) {
           tmem_ld_wait();
           float2 s[8];
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             s[q] = add2(make_float2(__uint_as_float(s0[2 * q]), __uint_as_float(s0[2 * q + 1])),
                         make_float2(__uint_as_float(s1[2 * q]), __uint_as_float(s1[2 * q + 1])));
-          const float4* nl = reinterpret_cast<const float4*>(&tail->nlse[sb][g * 16]);
-          const int least = tail->group_lim[sb][g >> 1];
+          if (g + 1 < groups) {   // on their way while these are worked on
+            tmem_ld_16(d + (g + 1) * 16, s0);
+            tmem_ld_16(d + kPairs + (g + 1) * 16, s1);
+          }
+          const float4* nl = reinterpret_cast<const float4*>(&tail->nlse[sr.slot][g * 16]);
+          const int least = tail->group_lim[sr.slot][g >> 1];
           if (least != kNone && least >= last) {
             // every pair of the group sees every key of the tile
 #pragma unroll
@@ -458,33 +447,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               acc[1] = add2(acc[1], make_float2(ex2f(y.x), ex2f(y.y)));
             }
           } else {
+            const int* lims = &tail->lim[sr.slot][g * 16];
 #pragma unroll
             for (int q = 0; q < 16; ++q) {
-              const int lim = tail->lim[sb][g * 16 + q];
-              const float x = fmaf(q & 1 ? s[q / 2].y : s[q / 2].x, a.scale, tail->nlse[sb][g * 16 + q]);
-              if (lim != kNone && (a.idx || j < lim)) some += ex2f(x * log2e.x);
+              const float v = tail->nlse[sr.slot][g * 16 + q];
+              const float x = ex2f(fmaf(q & 1 ? s[q / 2].y : s[q / 2].x, a.scale, v) * log2e.x);
+              const bool sees = lims[q] != kNone && (a.idx || j0 + key < lims[q]);
+              (q & 1 ? acc[0].y : acc[0].x) += sees ? x : 0.f;
             }
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_first_cta(d_empty[buf]);
-        sum += ((acc[0].x + acc[0].y) + (acc[1].x + acc[1].y)) + some;
-        if (!MULTI || c.nt == p.nts - 1 || u == n - 1) {
-          if (!there) sum = 0.f;
-          if (a.idx) {
-            if (j < a.k) p.w[static_cast<long long>(c.item) * a.k + j] = sum;
-          } else if (whole && (!MULTI || c.nt == p.nts - 1)) {
-            if (j < min(len, a.n)) {
-              const long long at = static_cast<long long>(c.item) * a.n + j;
-              a.mass[at] = a.prev ? fmaf(a.decay, a.prev[at], sum) : sum;
-            }
-          } else {
-            // part 0: a tile begun in front of the range; part 1: one that goes on behind it
-            p.part[(2ll * cluster + (whole ? 1 : 0)) * kTile + key] = sum;
-          }
+        const bool end = !MULTI || c.nt == p.nts - 1 || u == n - 1;   // of the tile, here
+        if (lane == 0) {
+          arrive_first_cta(d_empty0 + buf * 8);
+          if (MULTI || u == n - 1 || c.tile == c.tiles - 1) mbar_arrive(&tail->staged_empty[sr.slot]);
         }
-        if (MULTI && u == n - 1 && key == 0) {
+        if (MULTI || u == n - 1 || c.tile == c.tiles - 1) sr.next();
+        sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+        if (end) {
+          // the second half's sums go to the first half's threads
+          if (half == 1) {
+            ok = mbar_wait(&tail->other_empty, (done & 1u) ^ 1u, abort_flag, err, kErrTime);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tail->other[me] = sum;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tail->other_full);
+          } else {
+            ok = mbar_wait(&tail->other_full, done & 1u, abort_flag, err, kErrTime);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            sum = there ? sum + tail->other[me] : 0.f;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tail->other_empty);
+            if (a.idx) {
+              if (j0 + key < a.k) p.w[static_cast<long long>(c.item) * a.k + j0 + key] = sum;
+            } else if (whole && (!MULTI || c.nt == p.nts - 1)) {
+              if (j0 + key < min(len, a.n)) {
+                const long long at = static_cast<long long>(c.item) * a.n + j0 + key;
+                a.mass[at] = a.prev ? fmaf(a.decay, a.prev[at], sum) : sum;
+              }
+            } else {
+              // part 0: a tile begun in front of the range; part 1: one that goes on behind it
+              p.part[(2ll * cluster + (whole ? 1 : 0)) * kTile + key] = sum;
+            }
+          }
+          ++done;
+        }
+        if (MULTI && u == n - 1 && half == 0 && key == 0) {
           const int left = p.nts - 1 - c.nt;
           const int each = static_cast<int>(min(n, 0x40000000ll));   // this range is not the last one
           p.joins[cluster] = whole && left > 0 ? make_int4(c.item, c.tile, cluster + (left + each - 1) / each, 0)
@@ -492,8 +502,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         c.next(p);
       }
-    } else if (MULTI && key == 0) {
+    } else if (MULTI && half == 0 && key == 0) {
       p.joins[cluster] = make_int4(-1, 0, 0, 0);
+    }
+  } else if (warp == kStageWarp) {
+    // ================================================================ the pairs' lse and limits
+    if (n > 0) {
+      Cursor<MULTI> c(p, tail);
+      Ring<2> sr;
+      int cur_item = -1, len = 0;
+#pragma unroll 1
+      for (long long u = 0; u < n; ++u) {
+        if (MULTI || c.item != cur_item) {
+          if (c.item != cur_item) {
+            cur_item = c.item;
+            len = seq_len(a, a.idx ? c.item / a.Sq : c.item, false);
+          }
+          float lse[kPairs / 32];
+#pragma unroll
+          for (int i = 0; i < kPairs / 32; ++i) {
+            const int pr = c.nt * kPairs + i * 32 + lane;
+            lse[i] = pr < pairs ? __ldg(a.lse + static_cast<long long>(c.item) * pairs + pr) : -INFINITY;
+          }
+          if (!__all_sync(0xffffffffu, mbar_wait(&tail->staged_empty[sr.slot], sr.round ^ 1u, abort_flag,
+                                                 err, kErrTime)))
+            break;
+#pragma unroll
+          for (int i = 0; i < kPairs / 32; ++i) {
+            const int pr = c.nt * kPairs + i * 32 + lane;
+            // a pair without a key, and one that is not there, adds nothing
+            const int lim = lse[i] == -INFINITY ? kNone
+                                                : len - a.Sq + (a.idx ? c.item % a.Sq : pr / a.H) + 1;
+            tail->nlse[sr.slot][i * 32 + lane] = -lse[i];
+            tail->lim[sr.slot][i * 32 + lane] = lim;
+            const int least = __reduce_min_sync(0xffffffffu, lim);
+            if (lane == 0) tail->group_lim[sr.slot][i] = least;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tail->staged_full[sr.slot]);
+          sr.next();
+        }
+        c.next(p);
+      }
     }
   } else if (warp == kIssueWarp) {
     // ================================================================ UMMA issuer
@@ -513,21 +563,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool last = u == n - 1 || (MULTI ? c.nt == p.nts - 1 : c.tile == c.tiles - 1);
         ok = mbar_wait(&tail->d_empty[buf], (static_cast<uint32_t>(u >> 1) & 1u) ^ 1u, abort_flag, err,
                        kErrTime);
-#pragma unroll 1
-        for (int d = 0; ok && d < kAtoms; ++d) {
-          if (!MULTI || first)
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          if (ok && (!MULTI || first))
             ok = mbar_wait(&tail->k_full[kr.slot], kr.round, abort_flag, err, kErrTime);
           if (ok && (MULTI || first))
             ok = mbar_wait(&tail->q_full[qr.slot], qr.round, abort_flag, err, kErrTime);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t kd = umma_desc_adv(k0, kr.slot * kKeyAtom);
-          const uint64_t qd = umma_desc_adv(q0, qr.slot * kQueryAtom);
-          const uint32_t dst = tmem + (2 * buf + (d >= kFirstAtoms ? 1 : 0)) * kPairs;
+          const uint64_t kd = umma_desc_adv(k0, kr.slot * (kGroup * kKeyAtom));
+          const uint64_t qd = umma_desc_adv(q0, qr.slot * (kGroup * kQueryAtom));
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma2_bf16(dst, umma_desc_adv(kd, kk * 32), umma_desc_adv(qd, kk * 32), idesc,
-                       (d == 0 || d == kFirstAtoms) && kk == 0 ? 0u : 1u);
+          for (int i = 0; i < kGroup; ++i) {
+            const int d = g * kGroup + i;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma2_bf16(tmem + (2 * buf + (d >= kFirstAtoms ? 1 : 0)) * kPairs,
+                         umma_desc_adv(kd, i * kKeyAtom + kk * 32),
+                         umma_desc_adv(qd, i * kQueryAtom + kk * 32), idesc,
+                         (d == 0 || d == kFirstAtoms) && kk == 0 ? 0u : 1u);
+          }
           if (!MULTI || last) umma2_commit(&tail->k_empty[kr.slot]);
           if (MULTI || last) umma2_commit(&tail->q_empty[qr.slot]);
           kr.next();
@@ -556,7 +611,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ================================================================ Q
     if (lane == 0 && n > 0) {
       tma_prefetch_desc(&qmap);
-      const int pairs = a.idx ? a.H : a.Sq * a.H;
       const uint32_t full0 = first_cta(&tail->q_full[0]);
       Cursor<MULTI> c(p, tail);
       Ring<kQuerySlots> qr;
@@ -566,12 +620,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (MULTI || u == 0 || c.tile == 0) {
           const int row = c.item * pairs + c.nt * kPairs + rank * (p.box / 2);
 #pragma unroll 1
-          for (int d = 0; d < kAtoms; ++d) {
+          for (int g = 0; g < kGroups; ++g) {
             ok = mbar_wait(&tail->q_empty[qr.slot], qr.round ^ 1u, abort_flag, err, kErrTime);
             if (!ok) break;
             // (the second CTA's half may come in front of this: its bytes are only taken off)
-            if (rank == 0) mbar_arrive_expect_tx(&tail->q_full[qr.slot], p.box * 128);
-            tma2_load_2d(qsmem + qr.slot * kQueryAtom, &qmap, full0 + qr.slot * 8, d * 64, row);
+            if (rank == 0) mbar_arrive_expect_tx(&tail->q_full[qr.slot], kGroup * p.box * 128);
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i)
+              tma2_load_2d(qsmem + (qr.slot * kGroup + i) * kQueryAtom, &qmap, full0 + qr.slot * 8,
+                           (g * kGroup + i) * 64, row);
             qr.next();
           }
         }
@@ -585,7 +642,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (n > 0) {
+  } else if (warp >= kGatherWarp0 && n > 0) {
     // ================================================================ rows
     const int t = threadIdx.x - 32 * kGatherWarp0, key = t >> 2, sub = t & 3;
     const long long row_bytes = FP8 ? kDc + 16 + 2 * kDr : 2 * kD;
@@ -647,8 +704,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto tell_valid = [&](int tiles, bool there) {
       const uint32_t bits = __ballot_sync(0xffffffffu, there);
       if (lane == 0) {
-        tail->valid[tiles & 3][warp - kGatherWarp0] = bits;
-        mbar_arrive(&tail->valid_full[tiles & 3]);
+        tail->valid[tiles % 3][warp - kGatherWarp0] = bits;
+        mbar_arrive(&tail->valid_full[tiles % 3]);
       }
     };
     // A warp's part of an atom is written: one arrival for it. (One per thread, 512 an atom, is level:
@@ -661,11 +718,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     const uint32_t at = key * 128;
     if constexpr (!FP8) {
-      // copies of up to kLag atoms behind the newest are on their way
-      constexpr int kLag = 6;   // fewer than the ring's atoms: a slot comes free after its atom is told of
-      static_assert(kLag < kKeySlots, "a slot comes free");
+      // copies of a group behind the newest are on their way
       Ring<kKeySlots> landed;
-      int flying = 0;
+      bool flying = false;
       const uint8_t* row = row_of(page_of(look()));
       bool ok = true;
 #pragma unroll 1
@@ -673,35 +728,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         advance();
         const Found f = look();   // of the next tile
         Paged q = {-1, -1};
-        const uint8_t* src = row ? row : a.cache;
+        const uint8_t* src = (row ? row : a.cache) + sub * 16;
         const uint32_t bytes = row ? 16u : 0u;
-#pragma unroll 1
-        for (int d = 0; d < kAtoms; ++d) {
-          ok = wait_empty();
+        const uint32_t lo = at + ((sub ^ (key & 7)) << 4), hi = at + (((sub + 4) ^ (key & 7)) << 4);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          ok = ok && wait_empty();
           if (!ok) break;
-          if (d == 0) tell_valid(tiles, row != nullptr);
-          const uint32_t dst = base + kr.slot * kKeyAtom + at;
-          cp_async_16(dst + ((sub ^ (key & 7)) << 4), src + d * 128 + sub * 16, bytes);
-          cp_async_16(dst + (((sub + 4) ^ (key & 7)) << 4), src + d * 128 + 64 + sub * 16, bytes);
+          if (g == 0) tell_valid(tiles, row != nullptr);
+          const uint32_t dst = base + kr.slot * (kGroup * kKeyAtom);
+#pragma unroll
+          for (int i = 0; i < kGroup; ++i) {
+            cp_async_16(dst + i * kKeyAtom + lo, src + (g * kGroup + i) * 128, bytes);
+            cp_async_16(dst + i * kKeyAtom + hi, src + (g * kGroup + i) * 128 + 64, bytes);
+          }
           cp_async_commit();
           kr.next();
-          if (flying < kLag) {
-            ++flying;
-          } else {
-            cp_async_wait<kLag>();
+          if (flying) {
+            cp_async_wait<1>();
             tell_full(landed.slot);
             landed.next();
           }
-          if (d == 3) q = page_of(f);
+          flying = true;
+          if (g == 0) q = page_of(f);
         }
         row = row_of(q);
         // the last ones; a tile that stays is waited for as a whole before its slots come free again
-        if (MULTI || !more()) {
+        if (ok && (MULTI || !more())) {
           cp_async_wait<0>();
-          for (; ok && flying > 0; --flying) {
-            tell_full(landed.slot);
-            landed.next();
-          }
+          tell_full(landed.slot);
+          landed.next();
+          flying = false;
         }
       }
       cp_async_wait<0>();
@@ -709,103 +766,92 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // Raw ring: a thread copies in what it widens itself, step by step: eight pieces of 16 codes, two of
       // positional dims, kAhead steps ahead. The scales come by way of a register, a tile ahead.
       constexpr int kAhead = L::kRawSlots;
+      static_assert(kAhead < kRawSteps && kAhead >= 4, "one tile's steps, and a group's");
       const uint32_t raw0 = base + L::kRawOff + t * 16;
-      auto fetch = [&](const uint8_t* row, int step, int slot) {
-        const int from = step < 8 ? step * 64 : kDc + 16 + (step - 8) * 64;
-        cp_async_16(raw0 + slot * kRawAtom, (row ? row : a.cache) + from + sub * 16, row ? 16u : 0u);
+      struct Source {
+        const uint8_t* at;
+        uint32_t bytes;
       };
-      auto scales_of = [&](const uint8_t* row) {
-        return row ? __ldg(reinterpret_cast<const uint4*>(row + kDc)) : make_uint4(0, 0, 0, 0);
+      auto source = [&](const uint8_t* row) {
+        return Source{(row ? row : a.cache) + sub * 16, row ? 16u : 0u};
       };
-      const uint8_t* row = row_of(page_of(look()));   // of the tile that is fetched
-      bool there = row != nullptr;                    // of the tile that is widened
+      auto fetch = [&](const Source& from, int step, uint32_t dst) {
+        cp_async_16(dst, from.at + (step < 8 ? step * 64 : kDc + 16 + (step - 8) * 64), from.bytes);
+        cp_async_commit();
+      };
+      auto scales_of = [&](const Source& from) {
+        return from.bytes ? __ldg(reinterpret_cast<const uint4*>(from.at - sub * 16 + kDc))
+                          : make_uint4(0, 0, 0, 0);
+      };
+      Source row = source(row_of(page_of(look())));   // of the tile that is widened
       long long togo = left;                          // units of it and of those behind it
       uint4 scale = scales_of(row);
-      // the next two tiles
       advance();
-      const uint8_t* next = row_of(page_of(look()));
+      Source next = source(row_of(page_of(look())));
       if (more()) advance();
-      Found f = look();
-      Paged q = {-1, -1};
-      int fstep = 0;    // the next step to be fetched
-      for (int i = 0; i < kAhead; ++i) {   // (no more than a tile's steps)
-        fetch(row, fstep, i);
-        cp_async_commit();
-        ++fstep;
-      }
-      static_assert(kAhead < kRawSteps, "the first fetches are of one tile");
-      int slot = 0;
+      Found f = look();                               // the tile two ahead
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) fetch(row, i, raw0 + i * kRawAtom);
+      uint32_t raw = raw0;
       bool ok = true;
 #pragma unroll 1
       for (int tiles = 0; ok && togo > 0; ++tiles, togo -= MULTI ? p.nts : 1) {
-        uint4 next_scale = scale;
-        const bool there_now = there;
-        // one step: its piece out of the ring, and the piece kAhead steps on into the same place
-        auto step = [&]() {
-          cp_async_wait<kAhead - 1>();
+        const uint4 next_scale = scales_of(next);
+        Paged q = {-1, -1};
+        // step i: its piece out of the ring, and the piece kAhead steps on into the same place
+        auto step = [&](int i) {
           uint4 x;
           asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                       : "r"(raw0 + slot * kRawAtom)
+                       : "r"(raw)
                        : "memory");
+          fetch(i + kAhead < kRawSteps ? row : next, (i + kAhead) % kRawSteps, raw);
+          raw = raw == raw0 + (kAhead - 1) * kRawAtom ? raw0 : raw + kRawAtom;
           return x;
         };
-        auto refill = [&]() {
-          if (fstep == kRawSteps) {   // on to the next tile
-            fstep = 0;
-            row = next;
-            there = row != nullptr;
-            next_scale = scales_of(row);
-          }
-          fetch(row, fstep, slot);
-          cp_async_commit();
-          ++fstep;
-          slot = slot + 1 == kAhead ? 0 : slot + 1;
-        };
-#pragma unroll 1
-        for (int d = 0; d < 8; ++d) {
-          const uint4 x = step();
-          const uint32_t e = (d < 2 ? scale.x : d < 4 ? scale.y : d < 6 ? scale.z : scale.w) >> 16;
-          const uint32_t up = widen_factor(e);
-          uint4 w0, w1;
-          // (bytes 0 2 1 3, so that they come out in order)
-          widen4(__byte_perm(x.x, 0, 0x3120), up, w0.x, w0.y);
-          widen4(__byte_perm(x.y, 0, 0x3120), up, w0.z, w0.w);
-          widen4(__byte_perm(x.z, 0, 0x3120), up, w1.x, w1.y);
-          widen4(__byte_perm(x.w, 0, 0x3120), up, w1.z, w1.w);
-          if (e > kScaleMost) {   // a scale of more than 2^7, or of NaN
-            const uint32_t rest = widen_rest(e);
-            w0 = make_uint4(mul_bf16x2(w0.x, rest), mul_bf16x2(w0.y, rest), mul_bf16x2(w0.z, rest),
-                            mul_bf16x2(w0.w, rest));
-            w1 = make_uint4(mul_bf16x2(w1.x, rest), mul_bf16x2(w1.y, rest), mul_bf16x2(w1.z, rest),
-                            mul_bf16x2(w1.w, rest));
-          }
-          refill();
-          ok = wait_empty();
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          uint4 x[kGroup + 1];
+          cp_async_wait<kAhead - (kGroup + 1)>();   // (one more than the first groups need)
+#pragma unroll
+          for (int i = 0; i < kGroup + (g == 2 ? 1 : 0); ++i) x[i] = step(g * kGroup + i);
+          ok = ok && wait_empty();
           if (!ok) break;
-          if (d == 0) tell_valid(tiles, there_now);
-          uint8_t* dst = smem + kr.slot * kKeyAtom + at;
-          *reinterpret_cast<uint4*>(dst + (((2 * sub) ^ (key & 7)) << 4)) = w0;
-          *reinterpret_cast<uint4*>(dst + (((2 * sub + 1) ^ (key & 7)) << 4)) = w1;
+          if (g == 0) tell_valid(tiles, row.bytes != 0);
+          uint8_t* dst = smem + kr.slot * (kGroup * kKeyAtom) + at;
+#pragma unroll
+          for (int i = 0; i < kGroup; ++i) {
+            const int d = g * kGroup + i;
+            if (d == 8) {
+              *reinterpret_cast<uint4*>(dst + i * kKeyAtom + ((sub ^ (key & 7)) << 4)) = x[i];
+              *reinterpret_cast<uint4*>(dst + i * kKeyAtom + (((sub + 4) ^ (key & 7)) << 4)) = x[i + 1];
+              continue;
+            }
+            const uint32_t e = (d < 2 ? scale.x : d < 4 ? scale.y : d < 6 ? scale.z : scale.w) >> 16;
+            const uint32_t up = widen_factor(e);
+            uint4 w0, w1;
+            widen4_in_order(x[i].x, up, w0.x, w0.y);
+            widen4_in_order(x[i].y, up, w0.z, w0.w);
+            widen4_in_order(x[i].z, up, w1.x, w1.y);
+            widen4_in_order(x[i].w, up, w1.z, w1.w);
+            if (e > kScaleMost) {   // a scale of more than 2^7, or of NaN
+              const uint32_t rest = widen_rest(e);
+              w0 = make_uint4(mul_bf16x2(w0.x, rest), mul_bf16x2(w0.y, rest), mul_bf16x2(w0.z, rest),
+                              mul_bf16x2(w0.w, rest));
+              w1 = make_uint4(mul_bf16x2(w1.x, rest), mul_bf16x2(w1.y, rest), mul_bf16x2(w1.z, rest),
+                              mul_bf16x2(w1.w, rest));
+            }
+            *reinterpret_cast<uint4*>(dst + i * kKeyAtom + (((2 * sub) ^ (key & 7)) << 4)) = w0;
+            *reinterpret_cast<uint4*>(dst + i * kKeyAtom + (((2 * sub + 1) ^ (key & 7)) << 4)) = w1;
+          }
           tell_full(kr.slot);
           kr.next();
-          // the tile two ahead, between the fetches: its page, then its row
-          if (d == 4) q = page_of(f);
+          if (g == 1) q = page_of(f);
         }
         if (!ok) break;
-        const uint4 r0 = step();
-        refill();
-        const uint4 r1 = step();
-        refill();
-        ok = wait_empty();
-        if (!ok) break;
-        uint8_t* dst = smem + kr.slot * kKeyAtom + at;
-        *reinterpret_cast<uint4*>(dst + ((sub ^ (key & 7)) << 4)) = r0;
-        *reinterpret_cast<uint4*>(dst + (((sub + 4) ^ (key & 7)) << 4)) = r1;
-        tell_full(kr.slot);
-        kr.next();
+        row = next;
         scale = next_scale;
-        next = row_of(q);
+        next = source(row_of(q));
         if (more()) advance();
         f = look();
       }
