@@ -274,13 +274,10 @@ __device__ __forceinline__ void umma2_commit(uint64_t* bar) {
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld_16(uint32_t taddr, uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_ld_8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
       : "r"(taddr)
       : "memory");
 }
@@ -412,30 +409,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int last = a.idx ? kNone : min(j0 + (kTile - 1), len - 1) + 1;
         float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         const uint32_t d = tmem + lane_off + buf * 2 * kPairs;
-        const int groups = min(4 * half + 4, (pairs - c.nt * kPairs + 15) / 16);
-        uint32_t s0[16], s1[16];
-        if (4 * half < groups) {
-          tmem_ld_16(d + half * 64, s0);
-          tmem_ld_16(d + kPairs + half * 64, s1);
-        }
+        // eight pairs at a time, the next ones on their way (sixteen would not fit the registers)
+        const int c1 = min(64 * half + 64, pairs - c.nt * kPairs);
+        uint32_t s0[8], s1[8];
+        tmem_ld_8(d + half * 64, s0);
+        tmem_ld_8(d + kPairs + half * 64, s1);
 #pragma unroll 1
-        for (int g = 4 * half; g < groups; ++g) {
+        for (int c0 = 64 * half; c0 < c1; c0 += 8) {
           tmem_ld_wait();
-          float2 s[8];
+          float2 s[4];
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
+          for (int q = 0; q < 4; ++q)
             s[q] = add2(make_float2(__uint_as_float(s0[2 * q]), __uint_as_float(s0[2 * q + 1])),
                         make_float2(__uint_as_float(s1[2 * q]), __uint_as_float(s1[2 * q + 1])));
-          if (g + 1 < groups) {   // on their way while these are worked on
-            tmem_ld_16(d + (g + 1) * 16, s0);
-            tmem_ld_16(d + kPairs + (g + 1) * 16, s1);
-          }
-          const float4* nl = reinterpret_cast<const float4*>(&tail->nlse[sr.slot][g * 16]);
-          const int least = tail->group_lim[sr.slot][g >> 1];
+          const int next = (c0 + 8) & (kPairs - 1);   // (behind the last one: read, not used)
+          tmem_ld_8(d + next, s0);
+          tmem_ld_8(d + kPairs + next, s1);
+          const float4* nl = reinterpret_cast<const float4*>(&tail->nlse[sr.slot][c0]);
+          const int least = tail->group_lim[sr.slot][c0 >> 5];
           if (least != kNone && least >= last) {
             // every pair of the group sees every key of the tile
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
               const float4 v = nl[q];
               // the difference first, in one rounding: far from zero those of the products with
               // log2(e) would move the weight
@@ -447,16 +442,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               acc[1] = add2(acc[1], make_float2(ex2f(y.x), ex2f(y.y)));
             }
           } else {
-            const int* lims = &tail->lim[sr.slot][g * 16];
+            const int* lims = &tail->lim[sr.slot][c0];
 #pragma unroll
-            for (int q = 0; q < 16; ++q) {
-              const float v = tail->nlse[sr.slot][g * 16 + q];
+            for (int q = 0; q < 8; ++q) {
+              const float v = tail->nlse[sr.slot][c0 + q];
               const float x = ex2f(fmaf(q & 1 ? s[q / 2].y : s[q / 2].x, a.scale, v) * log2e.x);
               const bool sees = lims[q] != kNone && (a.idx || j0 + key < lims[q]);
               (q & 1 ? acc[0].y : acc[0].x) += sees ? x : 0.f;
             }
           }
         }
+        tmem_ld_wait();
         tc_fence_before();
         __syncwarp();
         const bool end = !MULTI || c.nt == p.nts - 1 || u == n - 1;   // of the tile, here
