@@ -396,6 +396,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           whole = c.nt == 0;
           ok = mbar_wait(&tail->valid_full[vr.slot], vr.round, abort_flag, err, kErrTime);
         }
+        // the earlier weight, on its way while the tile is
+        float before = 0.f;
+        if (half == 0 && a.prev && !a.idx && (!MULTI || c.nt == p.nts - 1) && c.tile * kTile + key < min(len, a.n))
+          before = a.prev[static_cast<long long>(c.item) * a.n + c.tile * kTile + key];
         ok = ok && mbar_wait(&tail->staged_full[sr.slot], sr.round, abort_flag, err, kErrTime);
         ok = ok && mbar_wait(&tail->d_full[buf], par, abort_flag, err, kErrTime);
         if (!__all_sync(0xffffffffu, ok)) break;
@@ -481,7 +485,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             } else if (whole && (!MULTI || c.nt == p.nts - 1)) {
               if (j0 + key < min(len, a.n)) {
                 const long long at = static_cast<long long>(c.item) * a.n + j0 + key;
-                a.mass[at] = a.prev ? fmaf(a.decay, a.prev[at], sum) : sum;
+                a.mass[at] = fmaf(a.decay, before, sum);
               }
             } else {
               // part 0: a tile begun in front of the range; part 1: one that goes on behind it
