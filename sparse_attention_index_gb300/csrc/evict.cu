@@ -27,8 +27,6 @@ constexpr int kErrPage = DSA_STAGE_EVICT | DSA_DEVERR_BAD_PAGE;
 
 // ------------------------------------------------------------------ choosing
 
-constexpr int kKeepThreads = 1024;
-constexpr int kKeepWarps = kKeepThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMostHeld = 49152;   // weights that a CTA keeps in shared memory (192 KB)
 
@@ -41,19 +39,15 @@ struct KeepParams {
   int* err;
 };
 
-struct KeepTail {
-  int hist[3][kBins];      // one per digit, so that a barrier per digit is enough
-  int above[kKeepWarps], equal[kKeepWarps];   // of each warp's part
+struct __align__(16) KeepTail {
+  int hist[3][kBins];      // one per digit
+  int above[32], equal[32];   // of each warp's part
   int2 total;              // of the CTA
-  int sums[kKeepWarps];
-  int digit, left, exact;
+  int sums[32];
+  int shares[8];           // weights in each CTA's share of the bins
+  int4 found;              // the digit, what is left to take of its bin, whether that is all of it
 };
 
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -62,11 +56,31 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
-__device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
+// Shared memory of another CTA. (No memory clobber: the loads of one histogram from all CTAs are on their
+// way together; what they read is settled at the barrier in front of them, which no load passes.)
+__device__ __forceinline__ uint32_t of_cta(const void* p, uint32_t rank) {
   uint32_t a;
-  int v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return a;
+}
+__device__ __forceinline__ int4 ld_cluster4(uint32_t a) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void st_cluster(uint32_t a, int v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster4(uint32_t a, int4 v) {
+  asm volatile("st.shared::cluster.v4.s32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ int2 ld_cluster2(uint32_t a) {
+  int2 v;
+  asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
 
@@ -77,11 +91,13 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+template <int C, int kKeepThreads>   // CTAs of a cluster, threads of a CTA
 __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const KeepParams p) {
-  extern __shared__ uint32_t keys[];
+  extern __shared__ __align__(16) uint32_t keys[];
   __shared__ KeepTail s;
+  constexpr int kKeepWarps = kKeepThreads / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int C = cluster_size(), rank = cluster_rank(), b = blockIdx.x / C;
+  const int rank = C == 1 ? 0 : cluster_rank(), b = blockIdx.x / C;
   int len = __ldg(p.lens + b);
   if (len < 0 || len > p.n) {
     if (tid == 0) report_error(p.err, kErrPage);
@@ -110,15 +126,40 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const KeepParams p) 
   const int at0 = min(all, rank * per), mine = min(all, at0 + per) - at0;
   mass += p.sink + at0;
   const bool held = per <= p.held;
-  for (int i = tid; i < 3 * kBins; i += kKeepThreads) (&s.hist[0][0])[i] = 0;
+  // the first weights, on their way while the histograms are cleared
+  constexpr int kFirst = 8;
+  float first[kFirst];
+#pragma unroll
+  for (int j = 0; j < kFirst; ++j)
+    first[j] = tid + j * kKeepThreads < mine ? __ldg(mass + tid + j * kKeepThreads) : 0.f;
+#pragma unroll
+  for (int i = tid; i < 3 * kBins / 4; i += kKeepThreads)
+    reinterpret_cast<int4*>(&s.hist[0][0])[i] = make_int4(0, 0, 0, 0);
   __syncthreads();
-#pragma unroll 8
-  for (int i = tid; i < mine; i += kKeepThreads) {
-    const uint32_t k = order_key(__ldg(mass + i));
+  auto take = [&](int i, float x) {
+    const uint32_t k = order_key(x);
     if (held) keys[i] = k;
     atomicAdd(&s.hist[0][k >> 21], 1);
-  }
-  auto key_at = [&](int i) { return held ? keys[i] : order_key(__ldg(mass + i)); };
+  };
+#pragma unroll
+  for (int j = 0; j < kFirst; ++j)
+    if (tid + j * kKeepThreads < mine) take(tid + j * kKeepThreads, first[j]);
+#pragma unroll 8
+  for (int i = tid + kFirst * kKeepThreads; i < mine; i += kKeepThreads) take(i, __ldg(mass + i));
+  // four weights from i on (a multiple of four; those behind the last one are 0)
+  auto keys_at = [&](int i, uint32_t (&k)[4]) {
+    if (held && i + 3 < mine) {
+      const uint4 v = *reinterpret_cast<const uint4*>(keys + i);
+      k[0] = v.x;
+      k[1] = v.y;
+      k[2] = v.z;
+      k[3] = v.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        k[j] = i + j < mine ? (held ? keys[i + j] : order_key(__ldg(mass + i + j))) : 0u;
+    }
+  };
 
   // the m-th heaviest: its digits, and how many of the equal ones are taken
   uint32_t found = 0;
@@ -127,16 +168,33 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const KeepParams p) 
   int shift = 21;
 #pragma unroll 1
   for (int d = 0; d < 3; ++d) {
-    cluster_sync();
-    // bins from the top, two per thread
-    const int bins = d == 2 ? 1024 : 2048, hi = bins - 1 - 2 * tid;
-    int c0 = 0, c1 = 0;
-    if (hi > 0)
+    if (C == 1)
+      __syncthreads();
+    else
+      cluster_sync();
+    // Each CTA adds up a share of the bins over the cluster, the first one the topmost, four bins a
+    // thread; then all know each share's weights, and the one that the border is in finds it.
+    // (Every CTA of eight reading all bins of all took 8000 cycles a digit; with two, that is what they do:
+    // 2500 cycles instead of 4200.)
+    constexpr bool kShared = C > 2;
+    const int bins = d == 2 ? 1024 : 2048, share = kShared ? bins / C : bins;
+    const int low4 = bins - (kShared ? rank * share : 0) - 4 - 4 * tid;
+    int c[4] = {0, 0, 0, 0};
+    if (tid < share / 4) {
+      int4 v[C];
+#pragma unroll
+      for (int r = 0; r < C; ++r)
+        v[r] = C == 1 ? *reinterpret_cast<const int4*>(&s.hist[d][low4]) : ld_cluster4(of_cta(&s.hist[d][low4], r));
+#pragma unroll
       for (int r = 0; r < C; ++r) {
-        c0 += ld_cluster(&s.hist[d][hi], r);
-        c1 += ld_cluster(&s.hist[d][hi - 1], r);
+        c[0] += v[r].w;
+        c[1] += v[r].z;
+        c[2] += v[r].y;
+        c[3] += v[r].x;
       }
-    int incl = c0 + c1;
+    }
+    const int own = (c[0] + c[1]) + (c[2] + c[3]);
+    int incl = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -144,42 +202,69 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const KeepParams p) 
     }
     if (lane == 31) s.sums[warp] = incl;
     __syncthreads();
-    int before = incl - (c0 + c1);
-    for (int w = 0; w < warp; ++w) before += s.sums[w];
-    if (before < left && before + c0 >= left) {
-      s.digit = hi;
-      s.left = left - before;
-      s.exact = before + c0 == left;
-    } else if (before + c0 < left && before + c0 + c1 >= left) {
-      s.digit = hi - 1;
-      s.left = left - before - c0;
-      s.exact = before + c0 + c1 == left;
+    int before = __reduce_add_sync(0xffffffffu, lane < warp ? s.sums[lane] : 0) + incl - own;
+    if (kShared) {
+      if (warp == 0) {
+        const int total = __reduce_add_sync(0xffffffffu, lane < kKeepWarps ? s.sums[lane] : 0);
+        if (lane < C) st_cluster(of_cta(&s.shares[rank], lane), total);
+      }
+      cluster_sync();
+      before += __reduce_add_sync(0xffffffffu, lane < rank ? s.shares[lane & 7] : 0);
     }
-    __syncthreads();
-    found = (found << (d == 2 ? 10 : 11)) | static_cast<uint32_t>(s.digit);
-    left = s.left;
-    exact = s.exact != 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (before < left && before + c[j] >= left) {
+        const int4 f = make_int4(low4 + 3 - j, left - before, before + c[j] == left, 0);
+        if (!kShared)
+          s.found = f;
+        else
+          for (int r = 0; r < C; ++r) st_cluster4(of_cta(&s.found, r), f);
+      }
+      before += c[j];
+    }
+    if (kShared)
+      cluster_sync();
+    else
+      __syncthreads();
+    found = (found << (d == 2 ? 10 : 11)) | static_cast<uint32_t>(s.found.x);
+    left = s.found.y;
+    exact = s.found.z != 0;
     if (d == 2 || exact) break;
     const int next = d == 0 ? 10 : 0;   // the next digit's lowest bit
-#pragma unroll 4
-    for (int i = tid; i < mine; i += kKeepThreads) {
-      const uint32_t k = key_at(i);
-      if (k >> shift == found) atomicAdd(&s.hist[d + 1][(k >> next) & (d == 0 ? 2047u : 1023u)], 1);
+    for (int i = tid * 4; i < (mine + 127) / 128 * 128; i += 4 * kKeepThreads) {
+      uint32_t k[4];
+      keys_at(i, k);   // (a key of 0 is no weight's)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool in = k[j] != 0 && k[j] >> shift == found;
+        const uint32_t lanes = __ballot_sync(0xffffffffu, in);
+        if (lanes == 0) continue;
+        const uint32_t bin = (k[j] >> next) & (d == 0 ? 2047u : 1023u);
+        // equal weights fall into one bin: the lanes with the same one count together
+        const uint32_t first_bin = __shfl_sync(0xffffffffu, bin, __ffs(lanes) - 1);
+        const uint32_t same = __ballot_sync(0xffffffffu, in && bin == first_bin);
+        if (lane == __ffs(lanes) - 1) atomicAdd(&s.hist[d + 1][bin], __popc(same));
+        if (in && bin != first_bin) atomicAdd(&s.hist[d + 1][bin], 1);
+      }
     }
     shift = next;
   }
   const uint32_t low = found << shift;   // exact: the lightest that stays, or what is below it
 
   // counts of each warp's part, then what is in front of it
-  const int part = (per / 32 + kKeepWarps - 1) / kKeepWarps * 32;
+  const int part = ((per + 127) / 128 + kKeepWarps - 1) / kKeepWarps * 128;
   const int w0 = min(mine, warp * part), w1 = min(mine, w0 + part);
-  auto above = [&](uint32_t k) { return exact ? k >= low : k > low; };
-  auto equal = [&](uint32_t k) { return !exact && k == low; };
+  auto above = [&](uint32_t k) { return k != 0 && (exact ? k >= low : k > low); };
+  auto equal = [&](uint32_t k) { return !exact && k == low && k != 0; };
   int na = 0, ne = 0;
-  for (int i = w0 + lane; i < w1; i += 32) {
-    const uint32_t k = key_at(i);
-    na += above(k);
-    ne += equal(k);
+  for (int i = w0 + 4 * lane; i < w1; i += 128) {
+    uint32_t k[4];
+    keys_at(i, k);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      na += above(k[j]);
+      ne += equal(k[j]);
+    }
   }
   na = __reduce_add_sync(0xffffffffu, na);
   ne = __reduce_add_sync(0xffffffffu, ne);
@@ -189,38 +274,54 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const KeepParams p) 
   }
   __syncthreads();
   if (warp == 0) {
-    const int a = __reduce_add_sync(0xffffffffu, s.above[lane]);
-    const int e = __reduce_add_sync(0xffffffffu, s.equal[lane]);
+    const int a = __reduce_add_sync(0xffffffffu, lane < kKeepWarps ? s.above[lane] : 0);
+    const int e = __reduce_add_sync(0xffffffffu, lane < kKeepWarps ? s.equal[lane] : 0);
     if (lane == 0) s.total = make_int2(a, e);
   }
-  cluster_sync();
-  int fa = 0, fe = 0;
-  for (int r = 0; r < rank; ++r) {
-    fa += ld_cluster(&s.total.x, r);
-    fe += ld_cluster(&s.total.y, r);
+  if (C == 1)
+    __syncthreads();
+  else
+    cluster_sync();
+  int fa = lane < warp ? s.above[lane] : 0, fe = lane < warp ? s.equal[lane] : 0;
+  if (C > 1 && lane < rank) {
+    const int2 t = ld_cluster2(of_cta(&s.total, lane));
+    fa += t.x;
+    fe += t.y;
   }
-  for (int w = 0; w < warp; ++w) {
-    fa += s.above[w];
-    fe += s.equal[w];
+  fa = __reduce_add_sync(0xffffffffu, fa);
+  fe = __reduce_add_sync(0xffffffffu, fe);
+  for (int i0 = w0; i0 < w1; i0 += 128) {
+    uint32_t k[4];
+    keys_at(i0 + 4 * lane, k);
+    // four weights a lane: how many of either kind are in front of the lane's, in the two halves of a word
+    int mine4 = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) mine4 += above(k[j]) + (equal(k[j]) << 16);
+    int incl = mine4;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    int a = fa + ((incl - mine4) & 0xffff), e = fe + ((incl - mine4) >> 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool is_above = above(k[j]), is_equal = equal(k[j]);
+      if (is_above || (is_equal && e < left)) keep[p.sink + a + min(e, left)] = p.sink + at0 + i0 + 4 * lane + j;
+      a += is_above;
+      e += is_equal;
+    }
+    const int all4 = __shfl_sync(0xffffffffu, incl, 31);
+    fa += all4 & 0xffff;
+    fe += all4 >> 16;
   }
-  const uint32_t lower = (1u << lane) - 1;
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const bool in = i0 + lane < w1;
-    const uint32_t k = in ? key_at(i0 + lane) : 0u;
-    const uint32_t ma = __ballot_sync(0xffffffffu, in && above(k));
-    const uint32_t me = __ballot_sync(0xffffffffu, in && equal(k));
-    const int ea = fe + __popc(me & lower);   // equal ones in front
-    const bool taken = (ma >> lane & 1u) || ((me >> lane & 1u) && ea < left);
-    if (taken) keep[p.sink + fa + __popc(ma & lower) + min(ea, left)] = p.sink + at0 + i0 + lane;
-    fa += __popc(ma);
-    fe += __popc(me);
-  }
-  cluster_sync();   // no CTA leaves while another may still read its counts
+  if (C > 1) cluster_sync();   // no CTA leaves while another may still read its counts
 }
 
 // ------------------------------------------------------------------ moving
 
-constexpr int kMoveThreads = 256, kMoveRows = 16;   // rows of a block
+constexpr int kMoveThreads = 256, kMoveRows = 32;   // rows of a block
+constexpr int kMoveDepth = 5;                       // 16-byte pieces per thread at a time
 constexpr int kWalkThreads = 512, kWalkDepth = 4;   // 16-byte pieces per thread and step
 
 struct MoveParams {
@@ -288,10 +389,18 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) 
   const uint4* in = reinterpret_cast<const uint4*>(p.cache);
   uint4* out = reinterpret_cast<uint4*>(p.cache);
   const uint32_t upr = p.upr, units = kMoveRows * upr;
-#pragma unroll 4
-  for (uint32_t u = threadIdx.x; u < units; u += kMoveThreads) {
-    const uint32_t r = u / upr, c = u - r * upr;
-    if (src[r] >= 0) out[dst[r] * upr + c] = __ldcs(in + src[r] * upr + c);
+  for (uint32_t u0 = threadIdx.x; u0 < units; u0 += kMoveThreads * kMoveDepth) {
+    uint4 v[kMoveDepth];
+    long long to[kMoveDepth];
+#pragma unroll
+    for (int k = 0; k < kMoveDepth; ++k) {
+      const uint32_t u = u0 + k * kMoveThreads, r = min(u / upr, kMoveRows - 1u), c = u - r * upr;
+      to[k] = u < units && src[r] >= 0 ? dst[r] * upr + c : -1;
+      if (to[k] >= 0) v[k] = __ldcs(in + src[r] * upr + c);
+    }
+#pragma unroll
+    for (int k = 0; k < kMoveDepth; ++k)
+      if (to[k] >= 0) out[to[k]] = v[k];
   }
   if (p.mass && p.new_n > p.budget) {   // the weights' ends, shared out among the blocks
     const int tail = p.new_n - p.budget;
@@ -306,7 +415,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) 
 }
 
 // in place: block (slice, b) walks down the rows of sequence b
-__global__ void __launch_bounds__(kWalkThreads, 2) walk_kernel(const MoveParams p) {
+__global__ void __launch_bounds__(kWalkThreads) walk_kernel(const MoveParams p) {
   const int b = blockIdx.y, per = p.unit_slice;
   const int u = blockIdx.x * per + threadIdx.x % per;
   const int step = kWalkThreads / per, chunk = step * kWalkDepth;
@@ -383,16 +492,12 @@ __global__ void __launch_bounds__(kWalkThreads) walk_mass_kernel(const MoveParam
 
 }  // namespace
 
-int launch_cache_keep(const float* mass, int n, const int32_t* lens, int B, int budget, int sink,
-                      int recent, int32_t* keep, int32_t* count, cudaStream_t stream) {
-  KeepParams p = {mass, lens, keep, count, n, budget, sink, recent, 0, device_error_word()};
-  int C = 8;
-  while (C > 1 && ((n + C - 1) / C < 2048 || static_cast<long long>(B) * C > 304)) C /= 2;
-  const int per = ((n + C - 1) / C + 31) / 32 * 32;
-  p.held = per <= kMostHeld ? per : 0;
-  const size_t smem = static_cast<size_t>(p.held) * 4;
+namespace {
+
+template <int C, int kKeepThreads>
+int launch_keep(const KeepParams& p, int B, cudaStream_t stream) {
   if (static_cast<long long>(B) * C > 0x7fffffffLL) return DSA_ERR_UNSUPPORTED;
-  if (cudaFuncSetAttribute(keep_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(keep_kernel<C, kKeepThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kMostHeld * 4) != cudaSuccess)
     return DSA_ERR_CUDA;
   cudaLaunchAttribute attr = {};
@@ -402,11 +507,32 @@ int launch_cache_keep(const float* mass, int n, const int32_t* lens, int B, int 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(B) * C);
   cfg.blockDim = dim3(kKeepThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.held) * 4;
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, keep_kernel, p) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, keep_kernel<C, kKeepThreads>, p) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_cache_keep(const float* mass, int n, const int32_t* lens, int B, int budget, int sink,
+                      int recent, int32_t* keep, int32_t* count, cudaStream_t stream) {
+  KeepParams p = {mass, lens, keep, count, n, budget, sink, recent, 0, device_error_word()};
+  // A CTA more in a cluster costs about 1.6 us and takes its share of the passes, 1 us per 700 weights:
+  // 2 x 131072 with 2 / 4 / 8 / 16 CTAs 137 / 35 / 26 / 29 us, 16 x 32768 21 / 16 / 21 / 49, 64 x 8192
+  // with 1 / 2 / 4 12.4 / 10.3 / 12.8, 128 x 4096 8.0 / 10.4 / 16.2.
+  int C = 1;
+  while (C < 8 && n / C > 4096 * C && 2ll * C * B <= 304) C *= 2;
+  const int per = ((n + C - 1) / C + 31) / 32 * 32;
+  p.held = per <= kMostHeld ? per : 0;
+  switch (C) {
+    case 8: return launch_keep<8, 1024>(p, B, stream);
+    case 4: return launch_keep<4, 1024>(p, B, stream);
+    case 2: return launch_keep<2, 512>(p, B, stream);
+    // (many long sequences: one CTA each)
+    default: return per > 8192 ? launch_keep<1, 1024>(p, B, stream) : launch_keep<1, 512>(p, B, stream);
+  }
 }
 
 int launch_cache_compact(const CompactArgs& a, cudaStream_t stream) {
