@@ -320,8 +320,11 @@ __global__ void __launch_bounds__(kKeepThreads) keep_kernel(const KeepParams p) 
 
 // ------------------------------------------------------------------ moving
 
-constexpr int kMoveThreads = 256, kMoveRows = 32;   // rows of a block
-constexpr int kMoveDepth = 5;                       // 16-byte pieces per thread at a time
+constexpr int kMoveThreads = 256, kMoveRows = 8;   // rows of a warp
+// 16-byte pieces per lane at a time: three rounds are the 576 of eight bf16 rows. 64 x 2048 e4m3 and 2 x
+// 16384 bf16 rows: 8 rows and 6 pieces 32.8 and 16.1 us, 16 and 6 31.5 and 18.4, 16 and 8 39.0 and 23.8,
+// 8 and 11 41.3 and 24.9.
+constexpr int kMoveDepth = 6;
 constexpr int kWalkThreads = 512, kWalkDepth = 4;   // 16-byte pieces per thread and step
 
 struct MoveParams {
@@ -364,43 +367,48 @@ __device__ __forceinline__ int entry(const MoveParams& p, long long row, int len
   return e;
 }
 
-// to other pages: kMoveRows rows per block
+// To other pages: a warp takes kMoveRows rows. A lane each looks them up (list entry, pages, slots: three
+// waits for memory), then the warp copies their 16-byte pieces one after the other, whatever rows they
+// are of, kMoveDepth a lane at a time. (A block per 32 rows with the slots in shared memory: 34.2 us for
+// 64 x 2048 e4m3 rows.)
 __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) {
-  __shared__ long long src[kMoveRows], dst[kMoveRows];
-  const long long row0 = static_cast<long long>(blockIdx.x) * kMoveRows;
-  if (threadIdx.x < kMoveRows) {
-    const long long row = row0 + threadIdx.x;
-    long long from = -1, to = -1;
-    if (row < p.rows) {
-      const int b = static_cast<int>(row / p.budget), j = static_cast<int>(row - static_cast<long long>(b) * p.budget);
-      const int e = entry(p, row, seq_len(p, b));
-      float w = 0.f;
-      if (e >= 0) {
-        from = slot_of(p, p.page_table + static_cast<long long>(b) * p.max_pages, e);
-        to = slot_of(p, p.new_table + static_cast<long long>(b) * p.new_max_pages, j);
-        if (p.mass && e < p.n) w = __ldg(p.mass + static_cast<long long>(b) * p.n + e);
-      }
-      if (p.mass) p.new_mass[static_cast<long long>(b) * p.new_n + j] = w;
+  const int lane = threadIdx.x & 31;
+  const long long warp = static_cast<long long>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5);
+  const long long row = warp * kMoveRows + lane;
+  int src = -1, dst = -1;   // slots (below 2^31)
+  if (lane < kMoveRows && row < p.rows) {
+    const int b = static_cast<int>(row / p.budget), j = static_cast<int>(row - static_cast<long long>(b) * p.budget);
+    const int e = entry(p, row, seq_len(p, b));
+    float w = 0.f;
+    if (e >= 0) {
+      src = static_cast<int>(slot_of(p, p.page_table + static_cast<long long>(b) * p.max_pages, e));
+      dst = static_cast<int>(slot_of(p, p.new_table + static_cast<long long>(b) * p.new_max_pages, j));
+      if (src < 0) dst = -1;
+      if (dst < 0) src = -1;
+      if (p.mass && e < p.n) w = __ldg(p.mass + static_cast<long long>(b) * p.n + e);
     }
-    src[threadIdx.x] = to < 0 ? -1 : from;
-    dst[threadIdx.x] = to;
+    if (p.mass) p.new_mass[static_cast<long long>(b) * p.new_n + j] = w;
   }
-  __syncthreads();
   const uint4* in = reinterpret_cast<const uint4*>(p.cache);
   uint4* out = reinterpret_cast<uint4*>(p.cache);
   const uint32_t upr = p.upr, units = kMoveRows * upr;
-  for (uint32_t u0 = threadIdx.x; u0 < units; u0 += kMoveThreads * kMoveDepth) {
+  // u / upr: exact for units < 2^20 / upr, which 16 rows of up to 255 pieces are
+  const uint32_t magic = (1u << 20) / upr + 1;
+#pragma unroll 1
+  for (uint32_t u0 = lane; u0 < units + lane; u0 += 32 * kMoveDepth) {   // the same for every lane
     uint4 v[kMoveDepth];
-    long long to[kMoveDepth];
 #pragma unroll
     for (int k = 0; k < kMoveDepth; ++k) {
-      const uint32_t u = u0 + k * kMoveThreads, r = min(u / upr, kMoveRows - 1u), c = u - r * upr;
-      to[k] = u < units && src[r] >= 0 ? dst[r] * upr + c : -1;
-      if (to[k] >= 0) v[k] = __ldcs(in + src[r] * upr + c);
+      const uint32_t u = u0 + 32 * k, r = (u * magic) >> 20, c = u - r * upr;
+      const int s = __shfl_sync(0xffffffffu, src, r);   // (past the last row: a lane without one)
+      if (u < units && s >= 0) v[k] = __ldcs(in + static_cast<long long>(s) * upr + c);
     }
 #pragma unroll
-    for (int k = 0; k < kMoveDepth; ++k)
-      if (to[k] >= 0) out[to[k]] = v[k];
+    for (int k = 0; k < kMoveDepth; ++k) {
+      const uint32_t u = u0 + 32 * k, r = (u * magic) >> 20, c = u - r * upr;
+      const int d = __shfl_sync(0xffffffffu, dst, r);
+      if (u < units && d >= 0) out[static_cast<long long>(d) * upr + c] = v[k];
+    }
   }
   if (p.mass && p.new_n > p.budget) {   // the weights' ends, shared out among the blocks
     const int tail = p.new_n - p.budget;
@@ -565,7 +573,7 @@ int launch_cache_compact(const CompactArgs& a, cudaStream_t stream) {
     p.new_mass = a.new_mass;
   }
   if (a.new_table) {
-    const long long blocks = (p.rows + kMoveRows - 1) / kMoveRows;
+    const long long per = kMoveThreads / 32 * kMoveRows, blocks = (p.rows + per - 1) / per;
     if (blocks > 0x7fffffffLL) return DSA_ERR_UNSUPPORTED;
     move_kernel<<<static_cast<unsigned>(blocks), kMoveThreads, 0, stream>>>(p);
   } else {
