@@ -983,19 +983,10 @@ def latent_attn_shared_workspace_bytes(B, Sq, H, G, Dc, Dr) -> int:
     return int(lib.dsa_latent_attn_shared_workspace_size(B, Sq, H, G, Dc, Dr))
 
 
-def dsa_latent_attn_shared(Q, cache, prefix_table, prefix_lens, starts, page_table, lens, scale: float,
-                           fmt: str = "e4m3", Dc: int = 512, O=None, lse=None, ws=None, stream=None):
-    """dsa_latent_attn for sequences that share long prefixes, each stored once in the cache.
-
-    prefix_table int32 [G, max_prefix_pages] and prefix_lens int32 [G]: the prefix of each group;
-    starts int32 [G + 1]: the sequences starts[g] <= b < starts[g + 1] are group g (those in front of
-    the first start and behind the last have no prefix). Every token sees its group's whole prefix and
-    then its own cached positions; page_table and lens are the sequences' own, without the prefix. The
-    rest as for dsa_latent_attn -> (O bf16 [B,Sq,H,Dc], lse fp32 [B,Sq,H]).
-
-    ws: a device byte buffer of at least latent_attn_shared_workspace_bytes(...) (allocated here if
-    None). What is allocated here is allocated on `stream`.
-    """
+def _shared_args(Q, cache, prefix_table, prefix_lens, starts, page_table, lens, scale, fmt, Dc, O, lse, ws,
+                 stream):
+    """dsa_latent_attn_shared's arguments checked and its outputs and workspace made: (the C arguments,
+    O, lse, ws)."""
     qp = _dev(Q, "Q", torch.bfloat16)
     if Q.dim() != 4 or Q.shape[3] < Dc:
         raise ValueError("Q must be [B, Sq, H, Dc + Dr]")
@@ -1024,10 +1015,28 @@ def dsa_latent_attn_shared(Q, cache, prefix_table, prefix_lens, starts, page_tab
         ws = _empty((need,), torch.uint8, dev, stream)
     if ws is not None and ws.device != dev:
         raise ValueError(f"ws is on {ws.device}, the other arguments on {dev}")
-    _call(lib.dsa_latent_attn_shared, "dsa_latent_attn_shared", dev, stream, qp, cp,
-          _CACHE_FORMATS[fmt], cache.shape[0], cache.shape[1], gp, P, pp, sp, G, tp,
-          page_table.shape[1], lp, B, Sq, H, Dc, Dr, float(scale), op, ep,
-          None if ws is None else _dev(ws, "ws"), 0 if ws is None else ws.numel() * ws.element_size())
+    return (qp, cp, _CACHE_FORMATS[fmt], cache.shape[0], cache.shape[1], gp, P, pp, sp, G, tp,
+            page_table.shape[1], lp, B, Sq, H, Dc, Dr, float(scale), op, ep,
+            None if ws is None else _dev(ws, "ws"),
+            0 if ws is None else ws.numel() * ws.element_size()), O, lse, ws
+
+
+def dsa_latent_attn_shared(Q, cache, prefix_table, prefix_lens, starts, page_table, lens, scale: float,
+                           fmt: str = "e4m3", Dc: int = 512, O=None, lse=None, ws=None, stream=None):
+    """dsa_latent_attn for sequences that share long prefixes, each stored once in the cache.
+
+    prefix_table int32 [G, max_prefix_pages] and prefix_lens int32 [G]: the prefix of each group;
+    starts int32 [G + 1]: the sequences starts[g] <= b < starts[g + 1] are group g (those in front of
+    the first start and behind the last have no prefix). Every token sees its group's whole prefix and
+    then its own cached positions; page_table and lens are the sequences' own, without the prefix. The
+    rest as for dsa_latent_attn -> (O bf16 [B,Sq,H,Dc], lse fp32 [B,Sq,H]).
+
+    ws: a device byte buffer of at least latent_attn_shared_workspace_bytes(...) (allocated here if
+    None). What is allocated here is allocated on `stream`.
+    """
+    args, O, lse, ws = _shared_args(Q, cache, prefix_table, prefix_lens, starts, page_table, lens, scale, fmt,
+                                    Dc, O, lse, ws, stream)
+    _call(lib.dsa_latent_attn_shared, "dsa_latent_attn_shared", Q.device, stream, *args)
     return O, lse
 
 
@@ -1046,51 +1055,13 @@ def _latent_refusal(qp, cp, fmt, num_pages, page_size, tp, max_pages, lp, ip, k,
     return DSA_OK if wp is not None and wp % 16 == 0 and ws_bytes >= need else DSA_ERR_WORKSPACE
 
 
-def dsa_decode_layer(Q, kv, pos, inv_freq, slots, cache, page_table, lens, scale: float,
-                     fmt: str = "e4m3", idx=None, mscale: float = 1.0, layout: str = "interleaved",
-                     Dc: int = 512, ws=None, stream=None):
-    """The attention of one serving step: rotary positions on the positional dims of Q and of the
-    new rows, the rows into the cache, the new tokens' attention over it -> (O, lse).
-
-    Q [B,Sq,H,Dc+Dr] and kv [B,Sq,Dc+Dr] bf16 before their rotation (neither is changed), pos and
-    slots int32 [B,Sq] (the new tokens' positions and cache slots, -1 for padding), inv_freq fp32
-    [Dr/2]; the rest as for dsa_latent_attn, with lens counting the new tokens. A step that is
-    refused leaves the cache as it was.
-    """
-    if not isinstance(kv, torch.Tensor) or kv.dim() != 3:
-        raise ValueError("kv must be [B, Sq, Dc + Dr]")
-    B, Sq, D = kv.shape
-    rows = dsa_rope(kv.view(B, Sq, 1, D), pos, inv_freq, off=Dc, layout=layout, mscale=mscale,
-                    stream=stream)
-    q = dsa_rope(Q, pos, inv_freq, off=Dc, layout=layout, mscale=mscale, stream=stream)
-    args, O, lse, ws = _latent_args(q, cache, page_table, lens, scale, fmt, idx, Dc, None, None, ws,
-                                    stream)
-    rc = _latent_refusal(*args)
-    if rc != DSA_OK:
-        raise DsaError(rc, "dsa_latent_attn")
-    dsa_cache_write(rows.view(B * Sq, D), slots.view(B * Sq), cache, Dc, fmt=fmt, stream=stream)
-    _call(lib.dsa_latent_attn, "dsa_latent_attn", q.device, stream, *args)
-    return O, lse
-
-
 @functools.lru_cache(maxsize=1024)
 def cache_mass_workspace_bytes(B, Sq, H, Dc, Dr, k=0) -> int:
     return int(lib.dsa_cache_mass_workspace_size(B, Sq, H, Dc, Dr, k))
 
 
-def dsa_cache_mass(Q, cache, page_table, lens, lse, scale: float, n: int, fmt: str = "e4m3", idx=None,
-                   prev=None, decay: float = 1.0, Dc: int = 512, mass=None, ws=None, stream=None):
-    """The attention weight that each cached position receives from the Sq newest tokens of its
-    sequence, summed over tokens and heads, on top of decay * prev -> mass fp32 [B, n].
-
-    Q, cache, page_table, lens, scale, fmt, idx as for dsa_latent_attn, and lse fp32 [B,Sq,H] from it
-    (or from dsa_latent_attn_shared; page_table and lens are then the sequences' own). n: positions
-    that mass has room for. prev fp32 [B, n] or None; mass=prev adds in place. Positions at or behind a
-    sequence's length get zero.
-
-    ws: a device byte buffer of at least cache_mass_workspace_bytes(...) (allocated here if
-    None). What is allocated here is allocated on `stream`.
-    """
+def _mass_args(Q, cache, page_table, lens, lse, scale, n, fmt, idx, prev, decay, Dc, mass, ws, stream):
+    """dsa_cache_mass's arguments checked and its output and workspace made: (the C arguments, mass, ws)."""
     qp = _dev(Q, "Q", torch.bfloat16)
     if Q.dim() != 4 or Q.shape[3] < Dc:
         raise ValueError("Q must be [B, Sq, H, Dc + Dr]")
@@ -1123,10 +1094,27 @@ def dsa_cache_mass(Q, cache, page_table, lens, lse, scale: float, n: int, fmt: s
         ws = _empty((need,), torch.uint8, dev, stream)
     if ws is not None and ws.device != dev:
         raise ValueError(f"ws is on {ws.device}, the other arguments on {dev}")
-    _call(lib.dsa_cache_mass, "dsa_cache_mass", dev, stream, qp, cp, _CACHE_FORMATS[fmt],
-          cache.shape[0], cache.shape[1], tp, page_table.shape[1], lp, ip, k, ep, B, Sq, H, Dc, Dr,
-          float(scale), pp, float(decay), mp, n, None if ws is None else _dev(ws, "ws"),
-          0 if ws is None else ws.numel() * ws.element_size())
+    return (qp, cp, _CACHE_FORMATS[fmt], cache.shape[0], cache.shape[1], tp, page_table.shape[1], lp, ip, k, ep,
+            B, Sq, H, Dc, Dr, float(scale), pp, float(decay), mp, n, None if ws is None else _dev(ws, "ws"),
+            0 if ws is None else ws.numel() * ws.element_size()), mass, ws
+
+
+def dsa_cache_mass(Q, cache, page_table, lens, lse, scale: float, n: int, fmt: str = "e4m3", idx=None,
+                   prev=None, decay: float = 1.0, Dc: int = 512, mass=None, ws=None, stream=None):
+    """The attention weight that each cached position receives from the Sq newest tokens of its
+    sequence, summed over tokens and heads, on top of decay * prev -> mass fp32 [B, n].
+
+    Q, cache, page_table, lens, scale, fmt, idx as for dsa_latent_attn, and lse fp32 [B,Sq,H] from it
+    (or from dsa_latent_attn_shared; page_table and lens are then the sequences' own). n: positions
+    that mass has room for. prev fp32 [B, n] or None; mass=prev adds in place. Positions at or behind a
+    sequence's length get zero.
+
+    ws: a device byte buffer of at least cache_mass_workspace_bytes(...) (allocated here if
+    None). What is allocated here is allocated on `stream`.
+    """
+    args, mass, ws = _mass_args(Q, cache, page_table, lens, lse, scale, n, fmt, idx, prev, decay, Dc, mass, ws,
+                                stream)
+    _call(lib.dsa_cache_mass, "dsa_cache_mass", Q.device, stream, *args)
     return mass
 
 
@@ -1199,3 +1187,87 @@ def dsa_cache_compact(cache, page_table, lens, keep, new_table, Dc: int, Dr: int
           cache.shape[0], cache.shape[1], tp, page_table.shape[1], lp, kp, budget, np_, new_pages, B,
           Dc, Dr, mp, n, wp, new_n)
     return new_mass
+
+
+def _shared_refusal(qp, cp, fmt, num_pages, page_size, gp, max_prefix, pp, sp, G, tp, max_pages, lp, B, Sq, H,
+                    Dc, Dr, scale, op, ep, wp, ws_bytes) -> int:
+    """The status with which the library refuses these arguments of dsa_latent_attn_shared, or DSA_OK."""
+    if min(B, Sq, H, G, num_pages, page_size, max_pages, max_prefix) < 1:
+        return DSA_ERR_INVALID_ARG
+    if any(p % 16 for p in (qp, cp, gp, pp, sp, tp, lp, op, ep)):
+        return DSA_ERR_INVALID_ARG
+    need = latent_attn_shared_workspace_bytes(B, Sq, H, G, Dc, Dr)   # 0: sizes that it does not take
+    scale = ctypes.c_float(scale).value
+    if (need == 0 or not 0.0 < scale <= ctypes.c_float(2.0e38).value
+            or max(num_pages, max_pages, max_prefix) * page_size >= 1 << 31):
+        return DSA_ERR_UNSUPPORTED
+    return DSA_OK if wp is not None and wp % 16 == 0 and ws_bytes >= need else DSA_ERR_WORKSPACE
+
+
+def _mass_refusal(qp, cp, fmt, num_pages, page_size, tp, max_pages, lp, ip, k, ep, B, Sq, H, Dc, Dr, scale, pp,
+                  decay, mp, n, wp, ws_bytes) -> int:
+    """The status with which the library refuses these arguments of dsa_cache_mass (prev None or mass
+    itself), or DSA_OK."""
+    if min(B, Sq, H, num_pages, page_size, max_pages, n) < 1:
+        return DSA_ERR_INVALID_ARG
+    if any(p is not None and p % 16 for p in (qp, cp, tp, lp, ip, ep, pp, mp)):
+        return DSA_ERR_INVALID_ARG
+    scale, decay = ctypes.c_float(scale).value, ctypes.c_float(decay).value
+    if (Dc != 512 or Dr != 64 or H > 128 or not 0.0 < scale <= ctypes.c_float(2.0e38).value
+            or not math.isfinite(decay) or max(num_pages, max_pages) * page_size >= 1 << 31
+            or B * Sq >= (1 << 31) // H or n > 1 << 30
+            or (k and (B * Sq >= (1 << 31) // k or B * (n // 8192 + 1) >= 1 << 31))):
+        return DSA_ERR_UNSUPPORTED
+    need = cache_mass_workspace_bytes(B, Sq, H, Dc, Dr, k)
+    return DSA_OK if need == 0 or (wp is not None and wp % 16 == 0 and ws_bytes >= need) else DSA_ERR_WORKSPACE
+
+
+def dsa_decode_layer(Q, kv, pos, inv_freq, slots, cache, page_table, lens, scale: float,
+                     fmt: str = "e4m3", idx=None, mscale: float = 1.0, layout: str = "interleaved",
+                     Dc: int = 512, ws=None, stream=None, *, prefix=None, mass=None, decay: float = 1.0):
+    """The attention of one serving step: rotary positions on the positional dims of Q and of the
+    new rows, the rows into the cache, the new tokens' attention over it -> (O, lse).
+
+    Q [B,Sq,H,Dc+Dr] and kv [B,Sq,Dc+Dr] bf16 before their rotation (neither is changed), pos and
+    slots int32 [B,Sq] (the new tokens' positions and cache slots, -1 for padding), inv_freq fp32
+    [Dr/2]; the rest as for dsa_latent_attn, with lens counting the new tokens. A step that is
+    refused leaves the cache as it was.
+
+    prefix: (prefix_table, prefix_lens, starts) of dsa_latent_attn_shared, for sequences that share cached
+    prefixes (page_table and lens are then their own positions, and ws is that call's workspace).
+    mass: fp32 [B, n], the attention weight of the sequences' own positions: becomes decay times what
+    it was plus the new tokens' (dsa_cache_mass, in place).
+    """
+    if not isinstance(kv, torch.Tensor) or kv.dim() != 3:
+        raise ValueError("kv must be [B, Sq, Dc + Dr]")
+    if prefix is not None and idx is not None:
+        raise ValueError("lists of selected positions and shared prefixes do not go together")
+    B, Sq, D = kv.shape
+    rows = dsa_rope(kv.view(B, Sq, 1, D), pos, inv_freq, off=Dc, layout=layout, mscale=mscale,
+                    stream=stream)
+    q = dsa_rope(Q, pos, inv_freq, off=Dc, layout=layout, mscale=mscale, stream=stream)
+    if prefix is None:
+        attn, name = lib.dsa_latent_attn, "dsa_latent_attn"
+        args, O, lse, ws = _latent_args(q, cache, page_table, lens, scale, fmt, idx, Dc, None, None, ws,
+                                        stream)
+        rc = _latent_refusal(*args)
+    else:
+        attn, name = lib.dsa_latent_attn_shared, "dsa_latent_attn_shared"
+        args, O, lse, ws = _shared_args(q, cache, *prefix, page_table, lens, scale, fmt, Dc, None, None, ws,
+                                        stream)
+        rc = _shared_refusal(*args)
+    if rc != DSA_OK:
+        raise DsaError(rc, name)
+    if mass is not None:
+        if not isinstance(mass, torch.Tensor) or mass.dim() != 2:
+            raise ValueError("mass must be [B, n]")
+        mass_args, _, mass_ws = _mass_args(q, cache, page_table, lens, lse, scale, mass.shape[1], fmt, idx, mass,
+                                           decay, Dc, mass, None, stream)
+        rc = _mass_refusal(*mass_args)
+        if rc != DSA_OK:
+            raise DsaError(rc, "dsa_cache_mass")
+    dsa_cache_write(rows.view(B * Sq, D), slots.view(B * Sq), cache, Dc, fmt=fmt, stream=stream)
+    _call(attn, name, q.device, stream, *args)
+    if mass is not None:
+        _call(lib.dsa_cache_mass, "dsa_cache_mass", q.device, stream, *mass_args)
+    return O, lse

@@ -209,3 +209,48 @@ def test_python_refusals(dsa):
     with pytest.raises(dsa.DsaError):
         dsa.dsa_latent_attn_shared(**good, ws=torch.empty(64, dtype=torch.uint8, device="cuda"))
     no_error(dsa)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("shared", [True, False])
+def test_decode_layer_with_prefix_and_weights(dsa, fmt, shared):
+    """One serving step over shared prefixes that keeps the positions' weights gives what its parts give."""
+    t = Batch(dsa, [0, 2, 4], [90, 200], [37, 2, 0, 160], 2, 16, 16, fmt, 101)
+    inv, m = dsa.rope_frequencies(64, scaling="yarn", factor=8.0)
+    g = gen(102)
+    Q = torch.randn(4, 2, 16, D, generator=g, device="cuda").to(torch.bfloat16)
+    kv = torch.randn(4, 2, D, generator=g, device="cuda").to(torch.bfloat16)
+    n = i32(t.lens)
+    at = (n[:, None] - 2 + torch.arange(2, device="cuda")).clamp(min=0).long()
+    slots = (t.table.long().gather(1, at // 16) * 16 + at % 16).to(torch.int32)
+    slots[2] = -1                                       # the padded sequence
+    pos = at.to(torch.int32)
+    mass = torch.rand(4, 170, generator=g, device="cuda")
+    one, mine = t.cache.clone(), mass.clone()
+    prefix = (t.prefix_table, i32(t.prefixes), i32(t.starts))
+    for _ in range(2):                                  # the second with the same rows again
+        O, lse = dsa.dsa_decode_layer(Q, kv, pos, inv, slots, one, t.table, n, 0.07, fmt=fmt, mscale=m,
+                                      prefix=prefix if shared else None, mass=mine, decay=0.5)
+    rot = dsa.dsa_rope(kv[:, :, None].contiguous(), pos, inv, off=DC, mscale=m)
+    dsa.dsa_cache_write(rot.view(-1, D), slots.view(-1), t.cache, DC, fmt=fmt)
+    q = dsa.dsa_rope(Q, pos, inv, off=DC, mscale=m)
+    if shared:
+        O2, lse2 = dsa.dsa_latent_attn_shared(q, t.cache, *prefix, t.table, n, 0.07, fmt=fmt)
+    else:
+        O2, lse2 = dsa.dsa_latent_attn(q, t.cache, t.table, n, 0.07, fmt=fmt)
+    for _ in range(2):
+        mass = dsa.dsa_cache_mass(q, t.cache, t.table, n, lse2, 0.07, 170, fmt=fmt, prev=mass, decay=0.5)
+    assert torch.equal(one, t.cache) and torch.equal(O, O2) and torch.equal(lse, lse2)
+    assert torch.equal(mine, mass)
+    # refused steps leave the cache and the weights
+    before = one.clone()
+    good = dict(Q=Q, kv=kv, pos=pos, inv_freq=inv, slots=slots, cache=one, page_table=t.table, lens=n, scale=0.07,
+                fmt=fmt, prefix=prefix, mass=mine)
+    many = tuple(torch.zeros(s, dtype=torch.int32, device="cuda") for s in ((65, 1), (65,), (66,)))
+    for bad in (dict(prefix=many), dict(prefix=(prefix[0], prefix[1], prefix[2][:2].clone())), dict(decay=math.inf),
+                dict(mass=mine[0]), dict(mass=mine.double()), dict(idx=torch.zeros(4, 2, 3, dtype=torch.int32, device="cuda")),
+                dict(scale=0.0), dict(ws=torch.empty(64, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises((dsa.DsaError, ValueError, TypeError)):
+            dsa.dsa_decode_layer(**{**good, **bad})
+    assert torch.equal(one, before) and torch.equal(mine, mass)
+    no_error(dsa)
