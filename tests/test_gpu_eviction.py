@@ -518,3 +518,79 @@ def test_captured_step(dsa):
     for a, b in zip((mass, keep, count, new_mass, start), got[2:]):
         assert torch.equal(a, b)
     no_error(dsa)
+
+
+@pytest.mark.parametrize("Sq,H,k", [(1, 16, 0), (2, 80, 0), (1, 128, 1), (3, 20, 70)])
+def test_mass_of_many_short_sequences(dsa, Sq, H, k):
+    """More sequences than clusters, empty ones among them."""
+    lens = [(b * 37) % 300 if b % 5 else 0 for b in range(300)]
+    Q, cache, table, ln, lse, scale, idx, rows = mass_inputs(dsa, lens, Sq, H, 32, "e4m3", 111, k)
+    got = dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, 301, idx=idx)
+    mass_check(got, Q, rows, lens, lse, scale, idx)
+    no_error(dsa)
+
+
+@pytest.mark.parametrize("Sq", [1, 40])
+def test_mass_into_other_widths(dsa, Sq):
+    """Rows of mass at every alignment, and the room behind the sequences cleared in all of them."""
+    lens, H = [260, 1 + Sq, 513], 16
+    Q, cache, table, ln, lse, scale, _, rows = mass_inputs(dsa, lens, Sq, H, 16, "bf16", 121)
+    want = dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, 513, fmt="bf16")
+    mass_check(want, Q, rows, lens, lse, scale)
+    for n in (514, 515, 517, 100003):
+        mass = torch.full((3, n), math.nan, device="cuda")
+        got = dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, n, fmt="bf16", mass=mass)
+        assert torch.equal(got[:, :513], want) and not got[:, 513:].any()
+    no_error(dsa)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_cache_of_more_than_2_to_the_31_bytes(dsa, fmt):
+    """Rows whose offsets do not fit 32 bits: attention over a shared prefix, weights, and rows moved to
+    and fro, against the same rows in a small cache."""
+    row, page = dsa.cache_row_bytes(DC, DR, fmt), 1024
+    pages = (1 << 32) // (row * page) + 8
+    big = torch.zeros(pages, page, row, dtype=torch.uint8, device="cuda")
+    lens, Sq, H = [1500, 900], 1, 16
+    Q, cache, table, ln, lse, scale, _, rows = mass_inputs(dsa, lens, Sq, H, page, fmt, 131)
+    far = table.clone()
+    for b, n in enumerate(lens):
+        for j in range(-(-n // page)):
+            far[b, j] = pages - 1 - (2 * b + j)
+            big[int(far[b, j])] = cache[int(table[b, j])]
+    want = dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, 1500, fmt=fmt)
+    got = dsa.dsa_cache_mass(Q, big, far, ln, lse, scale, 1500, fmt=fmt)
+    assert torch.equal(got, want)
+    starts, plen = i32([0, 2]), i32([1500])
+    a = dsa.dsa_latent_attn_shared(Q, cache, table[:1].clone(), plen, starts, table, ln, scale, fmt=fmt)
+    b = dsa.dsa_latent_attn_shared(Q, big, far[:1].clone(), plen, starts, far, ln, scale, fmt=fmt)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    keep, _ = dsa.dsa_cache_keep(want, ln, 700, recent=5)
+    near = i32([[0], [1]])
+    dsa.dsa_cache_compact(big, far, ln, keep, near, DC, DR, fmt=fmt)
+    dsa.dsa_cache_compact(big, far, ln, keep, None, DC, DR, fmt=fmt)
+    for s in range(2):
+        old = cache[table[s, :-(-lens[s] // page)].long()].view(-1, row)[keep[s].long()]
+        assert torch.equal(big[s, :700], old) and torch.equal(big[int(far[s, 0]), :700], old)
+    no_error(dsa)
+
+
+def test_two_streams_at_once(dsa):
+    """Calls on two streams, each with its own workspace and outputs, do not reach one another."""
+    lens, H = [700, 900], 128
+    sets = [mass_inputs(dsa, lens, Sq, H, 16, "e4m3", 141 + Sq) for Sq in (2, 3)]
+    want = [dsa.dsa_cache_mass(*t[:3], t[3], t[4], t[5], 900) for t in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, t in enumerate(sets):
+            m = dsa.dsa_cache_mass(*t[:3], t[3], t[4], t[5], 900, stream=streams[i])
+            keep, count = dsa.dsa_cache_keep(m, t[3], 300, recent=3, stream=streams[i])
+            got[i].append((m, keep, count))
+    torch.cuda.synchronize()
+    for i in range(2):
+        keep, count = dsa.dsa_cache_keep(want[i], sets[i][3], 300, recent=3)
+        for m, k, c in got[i]:
+            assert torch.equal(m, want[i]) and torch.equal(k, keep) and torch.equal(c, count)
+    no_error(dsa)
