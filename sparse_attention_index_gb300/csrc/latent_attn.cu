@@ -236,7 +236,8 @@ __device__ __forceinline__ int item_chunks(const Params& p, const Tail* tail, in
 // The chunks are cut by weight: going on to another tile costs about as much as kTileCost chunks
 // (its Q, an empty pipeline, an output), so a tile weighs that much in front of its chunks. Cluster
 // c has the chunks at weights [each c, each (c + 1)). Short ranges count no such cost: they would be
-// cut into setups alone.
+// cut into setups alone. With shared prefixes they do: there are as many short tiles as sequences, which
+// would else fall to a few clusters one after the other.
 template <bool SHARED>
 __device__ __forceinline__ void my_chunks(const Params& p, int cluster, Tail* tail) {
   const int items = SHARED ? tail->gtile[p.a.G] + p.items : p.items;
@@ -265,7 +266,7 @@ __device__ __forceinline__ void my_chunks(const Params& p, int cluster, Tail* ta
     }
     before += incl - s;
   }
-  const int cost = (total + p.clusters - 1) / p.clusters >= 4 * kTileCost ? kTileCost : 0;
+  const int cost = SHARED || (total + p.clusters - 1) / p.clusters >= 4 * kTileCost ? kTileCost : 0;
   const long long weight = total + static_cast<long long>(cost) * items;
   const long long each =
       max((weight + p.clusters - 1) / p.clusters, static_cast<long long>(kMinChunks));
