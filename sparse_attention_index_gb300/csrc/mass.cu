@@ -238,7 +238,7 @@ __device__ __forceinline__ uint32_t first_cta(const uint64_t* bar) {
   return r;
 }
 // Arrives at a barrier of the first CTA, without a scope of its own: a release at cluster scope waits
-// for all that the warp has on its way, copies too, and took 88 us instead of XX (32 ragged e4m3
+// for all that the warp has on its way, copies too, and took 88 us instead of 44 (32 ragged e4m3
 // sequences). What has to be in order here is in the writer's own SM, where the tensor cores read it:
 // its shared memory, which fence.proxy.async has made theirs in front of this, or TMEM, read in front of
 // tcgen05.wait::ld. Nothing that another thread reads by plain loads hangs on these barriers.
@@ -893,15 +893,27 @@ __global__ void __launch_bounds__(kAddThreads) add_lists_kernel(const Params p) 
   const int lo = (blockIdx.x - b * slices) * kSlice, size = min(kSlice, a.n - lo);
   const int len = seq_len(a, b, lo == 0 && threadIdx.x == 0);
   const long long at = static_cast<long long>(b) * a.n + lo;
+#pragma unroll 4
   for (int j = threadIdx.x; j < size; j += kAddThreads)
     m[j] = a.prev && lo + j < len ? a.decay * a.prev[at + j] : 0.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // for the weights, nothing else
   __syncthreads();
   for (int i = 0; i < a.Sq; ++i) {
     const long long list = (static_cast<long long>(b) * a.Sq + i) * a.k;
     const int limit = len - a.Sq + i + 1;
-    for (int s = threadIdx.x; s < a.k; s += kAddThreads) {
-      const int j = __ldg(a.idx + list + s);
-      if (j >= lo && j - lo < size && j < limit) atomicAdd(m + (j - lo), __ldcg(p.w + list + s));
+    constexpr int kAtOnce = 4;
+    for (long long s0 = threadIdx.x; s0 < a.k; s0 += kAtOnce * kAddThreads) {
+      int j[kAtOnce];
+      float w[kAtOnce];
+#pragma unroll
+      for (int q = 0; q < kAtOnce; ++q) {
+        const long long s = s0 + q * kAddThreads;
+        j[q] = s < a.k ? __ldg(a.idx + list + s) : -1;
+        w[q] = s < a.k ? __ldcg(p.w + list + s) : 0.f;
+      }
+#pragma unroll
+      for (int q = 0; q < kAtOnce; ++q)
+        if (j[q] >= lo && j[q] - lo < size && j[q] < limit) atomicAdd(m + (j[q] - lo), w[q]);
     }
     __syncthreads();
   }
@@ -990,22 +1002,24 @@ int launch(Params p, cudaStream_t stream) {
   p.w = static_cast<float*>(a.ws);
   mass_kernel<FP8, MULTI><<<2 * clusters, kThreads, smem, stream>>>(p, map);
   if (cudaGetLastError() != cudaSuccess) return DSA_ERR_CUDA;
-  if (a.idx) {
-    const long long blocks = static_cast<long long>(a.B) * ((a.n + kSlice - 1) / kSlice);
-    add_lists_kernel<<<static_cast<unsigned>(blocks), kAddThreads, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
-  }
-  if (!MULTI || clusters == 1) return DSA_OK;   // nothing is split
-  // its blocks may be set up while the last clusters finish; they wait for the parts
+  if (!a.idx && (!MULTI || clusters == 1)) return DSA_OK;   // nothing is split
+  // the second kernel's blocks may be set up while the last clusters finish; they wait for the weights, or
+  // the parts
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(clusters - 1);
-  cfg.blockDim = dim3(kTile);
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  if (a.idx) {
+    const long long blocks = static_cast<long long>(a.B) * ((a.n + kSlice - 1) / kSlice);
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(kAddThreads);
+    return cudaLaunchKernelEx(&cfg, add_lists_kernel, p) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  }
+  cfg.gridDim = dim3(clusters - 1);
+  cfg.blockDim = dim3(kTile);
   return cudaLaunchKernelEx(&cfg, join_kernel, p, clusters) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
