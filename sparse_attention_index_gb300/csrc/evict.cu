@@ -8,11 +8,13 @@
 // cluster through distributed shared memory. Ties at that value go to the lower positions: one pass
 // over the slice counts, an exclusive sum over warps and CTAs places, one more writes. The weights are
 // read from memory once and kept in shared memory as far as it holds them.
-// Bound: latency. 64 sequences of 8192 weights are 2 MB; the passes and their barriers are what it
-// takes.
+// Bound: latency. 64 sequences of up to 8192 weights (1 MB) take 9.4 us, 2 of 131072 20 us: the passes over
+// the slice and the barriers between them.
 //
-// Moving. Rows are copied 16 bytes a thread; memory is the bound. To other pages, all rows at once. In
-// place, row keep[j] goes to position j <= keep[j] and ascending lists never overwrite a row that is
+// Moving. Rows are copied 16 bytes a thread; memory is the bound (64 x 2048 e4m3 rows 33 us, 4.7 TB/s read
+// and written, 2 x 16384 bf16 rows 16.5 us, 4.6 TB/s, of which the first lookups take about 4; copies of
+// whole rows by the bulk engine are level on the former, 31 us, and slower on the latter, 20). To other
+// pages, all rows at once. In place, row keep[j] goes to position j <= keep[j] and ascending lists never overwrite a row that is
 // still to be read, as long as rows go in order: so a CTA takes a column slice of all rows of a
 // sequence and walks down, the slices being independent of one another.
 

@@ -36,6 +36,12 @@
 //               then 16-byte cp.async into 128B-swizzled tiles. e4m3 rows go through a raw ring
 //               two chunks ahead and are widened to bf16, exactly, since their scales are powers
 //               of two.
+// Shared prefixes (dsa_latent_attn_shared): the rows of a group of sequences are tiled together over its
+// prefix, whatever sequences they are of, in front of the sequences' own tiles in the same even ranges.
+// Every tile leaves its (O, m, l) in the workspace, and shared_join_kernel adds those of a row up: 64
+// sequences, 16 heads, a prefix of 32768 bf16 rows: 114 us, and 11 more for own rows of up to 1024 (one
+// sequence with as many rows over the prefix 109); as 64 sequences by themselves they would read and
+// multiply eight times as much.
 // P goes to the tensor cores through shared memory, so that a chunk's S columns are free again
 // once they have been read. TMEM: [Q: 144][S: 2 x 48][pad 16][O: 256] = 512 columns.
 //
