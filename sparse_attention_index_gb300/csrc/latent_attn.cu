@@ -1370,8 +1370,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) shared_join_kernel(const Para
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int* gstart = p.groups;
   const int* gtile = p.groups + kMaxGroups + 1;
-  int g = 0;
-  while (g < G && b >= __ldcg(gstart + g + 1)) ++g;
+  int g = 0;   // groups that end at or in front of b: the starts go up
+#pragma unroll
+  for (int i = 0; i < kMaxGroups; i += 32)
+    g += __popc(__ballot_sync(0xffffffffu, i + lane < G && b >= __ldcg(gstart + i + lane + 1)));
   const int prefix_tiles = __ldcg(gtile + G);
   // parts first[k] + i, i < n[k], at row where[k] of each: k = 0 the prefix's, k = 1 the own keys'
   int first[2] = {0, 0}, n[2] = {0, 0}, where[2] = {0, at};
