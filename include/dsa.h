@@ -698,7 +698,7 @@ int dsa_cache_keep(const float* mass, int n, const int32_t* lens, int B, int bud
  *
  * Supported: Dc and Dr as for the cache, budget <= 2^30, n and new_n <= 2^30, page_size >= 1,
  * num_pages * page_size, max_pages * page_size and new_max_pages * page_size below 2^31; in place,
- * B <= 65535.
+ * B <= 65535; to new pages, B * budget below 2^37.
  */
 int dsa_cache_compact(void* cache, int fmt, int64_t num_pages, int page_size,
                       const int32_t* page_table, int max_pages, const int32_t* lens,

@@ -14,7 +14,7 @@
 // Moving. Rows are copied 16 bytes a thread; memory is the bound (64 x 2048 e4m3 rows 33 us, 4.7 TB/s read
 // and written, 2 x 16384 bf16 rows 16.5 us, 4.6 TB/s, of which the first lookups take about 4; copies of
 // whole rows by the bulk engine are level on the former, 31 us, and slower on the latter, 20). To other
-// pages, all rows at once. In place, row keep[j] goes to position j <= keep[j] and ascending lists never overwrite a row that is
+// pages, all rows at once. In place (61 and 43 us: a chain of loads and a barrier per chunk of rows), row keep[j] goes to position j <= keep[j] and ascending lists never overwrite a row that is
 // still to be read, as long as rows go in order: so a CTA takes a column slice of all rows of a
 // sequence and walks down, the slices being independent of one another.
 
@@ -327,15 +327,17 @@ constexpr int kMoveThreads = 256, kMoveRows = 8;   // rows of a warp
 // 16384 bf16 rows: 8 rows and 6 pieces 32.8 and 16.1 us, 16 and 6 31.5 and 18.4, 16 and 8 39.0 and 23.8,
 // 8 and 11 41.3 and 24.9.
 constexpr int kMoveDepth = 6;
-constexpr int kWalkThreads = 512, kWalkDepth = 4;   // 16-byte pieces per thread and step
+constexpr int kWalkThreads = 512;
+constexpr int kWalkDepth = 4;   // 16-byte pieces per thread and chunk
 
 struct MoveParams {
   uint8_t* cache;
   const int32_t *page_table, *lens, *keep, *new_table;
-  const float* mass;
-  float* new_mass;
+  const float* mass;           // moved with the rows, or nullptr
+  float *new_mass, *tail;      // tail: new_mass where its rows' ends are to be cleared
   long long num_pages, rows;   // rows: B * budget
   int page_size, max_pages, new_max_pages, budget, upr;   // upr: 16-byte units per row
+  int page_shift;              // log2 of the page size, -1 where it is no power of two
   int n, new_n;                // columns of mass and new_mass
   int B, unit_slice;
   int* err;
@@ -348,9 +350,14 @@ __device__ __forceinline__ int seq_len(const MoveParams& p, int b) {
   return max(0, min(len, cap));
 }
 
+// the page that position j is in, of its sequence's
+__device__ __forceinline__ int page_of(const MoveParams& p, int j) {
+  return p.page_shift >= 0 ? j >> p.page_shift : j / p.page_size;
+}
+
 // the slot of position j, -1 where its page is not one of the cache
 __device__ __forceinline__ long long slot_of(const MoveParams& p, const int32_t* table, int j) {
-  const int pg = j / p.page_size;
+  const int pg = page_of(p, j);
   const int page = __ldg(table + pg);
   if (page < 0 || page >= p.num_pages) {
     report_error(p.err, kErrPage);
@@ -367,6 +374,18 @@ __device__ __forceinline__ int entry(const MoveParams& p, long long row, int len
     return -1;
   }
   return e;
+}
+
+// zeros behind the budget in every row of new_mass, shared out among the blocks
+__device__ __forceinline__ void clear_tails(const MoveParams& p, long long block, long long blocks) {
+  if (p.tail == nullptr || p.new_n <= p.budget) return;
+  const int tail = p.new_n - p.budget;
+  const long long count = static_cast<long long>(p.B) * tail, each = (count + blocks - 1) / blocks;
+  const long long end = min(count, (block + 1) * each);
+  for (long long i = block * each + threadIdx.x; i < end; i += blockDim.x) {
+    const long long b = i / tail;
+    p.tail[b * p.new_n + p.budget + (i - b * tail)] = 0.f;
+  }
 }
 
 // To other pages: a warp takes kMoveRows rows. A lane each looks them up (list entry, pages, slots: three
@@ -412,75 +431,104 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) 
       if (u < units && d >= 0) out[static_cast<long long>(d) * upr + c] = v[k];
     }
   }
-  if (p.mass && p.new_n > p.budget) {   // the weights' ends, shared out among the blocks
-    const int tail = p.new_n - p.budget;
-    const long long count = static_cast<long long>(p.B) * tail;
-    const long long each = (count + gridDim.x - 1) / gridDim.x;
-    const long long end = min(count, (blockIdx.x + 1ll) * each);
-    for (long long i = blockIdx.x * each + threadIdx.x; i < end; i += kMoveThreads) {
-      const long long b = i / tail;
-      p.new_mass[b * p.new_n + p.budget + (i - b * tail)] = 0.f;
-    }
-  }
+  clear_tails(p, blockIdx.x, gridDim.x);
 }
 
-// in place: block (slice, b) walks down the rows of sequence b
-__global__ void __launch_bounds__(kWalkThreads) walk_kernel(const MoveParams p) {
+// In place: block (slice, b) walks down the rows of sequence b, chunk after chunk of kWalkDepth rows a
+// thread (of `per` threads). List entries are read three chunks ahead, pages two, pieces one.
+template <int T>
+__global__ void __launch_bounds__(T) walk_kernel(const MoveParams p) {
   const int b = blockIdx.y, per = p.unit_slice;
   const int u = blockIdx.x * per + threadIdx.x % per;
-  const int step = kWalkThreads / per, chunk = step * kWalkDepth;
+  const int step = T / per, chunk = step * kWalkDepth, j0 = threadIdx.x / per;
   const int len = seq_len(p, b);
   const int32_t* table = p.page_table + static_cast<long long>(b) * p.max_pages;
+  const int32_t* list = p.keep + static_cast<long long>(b) * p.budget;
   uint4* data = reinterpret_cast<uint4*>(p.cache);
-  const int end = min(p.budget, len);   // row j comes from a position j or later
+  const int end = u < p.upr ? min(p.budget, len) : 0;   // row j comes from a position j or later
+  // the rows that move: their entries (-1: none), pages, then pieces and where they go (a slot, or -1)
+  int e[kWalkDepth], from[kWalkDepth], to[kWalkDepth], at[kWalkDepth], dst[2][kWalkDepth];
   uint4 v[2][kWalkDepth];
-  long long to[2][kWalkDepth];
-  auto load = [&](int c, uint4 (&x)[kWalkDepth], long long (&dst)[kWalkDepth]) {
+  auto entries = [&](int c) {
 #pragma unroll
     for (int k = 0; k < kWalkDepth; ++k) {
-      const int j = c * chunk + k * step + threadIdx.x / per;
-      dst[k] = -1;
-      if (j >= end || u >= p.upr) continue;
-      const int e = entry(p, static_cast<long long>(b) * p.budget + j, len);
-      if (e < 0 || e == j) continue;
-      if (e < j) {   // not an ascending list
+      const int j = c * chunk + k * step + j0;
+      e[k] = j < end ? __ldg(list + j) : -1;
+    }
+  };
+  auto pages = [&](int c) {
+#pragma unroll
+    for (int k = 0; k < kWalkDepth; ++k) {
+      const int j = c * chunk + k * step + j0;
+      at[k] = -1;
+      if (e[k] == -1 || e[k] == j) continue;
+      if (e[k] < j || e[k] >= len) {   // outside the sequence, or not an ascending list
         report_error(p.err, kErrIdx);
         continue;
       }
-      const long long from = slot_of(p, table, e), at = slot_of(p, table, j);
-      if (from < 0 || at < 0) continue;
-      x[k] = data[from * p.upr + u];
-      dst[k] = at * p.upr + u;
+      at[k] = e[k];
+      from[k] = __ldg(table + page_of(p, e[k]));
+      to[k] = __ldg(table + page_of(p, j));
     }
   };
-  auto store = [&](const uint4 (&x)[kWalkDepth], const long long (&dst)[kWalkDepth]) {
+  auto pieces = [&](int c, uint4 (&x)[kWalkDepth], int (&d)[kWalkDepth]) {
+#pragma unroll
+    for (int k = 0; k < kWalkDepth; ++k) {
+      const int j = c * chunk + k * step + j0;
+      d[k] = -1;
+      if (at[k] < 0) continue;
+      if (from[k] < 0 || from[k] >= p.num_pages || to[k] < 0 || to[k] >= p.num_pages) {
+        report_error(p.err, kErrPage);
+        continue;
+      }
+      const int src = from[k] * p.page_size + at[k] - page_of(p, at[k]) * p.page_size;   // (slots are
+      d[k] = to[k] * p.page_size + j - page_of(p, j) * p.page_size;                      // below 2^31)
+      x[k] = data[static_cast<long long>(src) * p.upr + u];
+    }
+  };
+  auto store = [&](const uint4 (&x)[kWalkDepth], const int (&d)[kWalkDepth]) {
 #pragma unroll
     for (int k = 0; k < kWalkDepth; ++k)
-      if (dst[k] >= 0) data[dst[k]] = x[k];
+      if (d[k] >= 0) data[static_cast<long long>(d[k]) * p.upr + u] = x[k];
   };
   // What chunk c + 1 reads lies behind all that chunks up to c write, so its loads go first; what
   // chunk c reads may be what it writes itself, so a barrier parts the two.
-  const int chunks = (end + chunk - 1) / chunk;
-  load(0, v[0], to[0]);
+  const int chunks = (min(p.budget, len) + chunk - 1) / chunk;   // the same for every thread
+  if (blockIdx.x == 0)   // behind the sequence's end there are no rows to name
+    for (int j = len + threadIdx.x; j < p.budget; j += T)
+      if (__ldg(list + j) != -1) report_error(p.err, kErrIdx);
+  entries(0);
+  pages(0);
+  entries(1);
+  pieces(0, v[0], dst[0]);
+  pages(1);
+  entries(2);
 #pragma unroll 1
   for (int c = 0; c < chunks; c += 2) {
     __syncthreads();
-    load(c + 1, v[1], to[1]);
-    store(v[0], to[0]);
+    pieces(c + 1, v[1], dst[1]);
+    pages(c + 2);
+    entries(c + 3);
+    store(v[0], dst[0]);
     __syncthreads();
-    load(c + 2, v[0], to[0]);
-    store(v[1], to[1]);
+    pieces(c + 2, v[0], dst[0]);
+    pages(c + 3);
+    entries(c + 4);
+    store(v[1], dst[1]);
   }
+  clear_tails(p, static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x,
+              static_cast<long long>(gridDim.x) * gridDim.y);
 }
 
-// The weights of sequence b, walked down the same way (new_mass may be mass), and zeros behind them.
+// The weights of sequence b, walked down the same way (new_mass may be mass). The kernel that moves the
+// rows comes after it and clears what is behind them.
 __global__ void __launch_bounds__(kWalkThreads) walk_mass_kernel(const MoveParams p) {
   const int b = blockIdx.x;
   const int len = seq_len(p, b);
   const float* mass = p.mass + static_cast<long long>(b) * p.n;
   float* out = p.new_mass + static_cast<long long>(b) * p.new_n;
   constexpr int kDepth = 8, kChunk = kWalkThreads * kDepth;
-  for (int j0 = 0; j0 < p.new_n; j0 += kChunk) {
+  for (int j0 = 0; j0 < p.budget; j0 += kChunk) {
     float x[kDepth];
 #pragma unroll
     for (int k = 0; k < kDepth; ++k) {
@@ -495,7 +543,7 @@ __global__ void __launch_bounds__(kWalkThreads) walk_mass_kernel(const MoveParam
 #pragma unroll
     for (int k = 0; k < kDepth; ++k) {
       const int j = j0 + k * kWalkThreads + threadIdx.x;
-      if (j < p.new_n) out[j] = x[k];
+      if (j < p.budget) out[j] = x[k];
     }
   }
 }
@@ -559,10 +607,16 @@ int launch_cache_compact(const CompactArgs& a, cudaStream_t stream) {
   p.new_max_pages = a.new_max_pages;
   p.budget = a.budget;
   p.upr = a.row_bytes / 16;
+  p.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (a.page_size == 1 << i) p.page_shift = i;
   p.n = a.n;
   p.new_n = a.new_n;
   p.B = a.B;
   p.err = device_error_word();
+  p.tail = a.mass ? a.new_mass : nullptr;
+  const long long per = kMoveThreads / 32 * kMoveRows, blocks = (p.rows + per - 1) / per;
+  if (a.new_table && blocks > 0x7fffffffLL) return DSA_ERR_UNSUPPORTED;   // before anything is launched
   const bool walk_mass = a.mass && (!a.new_table || a.new_mass == a.mass);
   if (walk_mass) {
     MoveParams w = p;
@@ -575,15 +629,17 @@ int launch_cache_compact(const CompactArgs& a, cudaStream_t stream) {
     p.new_mass = a.new_mass;
   }
   if (a.new_table) {
-    const long long per = kMoveThreads / 32 * kMoveRows, blocks = (p.rows + per - 1) / per;
-    if (blocks > 0x7fffffffLL) return DSA_ERR_UNSUPPORTED;
     move_kernel<<<static_cast<unsigned>(blocks), kMoveThreads, 0, stream>>>(p);
   } else {
     p.unit_slice = 8;
     while (p.unit_slice > 2 && static_cast<long long>(a.B) * (p.upr / p.unit_slice) < 304)
       p.unit_slice /= 2;
     const dim3 grid((p.upr + p.unit_slice - 1) / p.unit_slice, a.B);
-    walk_kernel<<<grid, kWalkThreads, 0, stream>>>(p);
+    // few blocks: as many threads as a block can have
+    if (static_cast<long long>(grid.x) * a.B <= 152)
+      walk_kernel<1024><<<grid, 1024, 0, stream>>>(p);
+    else
+      walk_kernel<256><<<grid, 256, 0, stream>>>(p);
   }
   return cudaGetLastError() == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }

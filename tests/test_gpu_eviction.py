@@ -219,6 +219,59 @@ def test_compact_bad_entries_and_pages(dsa):
         assert np.array_equal(cache.cpu().numpy().reshape(old.shape), want), place
 
 
+@pytest.mark.parametrize("place", ["new", "same"])
+def test_compact_entries_behind_the_end(dsa, place):
+    """A list that goes on behind a short sequence's end names rows that are not there."""
+    cache, table, new_table, _ = setup_rows(dsa, 2, [5, 700], 600, 16, "e4m3", 5)
+    keep = torch.full((2, 600), -1, dtype=torch.int32, device="cuda")
+    keep[0, :3] = i32([0, 2, 4])
+    keep[1] = torch.arange(50, 650, device="cuda")
+    old = cache.view(-1, cache.shape[-1]).cpu().numpy().copy()
+    t = table.cpu().numpy()
+    to = new_table.cpu().numpy() if place == "new" else t
+    want = old.copy()
+    for b, kept in enumerate((np.array([0, 2, 4]), np.arange(50, 650))):
+        want[slots_of(to[b], 16, np.arange(len(kept)))] = old[slots_of(t[b], 16, kept)]
+    keep[0, 599] = 3
+    dsa.dsa_cache_compact(cache, table, i32([5, 700]), keep, new_table if place == "new" else None, DC, DR)
+    got = cache.view(-1, cache.shape[-1]).cpu().numpy()
+    if place == "new":       # a row that is there, to a place that is there
+        want[slots_of(to[0], 16, np.array([599]))] = old[slots_of(t[0], 16, np.array([3]))]
+        no_error(dsa)
+    else:
+        assert dsa.dsa_get_last_device_error() == dsa.DSA_STAGE_EVICT | dsa.DSA_DEVERR_BAD_INDEX
+    assert np.array_equal(got, want)
+    keep[0, 599] = 5
+    dsa.dsa_cache_compact(cache, table, i32([5, 700]), keep, new_table if place == "new" else None, DC, DR)
+    assert dsa.dsa_get_last_device_error() == dsa.DSA_STAGE_EVICT | dsa.DSA_DEVERR_BAD_INDEX
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("B,n,budget", [(1, 9000, 5000), (3, 4000, 3999), (70, 600, 300), (200, 90, 64)])
+def test_compact_in_place_of_many(dsa, fmt, B, n, budget):
+    """Every block size and slice, lists that move by one row and by many."""
+    lens = [max(1, n - 7 * b) for b in range(B)]
+    cache, table, _, g = setup_rows(dsa, B, lens, budget, 64, fmt, n)
+    keep = torch.full((B, budget), -1, dtype=torch.int32, device="cuda")
+    for b, m in enumerate(lens):
+        c = min(m, budget)
+        if b % 3 == 0:                              # the last ones: every row by the same step
+            keep[b, :c] = torch.arange(m - c, m, device="cuda")
+        else:
+            keep[b, :c] = torch.randperm(m, generator=g, device="cuda")[:c].sort().values.to(torch.int32)
+    old = cache.view(-1, cache.shape[-1]).clone()
+    page = torch.arange(max(n, budget), device="cuda") // 64
+    off = torch.arange(max(n, budget), device="cuda") % 64
+    want = old.clone()
+    for b in range(B):
+        kept = keep[b][keep[b] >= 0].long()
+        slot = lambda j: table[b].long()[page[j]] * 64 + off[j]  # noqa: E731,B023
+        want[slot(torch.arange(len(kept), device="cuda"))] = old[slot(kept)]
+    dsa.dsa_cache_compact(cache, table, i32(lens), keep, None, DC, DR, fmt=fmt)
+    assert torch.equal(cache.view(old.shape), want)
+    no_error(dsa)
+
+
 def test_python_refusals(dsa):
     m, lens = torch.zeros(2, 8, device="cuda"), i32([8, 8])
     with pytest.raises(ValueError):
