@@ -243,7 +243,8 @@ __device__ __forceinline__ int item_chunks(const Params& p, const Tail* tail, in
 // (its Q, an empty pipeline, an output), so a tile weighs that much in front of its chunks. Cluster
 // c has the chunks at weights [each c, each (c + 1)). Short ranges count no such cost: they would be
 // cut into setups alone. With shared prefixes they do: there are as many short tiles as sequences, which
-// would else fall to a few clusters one after the other.
+// would else fall to a few clusters one after the other. (3 / 5 / 8 / 12 chunks: 32 sequences behind 8192
+// keys with 128 heads 141 / 129 / 132 / 136 us, 96 behind 3000 with 32 heads 62 / 64 / 69 / 77.)
 template <bool SHARED>
 __device__ __forceinline__ void my_chunks(const Params& p, int cluster, Tail* tail) {
   const int items = SHARED ? tail->gtile[p.a.G] + p.items : p.items;
