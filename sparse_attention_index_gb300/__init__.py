@@ -1154,7 +1154,8 @@ def dsa_cache_compact(cache, page_table, lens, keep, new_table, Dc: int, Dr: int
     sequence's own pages, which no other sequence may share.
 
     mass fp32 [B, n]: moved too, into new_mass fp32 [B, new_n] with zeros behind the last ([B, budget]
-    where None; new_mass=mass moves it in place). Returns new_mass.
+    where None; new_mass=mass moves it in place, for which the lists have to ascend even to new pages).
+    Returns new_mass.
     """
     kp = _dev(keep, "keep", torch.int32)
     if keep.dim() != 2:

@@ -406,7 +406,12 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) 
       dst = static_cast<int>(slot_of(p, p.new_table + static_cast<long long>(b) * p.new_max_pages, j));
       if (src < 0) dst = -1;
       if (dst < 0) src = -1;
-      if (p.mass && e < p.n) w = __ldg(p.mass + static_cast<long long>(b) * p.n + e);
+      if (p.mass) {
+        if (e < p.n)
+          w = __ldg(p.mass + static_cast<long long>(b) * p.n + e);
+        else
+          report_error(p.err, kErrIdx);   // a row without a weight
+      }
     }
     if (p.mass) p.new_mass[static_cast<long long>(b) * p.new_n + j] = w;
   }
@@ -536,7 +541,10 @@ __global__ void __launch_bounds__(kWalkThreads) walk_mass_kernel(const MoveParam
       x[k] = 0.f;
       if (j < p.budget) {
         const int e = entry(p, static_cast<long long>(b) * p.budget + j, len);
-        if (e >= j && e < p.n) x[k] = mass[e];
+        if (e >= j && e < p.n)
+          x[k] = mass[e];
+        else if (e >= 0)   // overwritten by now, or a row without a weight
+          report_error(p.err, kErrIdx);
       }
     }
     __syncthreads();

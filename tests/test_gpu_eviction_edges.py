@@ -1,0 +1,83 @@
+"""Eviction from the paged latent cache where its arguments are at the edge of the contract: lists that do
+not ascend, and entries that the weights have no room for."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_eviction import DC, DR, setup_rows, slots_of
+from test_gpu_serving import i32, no_error
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dsa():
+    import sparse_attention_index_gb300 as m
+    m.dsa_get_last_device_error()
+    return m
+
+
+def bad_index(dsa):
+    return dsa.dsa_get_last_device_error() == dsa.DSA_STAGE_EVICT | dsa.DSA_DEVERR_BAD_INDEX
+
+
+def moved(cache, table, to, keep, page):
+    """The cache's rows after every entry of keep has moved."""
+    old = cache.cpu().numpy().reshape(-1, cache.shape[-1])
+    want = old.copy()
+    t, to = table.cpu().numpy(), to.cpu().numpy()
+    for b, row in enumerate(keep.cpu().numpy()):
+        for j, e in enumerate(row):
+            if e >= 0:
+                want[slots_of(to[b], page, np.array([j]))] = old[slots_of(t[b], page, np.array([e]))]
+    return want
+
+
+@pytest.mark.parametrize("aliased", [False, True])
+def test_list_that_does_not_ascend_to_new_pages(dsa, aliased):
+    """Every row moves. The weights move in place from higher places to lower ones alone: one that would not
+    is zero there and recorded; into another buffer all of them move."""
+    cache, table, new_table, g = setup_rows(dsa, 2, [60, 60], 6, 16, "e4m3", 11)
+    keep = i32([[7, 0, 9, 30, -1, -1], [2, 3, 5, 8, 13, 21]])
+    want = moved(cache, table, new_table, keep, 16)
+    mass = torch.rand(2, 60, generator=g, device="cuda") + 1
+    want_mass = torch.zeros(2, 60, device="cuda")
+    for b in range(2):
+        for j, e in enumerate(keep[b].tolist()):
+            if e >= (j if aliased else 0):
+                want_mass[b, j] = mass[b, e]
+    out = mass if aliased else torch.full_like(mass, -1.0)
+    dsa.dsa_cache_compact(cache, table, i32([60, 60]), keep, new_table, DC, DR, mass=mass, new_mass=out)
+    if aliased:
+        assert bad_index(dsa)
+    else:
+        no_error(dsa)
+    assert torch.equal(out, want_mass)
+    assert np.array_equal(cache.cpu().numpy().reshape(want.shape), want)
+
+
+@pytest.mark.parametrize("place", ["new", "same"])
+@pytest.mark.parametrize("aliased", [False, True])
+def test_entries_behind_the_weights(dsa, place, aliased):
+    """An entry at or behind n moves its row; it has no weight, which is recorded."""
+    cache, table, new_table, g = setup_rows(dsa, 2, [60, 60], 6, 16, "bf16", 12)
+    keep = i32([[1, 4, 9, 10, 40, 59], [0, 2, 5, 6, 8, 9]])
+    to = new_table if place == "new" else table
+    want = moved(cache, table, to, keep, 16)
+    mass = torch.rand(2, 10, generator=g, device="cuda") + 1
+    want_mass = torch.zeros(2, 10, device="cuda")
+    for b in range(2):
+        for j, e in enumerate(keep[b].tolist()):
+            if e < 10:
+                want_mass[b, j] = mass[b, e]
+    out = mass if aliased else torch.full_like(mass, -1.0)
+    dsa.dsa_cache_compact(cache, table, i32([60, 60]), keep, new_table if place == "new" else None, DC, DR,
+                          fmt="bf16", mass=mass, new_mass=out)
+    assert bad_index(dsa)
+    assert torch.equal(out, want_mass)
+    assert np.array_equal(cache.cpu().numpy().reshape(want.shape), want)
+    # without those entries nothing is recorded
+    keep[0, 3:] = -1
+    dsa.dsa_cache_compact(cache, table, i32([60, 60]), keep, new_table if place == "new" else None, DC, DR,
+                          fmt="bf16", mass=out, new_mass=out)
+    no_error(dsa)
