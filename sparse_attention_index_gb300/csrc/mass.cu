@@ -290,6 +290,19 @@ __device__ __forceinline__ void tmem_ld_8(uint32_t taddr, uint32_t (&r)[8]) {
       : "memory");
 }
 
+// Waits for the last commit. It was issued behind all others, so that by then none of them has an arrival at
+// this CTA's barriers left to make: no CTA may leave its shared memory in front of that. (Not mbar_wait: that
+// gives up as soon as the block does.)
+__device__ __forceinline__ void drain_wait(uint64_t* bar, int* err) {
+  const unsigned long long t0 = globaltimer_ns();
+  while (!mbar_try_wait(smem_u32(bar), 0)) {
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      report_error(err, kErrTime);
+      break;
+    }
+  }
+}
+
 // the slot counter of a ring, and the parity to wait for
 template <int N>
 struct Ring {
@@ -607,13 +620,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         c.next(p);
       }
       umma2_commit(&tail->drain);
-      const unsigned long long t0 = globaltimer_ns();
-      while (!mbar_try_wait(smem_u32(&tail->drain), 0)) {
-        if (globaltimer_ns() - t0 > kWaitLimitNs) {
-          report_error(err, kErrTime);
-          break;
-        }
-      }
+      drain_wait(&tail->drain, err);
     }
   } else if (warp == kQueryWarp) {
     // ================================================================ Q
@@ -642,6 +649,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         c.next(p);
       }
+      // The commits arrive in both CTAs: the second one waits for them here, from its last query on. (In the
+      // epilogue, behind its last products, the same wait took 2% of the time of many pairs.)
+      if (rank == 1) drain_wait(&tail->drain, err);
       if (*abort_flag) {
         // what is on its way lands before the block ends: some time for it, since the barrier's phase
         // may hang on the other CTA

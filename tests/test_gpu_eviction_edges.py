@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_eviction import DC, DR, setup_rows, slots_of
+from test_gpu_eviction import DC, DR, mass_check, mass_inputs, setup_rows, slots_of
 from test_gpu_serving import i32, no_error
 
 pytestmark = pytest.mark.gpu
@@ -80,4 +80,17 @@ def test_entries_behind_the_weights(dsa, place, aliased):
     keep[0, 3:] = -1
     dsa.dsa_cache_compact(cache, table, i32([60, 60]), keep, new_table if place == "new" else None, DC, DR,
                           fmt="bf16", mass=out, new_mass=out)
+    no_error(dsa)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Sq", [1, 9])
+def test_weights_of_calls_that_follow_at_once(dsa, fmt, Sq):
+    """Blocks that end with their last products, one launch behind the other: the same bits every time."""
+    lens = [Sq + b for b in range(20)] + [300, 513]
+    Q, cache, table, ln, lse, scale, _, rows = mass_inputs(dsa, lens, Sq, 16, 16, fmt, 151)
+    want = dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, 520, fmt=fmt)
+    mass_check(want, Q, rows, lens, lse, scale)
+    got = [dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, 520, fmt=fmt) for _ in range(200)]
+    assert all(torch.equal(m, want) for m in got)
     no_error(dsa)
