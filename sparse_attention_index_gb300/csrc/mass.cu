@@ -78,6 +78,20 @@ struct Layout {
   static constexpr uint32_t kTailOff = kRawOff + kRawSlots * kRawAtom;
 };
 
+// Columns of the product for so many pairs: half of them are rows in each CTA. A multiple of 32, which the
+// pair instruction takes at 256 rows without doubt: whether steps of 16 are among its shapes there, the
+// descriptions that are known disagree. (Columns behind the last pair cost nothing that shows: one
+// sequence with 16 heads 8.9 us with 16 and with 32.)
+constexpr int pair_columns(int pairs) { return pairs < kPairs ? (pairs + 31) / 32 * 32 : kPairs; }
+constexpr bool shapes_are_sound() {
+  for (int pairs = 1; pairs <= 2 * kPairs; ++pairs) {
+    const int n = pair_columns(pairs);
+    if (n % 32 != 0 || n < 32 || n > kPairs || (pairs <= kPairs && n < pairs)) return false;
+  }
+  return true;
+}
+static_assert(shapes_are_sound(), "columns of the pair instruction");
+
 struct Tail {
   float nlse[2][kPairs];     // -lse of the pairs
   int lim[2][kPairs];        // positions below it are seen by the pair; a pair that adds nothing: none
@@ -102,7 +116,7 @@ struct Params {
   MassArgs a;
   int items;        // sequences, or tokens with a list each
   int nts;          // columns of 128 pairs
-  int box;          // pairs at a time (a multiple of 16), half of them in each CTA
+  int box;          // columns at a time (pair_columns), half of them in each CTA
   int page_shift;   // log2 of the page size, -1 where it is no power of two
   float* w;         // lists: the weight of each entry [B, Sq, k]
   float* part;      // [2 * clusters][256]
@@ -1002,7 +1016,7 @@ int launch(Params p, cudaStream_t stream) {
   const int pairs = a.idx ? a.H : a.Sq * a.H;
   p.items = a.idx ? a.B * a.Sq : a.B;
   p.nts = (pairs - 1) / kPairs + 1;
-  p.box = pairs < kPairs ? (pairs + 15) / 16 * 16 : kPairs;
+  p.box = pair_columns(pairs);
   CUtensorMap map;
   if (!query_map(&map, a.Q, static_cast<long long>(a.B) * a.Sq * a.H, p.box / 2)) return DSA_ERR_CUDA;
   const size_t smem = Layout<FP8, MULTI>::kTailOff + sizeof(Tail);

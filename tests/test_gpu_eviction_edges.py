@@ -94,3 +94,17 @@ def test_weights_of_calls_that_follow_at_once(dsa, fmt, Sq):
     got = [dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, 520, fmt=fmt) for _ in range(200)]
     assert all(torch.equal(m, want) for m in got)
     no_error(dsa)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Sq,H,k", [
+    (1, 1, 0), (1, 16, 0), (1, 31, 0), (1, 32, 0), (1, 33, 0), (3, 16, 0), (1, 49, 0), (5, 16, 0), (1, 65, 0),
+    (7, 16, 0), (1, 97, 0), (1, 127, 0), (129, 1, 0), (2, 15, 30), (2, 17, 30), (2, 48, 30), (2, 80, 30),
+    (2, 112, 30)])
+def test_weights_of_every_number_of_pairs(dsa, fmt, Sq, H, k):
+    """Numbers of (token, head) pairs on both sides of every width of the products."""
+    lens = [Sq, Sq + 40, 300]
+    Q, cache, table, ln, lse, scale, idx, rows = mass_inputs(dsa, lens, Sq, H, 16, fmt, 161, k)
+    got = dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, 301, fmt=fmt, idx=idx)
+    mass_check(got, Q, rows, lens, lse, scale, idx)
+    no_error(dsa)
