@@ -40,6 +40,7 @@
 // wait is bounded (2 s), after which the kernel reports DSA_STAGE_BWD | TIMEOUT.
 
 #include "dsa_attn_common.cuh"
+#include "tensor_map.h"
 
 namespace dsa {
 namespace {
@@ -912,29 +913,10 @@ __global__ void __launch_bounds__(kThreadsB, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-typedef CUresult (*EncodeTiledFnBd)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFnBd encode_fn_bd() {
-  static EncodeTiledFnBd fn = nullptr;
-  if (fn == nullptr) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    fn = reinterpret_cast<EncodeTiledFnBd>(ptr);
-  }
-  return fn;
-}
-
 // K / V [rows, Hkv, cols] bf16 as (column, K/V head, row): boxes of 64 columns x 1 head
 // x 128 rows, 128-byte swizzle (the shared-memory tile of a [128 x 64] 2-D box)
 bool make_kv_map(CUtensorMap* map, const void* base, long long rows, int Hkv, int cols) {
-  EncodeTiledFnBd fn = encode_fn_bd();
+  const EncodeTiled fn = encode_tiled();
   if (fn == nullptr) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(Hkv),
                         static_cast<cuuint64_t>(rows)};
@@ -949,7 +931,7 @@ bool make_kv_map(CUtensorMap* map, const void* base, long long rows, int Hkv, in
 
 // Q / dO [B*S, H, cols] bf16 as (dim, head, row): boxes of 64 dims x 1 head x 64 rows
 bool make_head_rows_map(CUtensorMap* map, const void* base, long long rows, int H, int cols) {
-  EncodeTiledFnBd fn = encode_fn_bd();
+  const EncodeTiled fn = encode_tiled();
   if (fn == nullptr) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(H),
                         static_cast<cuuint64_t>(rows)};

@@ -28,6 +28,7 @@
 // Items are handed out heaviest (last query tile) first, strided over CTAs.
 
 #include "dsa_attn_common.cuh"
+#include "tensor_map.h"
 
 namespace dsa {
 namespace {
@@ -541,26 +542,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-typedef CUresult (*EncodeTiledFnDense)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                       const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                       const cuuint32_t*, CUtensorMapInterleave,
-                                       CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                       CUtensorMapFloatOOBfill);
-
 // [rows, Hkv, cols] bf16 as (column, K/V head, row): a box of 64 columns x 1 head x 128
 // rows, 128-byte swizzle (the same shared-memory tile as a [128 x 64] 2-D box); rows past
 // the end read as zeros
 bool make_tile_map(CUtensorMap* map, const void* base, long long rows, int Hkv, int cols) {
-  static EncodeTiledFnDense fn = nullptr;
-  if (fn == nullptr) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return false;
-    fn = reinterpret_cast<EncodeTiledFnDense>(ptr);
-  }
+  const EncodeTiled fn = encode_tiled();
+  if (fn == nullptr) return false;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(Hkv),
                         static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2,

@@ -34,6 +34,7 @@
 
 #include "dsa_common.cuh"
 #include "dsa_internal.h"
+#include "tensor_map.h"
 
 namespace dsa {
 namespace {
@@ -600,28 +601,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ----------------------------------------------------------------- host side
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn get_encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (fn == nullptr) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000,
-                                         cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return nullptr;
-    fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  }
-  return fn;
-}
-
 bool make_map(CUtensorMap* map, const void* base, uint64_t rows, int cols, int box_cols,
               int box_rows, CUtensorMapSwizzle swz, bool f8) {
-  EncodeTiledFn fn = get_encode_fn();
+  const EncodeTiled fn = encode_tiled();
   if (fn == nullptr) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * (f8 ? 1 : 2)};

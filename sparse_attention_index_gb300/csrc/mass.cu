@@ -44,6 +44,7 @@
 #include "dsa_common.cuh"
 #include "dsa_internal.h"
 #include "latent_row.cuh"
+#include "tensor_map.h"
 
 namespace dsa {
 namespace {
@@ -952,23 +953,10 @@ __global__ void __launch_bounds__(kAddThreads) add_lists_kernel(const Params p) 
   for (int j = threadIdx.x; j < size; j += kAddThreads) a.mass[at + j] = m[j];
 }
 
-typedef CUresult (*EncodeTiledFnMass)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                      const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                      const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                      CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 // Q [rows, 576] bf16 in boxes of 64 dims x box rows, 128B-swizzled
 bool query_map(CUtensorMap* map, const void* Q, long long rows, int box) {
-  static EncodeTiledFnMass fn = nullptr;
-  if (fn == nullptr) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return false;
-    fn = reinterpret_cast<EncodeTiledFnMass>(ptr);
-  }
+  const EncodeTiled fn = encode_tiled();
+  if (fn == nullptr) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(kD), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(kD) * 2};
   cuuint32_t boxes[2] = {64, static_cast<cuuint32_t>(box)};

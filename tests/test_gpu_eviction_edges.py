@@ -1,5 +1,9 @@
 """Eviction from the paged latent cache where its arguments are at the edge of the contract: lists that do
 not ascend, and entries that the weights have no room for."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -108,3 +112,40 @@ def test_weights_of_every_number_of_pairs(dsa, fmt, Sq, H, k):
     got = dsa.dsa_cache_mass(Q, cache, table, ln, lse, scale, 301, fmt=fmt, idx=idx)
     mass_check(got, Q, rows, lens, lse, scale, idx)
     no_error(dsa)
+
+
+FIRST_CALLS = """
+import threading, torch
+import sparse_attention_index_gb300 as dsa
+B, Sq, H, n = 2, 1, 16, 100
+dev = torch.device("cuda:0")
+g = torch.Generator(device=dev).manual_seed(5)
+Q = torch.randn(B, Sq, H, 576, generator=g, device=dev).to(torch.bfloat16)
+cache = torch.zeros(14, 16, 1152, dtype=torch.uint8, device=dev)
+rows = torch.randn(14 * 16, 576, generator=g, device=dev).to(torch.bfloat16)
+cache.view(-1, 1152).copy_(rows.view(torch.uint8).view(-1, 1152))
+table = torch.arange(14, dtype=torch.int32, device=dev).view(2, 7)
+lens = torch.tensor([100, 60], dtype=torch.int32, device=dev)
+lse = torch.full((B, Sq, H), 3.0, device=dev)
+torch.cuda.synchronize()
+got, gate = [None] * 8, threading.Barrier(8)
+def work(i):
+    s = torch.cuda.Stream()
+    gate.wait()
+    got[i] = dsa.dsa_cache_mass(Q, cache, table, lens, lse, 0.05, n, fmt="bf16", stream=s)
+    s.synchronize()
+threads = [threading.Thread(target=work, args=(i,)) for i in range(8)]
+for t in threads: t.start()
+for t in threads: t.join()
+want = dsa.dsa_cache_mass(Q, cache, table, lens, lse, 0.05, n, fmt="bf16")
+assert all(torch.equal(m, want) for m in got)
+assert bool(want[0].gt(0).all()) and not want[1, 60:].any()
+assert dsa.dsa_get_last_device_error() == 0
+"""
+
+
+def test_first_calls_from_several_threads(dsa):
+    """A process whose first calls come from eight host threads at once."""
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr[-2000:]
