@@ -486,8 +486,9 @@ __global__ void __launch_bounds__(T) walk_kernel(const MoveParams p) {
         report_error(p.err, kErrPage);
         continue;
       }
-      const int src = from[k] * p.page_size + at[k] - page_of(p, at[k]) * p.page_size;   // (slots are
-      d[k] = to[k] * p.page_size + j - page_of(p, j) * p.page_size;                      // below 2^31)
+      // (a slot is below 2^31; a page's first one and the position together may be past it)
+      const int src = from[k] * p.page_size + (at[k] - page_of(p, at[k]) * p.page_size);
+      d[k] = to[k] * p.page_size + (j - page_of(p, j) * p.page_size);
       x[k] = data[static_cast<long long>(src) * p.upr + u];
     }
   };
