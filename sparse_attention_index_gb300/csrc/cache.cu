@@ -249,7 +249,8 @@ int run(CacheParams p, int rows, int fmt, bool write, cudaStream_t stream) {
 }  // namespace
 
 size_t cache_row_bytes(int fmt, int Dc, int Dr) {
-  if (Dc < 128 || Dc > 1024 || Dc % 128 != 0 || Dr < 0 || Dr > 256 || Dr % 8 != 0) return 0;
+  if (Dc < 128 || Dc > kCacheMostDc || Dc % 128 != 0 || Dr < 0 || Dr > kCacheMostDr || Dr % 8 != 0)
+    return 0;
   if (fmt == DSA_CACHE_BF16) return 2 * static_cast<size_t>(Dc + Dr);
   if (fmt != DSA_CACHE_E4M3) return 0;
   return static_cast<size_t>(Dc) + (Dc / 128 * 4 + 15) / 16 * 16 + 2 * static_cast<size_t>(Dr);

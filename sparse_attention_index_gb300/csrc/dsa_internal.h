@@ -156,6 +156,7 @@ bool indexer_dims_supported(int Hi, int Di);
 int launch_rope(const void* x, void* y, int is_f32, const int32_t* pos, const float* inv_freq,
                 int T, int H, int D, int off, int rot, int half, float mscale, int inverse,
                 cudaStream_t stream);
+constexpr int kCacheMostDc = 1024, kCacheMostDr = 256;
 size_t cache_row_bytes(int fmt, int Dc, int Dr);   // 0: not supported
 int launch_cache_write(const void* kv, const int32_t* slots, int T, int Dc, int Dr, int fmt,
                        void* cache, int64_t num_slots, cudaStream_t stream);

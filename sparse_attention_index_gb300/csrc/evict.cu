@@ -418,7 +418,10 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveParams p) 
   const uint4* in = reinterpret_cast<const uint4*>(p.cache);
   uint4* out = reinterpret_cast<uint4*>(p.cache);
   const uint32_t upr = p.upr, units = kMoveRows * upr;
-  // u / upr: exact for units < 2^20 / upr, which 16 rows of up to 255 pieces are
+  // u / upr as (u magic) >> 20: magic is at most one above 2^20 / upr, so the quotient is right as long as
+  // u upr < 2^20
+  constexpr uint32_t kMostPieces = 2 * (kCacheMostDc + kCacheMostDr) / 16;   // of the widest row, in bf16
+  static_assert(kMoveRows * kMostPieces * kMostPieces <= 1u << 20, "the division of a warp's pieces");
   const uint32_t magic = (1u << 20) / upr + 1;
 #pragma unroll 1
   for (uint32_t u0 = lane; u0 < units + lane; u0 += 32 * kMoveDepth) {   // the same for every lane

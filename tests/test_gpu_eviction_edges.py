@@ -149,3 +149,20 @@ def test_first_calls_from_several_threads(dsa):
     r = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True, timeout=300,
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("place", ["new", "same"])
+@pytest.mark.parametrize("fmt,dims", [("bf16", (128, 0)), ("bf16", (1024, 256)), ("bf16", (640, 72)),
+                                      ("e4m3", (128, 0)), ("e4m3", (1024, 256)), ("e4m3", (384, 200))])
+def test_rows_of_every_width(dsa, place, fmt, dims):
+    """The narrowest and the widest rows, and odd numbers of 16-byte pieces."""
+    lens, budget, page = [90, 301, 77], 80, 16
+    cache, table, new_table, g = setup_rows(dsa, 3, lens, budget, page, fmt, sum(dims), dims)
+    keep = torch.full((3, budget), -1, dtype=torch.int32, device="cuda")
+    for b, n in enumerate(lens):
+        at = torch.randperm(n, generator=g, device="cuda")[:budget].sort().values
+        keep[b, :len(at)] = at.to(torch.int32)
+    want = moved(cache, table, new_table if place == "new" else table, keep, page)
+    dsa.dsa_cache_compact(cache, table, i32(lens), keep, new_table if place == "new" else None, *dims, fmt=fmt)
+    assert np.array_equal(cache.cpu().numpy().reshape(want.shape), want)
+    no_error(dsa)
