@@ -602,8 +602,14 @@ int dsa_latent_attn(const void* Q, const void* cache, int fmt, int64_t num_pages
  *
  *   prefix_table int32 [G, max_prefix_pages]   prefix_lens int32 [G]   starts int32 [G + 1]
  *   Q, cache, page_table, lens, O, lse as for dsa_latent_attn
- *   ws    workspace of dsa_latent_attn_shared_workspace_size() bytes (overwritten): fp32 parts, about
- *         2 KB for each of two parts per (token, head). Nothing is kept in it between calls.
+ *   ws    workspace of dsa_latent_attn_shared_workspace_size() bytes (overwritten). Nothing is kept in it
+ *         between calls. It holds fp32 parts of 128 rows, 2056 bytes a row, whether rows are used or not:
+ *             B * Sq * H / 128 + min(G, B)   for the rows of the groups (each group's rounded up),
+ *             B * ceil(Sq * H / 128)         for those of the sequences,
+ *             80                             for tiles that are split over the GPU
+ *         (of B * Sq * H rows rounded up to 32 where those are fewer than 128). With few heads and many
+ *         sequences that is a part of 263 KB a sequence: 40 MB for 64 sequences of 16 heads, 308 MB for
+ *         1024 of 8, 1.1 GB for 4096 of one.
  *
  * Lengths, prefix lengths and pages outside their range are treated and recorded as by
  * dsa_latent_attn; a start below the one in front of it, below 0 or above B is taken as the nearest

@@ -1032,7 +1032,8 @@ def dsa_latent_attn_shared(Q, cache, prefix_table, prefix_lens, starts, page_tab
     rest as for dsa_latent_attn -> (O bf16 [B,Sq,H,Dc], lse fp32 [B,Sq,H]).
 
     ws: a device byte buffer of at least latent_attn_shared_workspace_bytes(...) (allocated here if
-    None). What is allocated here is allocated on `stream`.
+    None): 263 KB or more for every sequence, however few its heads. What is allocated here is allocated
+    on `stream`.
     """
     args, O, lse, ws = _shared_args(Q, cache, prefix_table, prefix_lens, starts, page_table, lens, scale, fmt,
                                     Dc, O, lse, ws, stream)
