@@ -650,10 +650,13 @@ int dsa_latent_attn_shared(const void* Q, const void* cache, int fmt, int64_t nu
  *         weights, or the parts of sums that are split over the GPU
  *
  * A token whose lse is -inf adds nothing (it has no key); a NaN in lse, in Q or in a row reaches the
- * positions that it bears on. A logit counts as an infinity where it is past fp32. Lengths, list entries
+ * positions that it bears on. Q . row_j counts as an infinity where it is past fp32; where it is not, a
+ * token whose lse is +inf (a logit of it is past fp32) adds nothing. Lengths, list entries
  * and pages outside their range are treated as by dsa_latent_attn and recorded with DSA_STAGE_EVICT;
  * positions n and behind are left out, and a length above n is recorded as DSA_DEVERR_BAD_PAGE. The
- * arithmetic is fp32 (products of bf16 exact, sums in a fixed order: the same bits every time).
+ * arithmetic is fp32: products of bf16 exact, sums in a fixed order (the same bits every time). Q . row_j is
+ * added up by the tensor cores in two accumulators, and they cut off what lies behind an addition's last bit
+ * instead of rounding it: with logits of ordinary size a weight is off by about 7e-7 of itself.
  *
  * Supported: as for dsa_latent_attn, with a finite decay, n <= 2^30 and, with lists, B * Sq * k and
  * B * (n / 8192 + 1) below 2^31.
