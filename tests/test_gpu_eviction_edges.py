@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from test_gpu_eviction import DC, DR, mass_check, mass_inputs, setup_rows, slots_of
-from test_gpu_serving import i32, no_error
+from test_gpu_serving import D, attn_check, gen, i32, no_error
 
 pytestmark = pytest.mark.gpu
 
@@ -165,4 +165,77 @@ def test_rows_of_every_width(dsa, place, fmt, dims):
     want = moved(cache, table, new_table if place == "new" else table, keep, page)
     dsa.dsa_cache_compact(cache, table, i32(lens), keep, new_table if place == "new" else None, *dims, fmt=fmt)
     assert np.array_equal(cache.cpu().numpy().reshape(want.shape), want)
+    no_error(dsa)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_serving_goes_on_after_a_cut(dsa, fmt):
+    """The steps that a user makes: one with the weights kept, the cut in place with the indexer's keys along,
+    and the next one, whose positions go on from the old length and whose lengths from the new one."""
+    lens, H, page, budget, n, scale = [300, 40, 777, 129], 16, 16, 100, 800, 192 ** -0.5
+    _, cache, table, _, _, _, _, rows = mass_inputs(dsa, lens, 1, H, page, fmt, 171)
+    g, B = gen(172), len(lens)
+    inv, m = dsa.rope_frequencies(64, scaling="yarn", factor=8.0)
+    Q = torch.randn(B, 1, H, D, generator=g, device="cuda").to(torch.bfloat16)
+    kv = torch.randn(B, 1, D, generator=g, device="cuda").to(torch.bfloat16)
+    keys = torch.randn(B, n, 128, generator=g, device="cuda").to(torch.bfloat16)
+    mass = torch.zeros(B, n, device="cuda")
+
+    def step(pos, at, count):
+        slots = (table.long().gather(1, (at // page).long()[:, None]) * page + (at % page)[:, None]).to(torch.int32)
+        O, lse = dsa.dsa_decode_layer(Q, kv, pos[:, None].contiguous(), inv, slots, cache, table, count, scale,
+                                      fmt=fmt, mscale=m, mass=mass, decay=0.5)
+        new = dsa.dsa_cache_read(cache, slots.view(-1), DC, DR, fmt=fmt).double()
+        return O, lse, new, dsa.dsa_rope(Q, pos[:, None].contiguous(), inv, off=DC, mscale=m)
+
+    # the newest row of each sequence is that of the first step
+    ln = i32(lens)
+    O, lse, new, q = step(ln - 1, ln - 1, ln)
+    have = [torch.cat([rows[b][:lens[b] - 1], new[b:b + 1]]) for b in range(B)]
+    attn_check(O, lse, q, have, lens, scale)
+    mass_check(mass, q, have, lens, lse, scale)
+    keep, count = dsa.dsa_cache_keep(mass, ln, budget, sink=2, recent=10)
+    before, old_keys = mass.clone(), keys.clone()
+    dsa.dsa_cache_compact(cache, table, ln, keep, None, DC, DR, fmt=fmt, mass=mass, new_mass=mass)
+    # the indexer's keys: a cache of one page a sequence, without positional dims
+    dsa.dsa_cache_compact(keys.view(torch.uint8).view(B, n, 256), torch.arange(B, dtype=torch.int32, device="cuda")[:, None].contiguous(),
+                          ln, keep, None, 128, 0, fmt="bf16")
+    kept = [keep[b][keep[b] >= 0].long() for b in range(B)]
+    for b in range(B):
+        assert torch.equal(keys[b, :len(kept[b])], old_keys[b, kept[b]])
+        assert torch.equal(keys[b, len(kept[b]):], old_keys[b, len(kept[b]):])
+        assert torch.equal(mass[b, :len(kept[b])], before[b, kept[b]]) and not mass[b, len(kept[b]):].any()
+    # the next token: its position as if nothing had been cut, its place behind what was kept
+    prev, now = mass.clone(), [len(k) + 1 for k in kept]
+    O, lse, new, q = step(ln, count, count + 1)
+    have = [torch.cat([have[b][kept[b]], new[b:b + 1]]) for b in range(B)]
+    attn_check(O, lse, q, have, now, scale)
+    mass_check(mass, q, have, now, lse, scale, None, prev, 0.5)
+    no_error(dsa)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_decode_layer_with_lists_and_weights(dsa, fmt):
+    """A serving step over selected positions that keeps their weights, in place, gives what its parts give."""
+    lens, Sq, H, k, n = [300, 41], 2, 24, 64, 310
+    Q, cache, table, ln, _, scale, idx, _ = mass_inputs(dsa, lens, Sq, H, 16, fmt, 181, k)
+    g = gen(182)
+    inv, m = dsa.rope_frequencies(64)
+    kv = torch.randn(2, Sq, D, generator=g, device="cuda").to(torch.bfloat16)
+    at = (ln[:, None] - Sq + torch.arange(Sq, device="cuda")).to(torch.int32)
+    slots = (table.long().gather(1, (at // 16).long()) * 16 + at % 16).to(torch.int32)
+    mass = torch.rand(2, n, generator=g, device="cuda")
+    other, prev = cache.clone(), mass.clone()
+    O, lse = dsa.dsa_decode_layer(Q, kv, at, inv, slots, cache, table, ln, scale, fmt=fmt, idx=idx, mscale=m,
+                                  mass=mass, decay=0.75)
+    rot = dsa.dsa_rope(kv[:, :, None].contiguous(), at, inv, off=DC, mscale=m)
+    dsa.dsa_cache_write(rot.view(-1, D), slots.view(-1), other, DC, fmt=fmt)
+    q = dsa.dsa_rope(Q, at, inv, off=DC, mscale=m)
+    O2, lse2 = dsa.dsa_latent_attn(q, other, table, ln, scale, fmt=fmt, idx=idx)
+    want = dsa.dsa_cache_mass(q, other, table, ln, lse2, scale, n, fmt=fmt, idx=idx, prev=prev, decay=0.75)
+    assert torch.equal(O, O2) and torch.equal(lse, lse2) and torch.equal(mass, want) and torch.equal(cache, other)
+    rows = [dsa.dsa_cache_read(other, (table[b].long()[torch.arange(x, device="cuda") // 16] * 16
+                                       + torch.arange(x, device="cuda") % 16).to(torch.int32), DC, DR, fmt=fmt).double()
+            for b, x in enumerate(lens)]
+    mass_check(want, q, rows, lens, lse2, scale, idx, prev, 0.75)
     no_error(dsa)
