@@ -597,7 +597,10 @@ int dsa_latent_attn(const void* Q, const void* cache, int fmt, int64_t num_pages
  *     O[b,i,h] = sum softmax(l) row[0 : Dc],   lse[b,i,h] = log sum exp(l),   l = scale * Q[b,i,h] . row
  *
  * over both. The rows of a group's prefix are read for up to 128 (token, head) pairs of the group at
- * once, whatever sequences they belong to; the two parts are joined in fp32. A token that has no
+ * once, whatever sequences they belong to; the two parts are joined in fp32. With fewer than 128 pairs a
+ * sequence (Sq * H) that saves most of the time over the prefix; from 128 on, dsa_latent_attn with the
+ * prefix's pages in front of each sequence's own (where the prefix ends with a page) is 1 to 9% quicker
+ * over many sequences, and this call over a few. A token that has no
  * position of its own (len < Sq - i: padding) sees no prefix either: O = 0 and lse = -inf.
  *
  *   prefix_table int32 [G, max_prefix_pages]   prefix_lens int32 [G]   starts int32 [G + 1]

@@ -1029,7 +1029,8 @@ def dsa_latent_attn_shared(Q, cache, prefix_table, prefix_lens, starts, page_tab
     starts int32 [G + 1]: the sequences starts[g] <= b < starts[g + 1] are group g (those in front of
     the first start and behind the last have no prefix). Every token sees its group's whole prefix and
     then its own cached positions; page_table and lens are the sequences' own, without the prefix. The
-    rest as for dsa_latent_attn -> (O bf16 [B,Sq,H,Dc], lse fp32 [B,Sq,H]).
+    rest as for dsa_latent_attn -> (O bf16 [B,Sq,H,Dc], lse fp32 [B,Sq,H]). Meant for fewer than 128
+    (token, head) pairs a sequence: from there on dsa_latent_attn over one table is as quick.
 
     ws: a device byte buffer of at least latent_attn_shared_workspace_bytes(...) (allocated here if
     None): 263 KB or more for every sequence, however few its heads. What is allocated here is allocated

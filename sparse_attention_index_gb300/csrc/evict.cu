@@ -8,15 +8,17 @@
 // cluster through distributed shared memory. Ties at that value go to the lower positions: one pass
 // over the slice counts, an exclusive sum over warps and CTAs places, one more writes. The weights are
 // read from memory once and kept in shared memory as far as it holds them.
-// Bound: latency. 64 sequences of up to 8192 weights (1 MB) take 9.4 us, 2 of 131072 20 us: the passes over
+// Bound: latency. 64 sequences of up to 8192 weights (1 MB) take 9 us, 2 of 131072 20 us: the passes over
 // the slice and the barriers between them.
 //
 // Moving. Rows are copied 16 bytes a thread; memory is the bound (64 x 2048 e4m3 rows 33 us, 4.7 TB/s read
-// and written, 2 x 16384 bf16 rows 16.5 us, 4.6 TB/s, of which the first lookups take about 4; copies of
+// and written, 2 x 16384 bf16 rows 16.6 us, 4.6 TB/s, of which the first lookups take about 4; copies of
 // whole rows by the bulk engine are level on the former, 31 us, and slower on the latter, 20). To other
-// pages, all rows at once. In place (61 and 43 us: a chain of loads and a barrier per chunk of rows), row keep[j] goes to position j <= keep[j] and ascending lists never overwrite a row that is
-// still to be read, as long as rows go in order: so a CTA takes a column slice of all rows of a
-// sequence and walks down, the slices being independent of one another.
+// pages, all rows at once. In place (62 and 43 us: a chain of loads and a barrier per chunk of rows), row
+// keep[j] goes to position j <= keep[j] and ascending lists never overwrite a row that is still to be read,
+// as long as rows go in order: so a CTA takes a column slice of all rows of a sequence and walks down, the
+// slices being independent of one another. Weights in place walk the same way, one CTA a sequence in front
+// of the rows (66 and 59 us with them).
 
 #include "dsa_common.cuh"
 #include "dsa_internal.h"
@@ -589,9 +591,11 @@ int launch_keep(const KeepParams& p, int B, cudaStream_t stream) {
 int launch_cache_keep(const float* mass, int n, const int32_t* lens, int B, int budget, int sink,
                       int recent, int32_t* keep, int32_t* count, cudaStream_t stream) {
   KeepParams p = {mass, lens, keep, count, n, budget, sink, recent, 0, device_error_word()};
-  // A CTA more in a cluster costs about 1.6 us and takes its share of the passes, 1 us per 700 weights:
-  // 2 x 131072 with 2 / 4 / 8 / 16 CTAs 137 / 35 / 26 / 29 us, 16 x 32768 21 / 16 / 21 / 49, 64 x 8192
-  // with 1 / 2 / 4 12.4 / 10.3 / 12.8, 128 x 4096 8.0 / 10.4 / 16.2.
+  // More CTAs a cluster share out the passes over the weights and pay for it at the barriers, and dearly as
+  // soon as not all of them are resident at once. With 1 / 2 / 4 / 8 CTAs, us from a graph: 2 x 131072
+  // weights 126 / 101 / 27.5 / 19.5 (up to 49152 a CTA stay in shared memory), 16 x 32768 23 / 18.6 / 13.7 /
+  // 19.0, 64 x 8192 10.9 / 9.5 / 18.7 / 42, 128 x 4096 7.1 / 9.8 / 32 / 74. Between these sizes the rule may
+  // take half of what would be quickest: 4 x 65536 four (19.2; eight 14.3), 32 x 16384 two (13.1; four 11.5).
   int C = 1;
   while (C < 8 && n / C > 4096 * C && 2ll * C * B <= 304) C *= 2;
   const int per = ((n + C - 1) / C + 31) / 32 * 32;

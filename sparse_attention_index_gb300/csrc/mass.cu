@@ -33,11 +33,14 @@
 
 // Measured (device time): 32 sequences of 256 to 8192 rows, 128 heads: bf16 34 us (4.8 TB/s; 6.3 in
 // steady state, the rest is the start of a launch and the last round of tiles), e4m3 33 us (2.9 TB/s); 32
-// tokens over 2 x 16384 bf16 rows 131 us (1180 TFLOP/s). What bounds it: bf16 memory; e4m3 shared memory,
-// through which a tile's bytes go as raw codes, twice, as bf16 and to the tensor cores (about 4000 of 7000
-// cycles a tile at 128 bytes a cycle), and the hand-offs around it; many pairs the products, 36 of
-// 256 x 128 x 16 at 64 cycles of about 4300 a unit, beside which one thread waits and commits, and which
-// take the 128 bytes a cycle of shared memory too.
+// tokens over 2 x 16384 rows, bf16 131 us (1180 TFLOP/s), e4m3 137. What bounds it: bf16 memory; e4m3 no unit
+// but the chain between them: of about 8300 cycles a tile the products take 2304, the rows' way from memory
+// about 3900, what goes through shared memory (raw codes in and out, bf16 in, the products' reads) about 4000
+// at 128 bytes a cycle, and the issuer waits 1800 to 2600 for rows, whose ring of two groups ties the gather
+// to the products (without the copies, the widening, the fence or most of the epilogue the batch takes
+// 31.0, 31.7, 32.7 or 31.6 us); many pairs the products, 36 of 256 x 128 x 16 at 64 cycles of about 4300 a
+// unit, beside which one thread waits and commits and which take the 128 bytes a cycle of shared memory too,
+// and the epilogue, whose steps of eight columns each wait for TMEM (with an eighth of them 118 us).
 
 #include <mutex>
 
@@ -81,8 +84,9 @@ struct Layout {
 
 // Columns of the product for so many pairs: half of them are rows in each CTA. A multiple of 32, which the
 // pair instruction takes at 256 rows without doubt: whether steps of 16 are among its shapes there, the
-// descriptions that are known disagree. (Columns behind the last pair cost nothing that shows: one
-// sequence with 16 heads 8.9 us with 16 and with 32.)
+// descriptions that are known disagree. (What the columns behind the last pair cost: one short sequence
+// with 16 heads nothing; 32 sequences of up to 8192 rows with 16 / 48 / 80 / 112 heads in e4m3 32.6 / 31.9 /
+// 32.7 / 34.1 us, with steps of 16 32.5 / 31.5 / 32.4 / 33.6; in bf16 32.8 / 33.2 / 33.5 / 33.9 either way.)
 constexpr int pair_columns(int pairs) { return pairs < kPairs ? (pairs + 31) / 32 * 32 : kPairs; }
 constexpr bool shapes_are_sound() {
   for (int pairs = 1; pairs <= 2 * kPairs; ++pairs) {
