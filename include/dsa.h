@@ -706,9 +706,9 @@ int dsa_cache_keep(const float* mass, int n, const int32_t* lens, int B, int bud
  * DSA_DEVERR_BAD_INDEX, and so is, in place, one below its own place j. Where the weights alone move in
  * place (new_mass = mass, new pages), an entry below its own place moves its row, its weight becomes 0 and
  * it is recorded the same way; so does, wherever the weights go, an entry at n or behind. A page outside
- * [0, num_pages) moves nothing; it and a length below 0 or above max_pages * page_size (taken as the
- * nearest of the two) are recorded as DSA_STAGE_EVICT | DSA_DEVERR_BAD_PAGE. Every other byte of the
- * cache stays as it was.
+ * [0, num_pages) moves no row (the weight moves all the same); it and a length below 0 or above
+ * max_pages * page_size (taken as the nearest of the two) are recorded as DSA_STAGE_EVICT |
+ * DSA_DEVERR_BAD_PAGE. Every other byte of the cache stays as it was.
  *
  * Supported: Dc and Dr as for the cache, budget <= 2^30, n and new_n <= 2^30, page_size >= 1,
  * num_pages * page_size, max_pages * page_size and new_max_pages * page_size below 2^31; in place,

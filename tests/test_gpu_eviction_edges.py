@@ -239,3 +239,21 @@ def test_decode_layer_with_lists_and_weights(dsa, fmt):
             for b, x in enumerate(lens)]
     mass_check(want, q, rows, lens, lse2, scale, idx, prev, 0.75)
     no_error(dsa)
+
+
+@pytest.mark.parametrize("place", ["new", "same"])
+@pytest.mark.parametrize("aliased", [False, True])
+def test_weight_of_a_row_without_a_page(dsa, place, aliased):
+    """A page that is none of the cache's moves no row; the weights move as they would."""
+    cache, table, new_table, g = setup_rows(dsa, 1, [60], 20, 16, "e4m3", 13)
+    table[0, 2] = cache.shape[0]
+    before = cache.clone().view(-1, cache.shape[-1])
+    keep = i32([[33, 34] + [-1] * 18])
+    mass = torch.rand(1, 60, generator=g, device="cuda") + 1
+    want = torch.zeros(1, 60, device="cuda")
+    want[0, :2] = mass[0, 33:35]
+    out = mass if aliased else torch.full_like(mass, -1.0)
+    dsa.dsa_cache_compact(cache, table, i32([60]), keep, new_table if place == "new" else None, DC, DR, mass=mass,
+                          new_mass=out)
+    assert dsa.dsa_get_last_device_error() == dsa.DSA_STAGE_EVICT | dsa.DSA_DEVERR_BAD_PAGE
+    assert torch.equal(out, want) and torch.equal(cache.view(before.shape), before)
