@@ -31,9 +31,9 @@
 //   warps 12-27  rows, a quarter of a key's atom per thread: cp.async, bf16 into the operand's place, e4m3
 //                into a ring of raw atoms, then widened to bf16, exactly
 
-// Measured (device time): 32 sequences of 256 to 8192 rows, 128 heads: bf16 34 us (4.8 TB/s; 6.3 in
+// Measured (device time): 32 sequences of 256 to 8192 rows, 128 heads: bf16 33 us (4.9 TB/s; 6.3 in
 // steady state, the rest is the start of a launch and the last round of tiles), e4m3 33 us (2.9 TB/s); 32
-// tokens over 2 x 16384 rows, bf16 131 us (1180 TFLOP/s), e4m3 137. What bounds it: bf16 memory; e4m3 no unit
+// tokens over 2 x 16384 rows, bf16 131 us (1180 TFLOP/s), e4m3 135. What bounds it: bf16 memory; e4m3 no unit
 // but the chain between them: of about 8300 cycles a tile the products take 2304, the rows' way from memory
 // about 3900, what goes through shared memory (raw codes in and out, bf16 in, the products' reads) about 4000
 // at 128 bytes a cycle, and the issuer waits 1800 to 2600 for rows, whose ring of two groups ties the gather
@@ -84,9 +84,9 @@ struct Layout {
 
 // Columns of the product for so many pairs: half of them are rows in each CTA. A multiple of 32, which the
 // pair instruction takes at 256 rows without doubt: whether steps of 16 are among its shapes there, the
-// descriptions that are known disagree. (What the columns behind the last pair cost: one short sequence
-// with 16 heads nothing; 32 sequences of up to 8192 rows with 16 / 48 / 80 / 112 heads in e4m3 32.6 / 31.9 /
-// 32.7 / 34.1 us, with steps of 16 32.5 / 31.5 / 32.4 / 33.6; in bf16 32.8 / 33.2 / 33.5 / 33.9 either way.)
+// descriptions that are known disagree. (The columns behind the last pair cost nothing that shows: 32
+// sequences of up to 8192 e4m3 rows with 16 / 48 / 80 / 112 heads 32.1 / 31.6 / 32.4 / 33.5 us, with steps
+// of 16 32.5 / 31.5 / 32.4 / 33.6.)
 constexpr int pair_columns(int pairs) { return pairs < kPairs ? (pairs + 31) / 32 * 32 : kPairs; }
 constexpr bool shapes_are_sound() {
   for (int pairs = 1; pairs <= 2 * kPairs; ++pairs) {
@@ -668,9 +668,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         c.next(p);
       }
-      // The commits arrive in both CTAs: the second one waits for them here, from its last query on. (In the
-      // epilogue, behind its last products, the same wait took 2% of the time of many pairs.)
-      if (rank == 1) drain_wait(&tail->drain, err);
+      // The commits arrive in both CTAs, and the second one waits for them too: from its last query on, or, where
+      // a query may stay for a whole range, from its last row on, so that the wait is of a few units. (In the
+      // epilogue, behind the last products, it took 2% of the time of many pairs.)
+      if (MULTI && rank == 1) drain_wait(&tail->drain, err);
       if (*abort_flag) {
         // what is on its way lands before the block ends: some time for it, since the barrier's phase
         // may hang on the other CTA
@@ -894,6 +895,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       cp_async_wait<0>();
     }
+    if (!MULTI && rank == 1 && t == 0) drain_wait(&tail->drain, err);
+    __syncwarp();
   }
 
   tc_fence_before();
